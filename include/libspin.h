@@ -42,6 +42,7 @@
 #ifndef LIBSPIN_H
 #define LIBSPIN_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -419,6 +420,168 @@ spin_status spin_kv_quant8(const void* X, spin_dtype x_dtype, int T, int H, int 
 spin_status spin_kv_qkv(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq,
                         int Hkv, int D, int bits, float* Q_rot, uint8_t* K_codes, uint16_t* K_scale,
                         float* K_rot, uint8_t* V_codes, uint16_t* V_scale, void* stream);
+
+/*
+ * The paged KV cache, written by spin_kv_append and read by spin_kv_attn and
+ * spin_kv_attn_shared (the abstract's 4-bit KV cache in the form a server
+ * keeps it; the pages fix no storage).  A pool of n_pages pages of page_size
+ * tokens, a power of two from SPIN_KV_MIN_PAGE to SPIN_KV_MAX_PAGE, for Hkv
+ * heads of D = 128 values, bits = 4 or 8 per code, codes and scales as
+ * spin_kv_quant (spin_kv_quant8) defines them:
+ *   K_codes  uint8  [n_pages][Hkv][page_size][16 * bits]
+ *            a token's 128 codes in order (4 bits: even code in the low nibble)
+ *   V_codes  uint8  [n_pages][Hkv][page_size / 4][16][4][bits]
+ *            the bytes of codes 8 o .. 8 o + 7 (o = 0 .. 15) of four
+ *            consecutive tokens beside each other: the second product of
+ *            attention sums over tokens and takes them eight at a time
+ *   K_scale, V_scale  uint16 (fp16 bits) [n_pages][Hkv][page_size]
+ *
+ * A batch of B sequences:
+ *   q_start     [B + 1] int32, not falling: rows q_start[b] .. q_start[b + 1] - 1
+ *               of the T query rows are sequence b's new tokens (none is
+ *               allowed).  Rows before q_start[0] and from q_start[B] on belong
+ *               to no sequence: nothing of them is read or written.
+ *   kv_len      [B] int32: tokens of the sequence in its own pages, the new
+ *               ones among them, so that the i-th new token has place
+ *               kv_len[b] - (q_start[b + 1] - q_start[b]) + i
+ *   page_table  [B][max_pages] int32: its place p lies in slot p % page_size
+ *               of page page_table[b][p / page_size].  Entries past the
+ *               sequence's pages are not used.
+ * These arrays lie on the device; what they hold cannot be checked by the
+ * host, and is checked by the kernels: an entry that is no page of the pool
+ * (-1, say) has no tokens (nothing is stored there, nothing is seen there), a
+ * kv_len above max_pages * page_size counts as that much, below 0 as 0.  With
+ * q_start not rising as it should, the rows concerned get wrong values, and
+ * nothing is read or written outside the arrays.  A page may stand in several
+ * tables (a shared prefix), as long as no two rows of one spin_kv_append call
+ * are stored in the same slot.
+ */
+#define SPIN_KV_MIN_PAGE 16
+#define SPIN_KV_MAX_PAGE 1024
+/* Most tokens of a sequence: max_pages * page_size, prefix_len, rotary positions. */
+#define SPIN_KV_MAX_CONTEXT (1 << 29)
+
+/*
+ * spin_rope_table — cosines and sines of the position rotation, for
+ * spin_kv_append.
+ *
+ *   inv_freq    [n] float64: the turn of pair i per position, 1 <= n <= 64.
+ *               Scaling for long contexts lies in it (frequencies divided by a
+ *               factor, another base, a factor per frequency).
+ *   attn_scale  multiplies every entry (1 for none)
+ *   table       [P][2 n] float32   OUTPUT: row p holds n cosines, then n sines
+ *               of the angles (pos0 + p) * inv_freq[i], times attn_scale
+ * Angles and functions are computed in float64 and rounded once.
+ * Requirements: pos0, P >= 0, pos0 + P <= SPIN_KV_MAX_CONTEXT.
+ */
+spin_status spin_rope_table(const double* inv_freq, int n, int pos0, int P, double attn_scale, float* table,
+                            void* stream);
+
+/*
+ * spin_kv_append — the KV step of an attention layer on the rows qkv_proj
+ * wrote: norms of the heads, position rotation, R3, and the codes of keys and
+ * values into the paged cache, in one launch (page "SpinQuant, Reproduced",
+ * Q5: R3 rotates queries and keys online, after the position rotation, with
+ * which it does not commute; abstract: 4-bit KV cache).
+ *
+ *   Q, K, V   [T] rows of Hq (Hkv) vectors of D = 128 values, float32 or
+ *             float16; q_stride, k_stride, v_stride values from a token to the
+ *             next (of the [T][(Hq + 2 Hkv) 128] product of qkv_proj:
+ *             (Hq + 2 Hkv) 128 for each).  Q and Q_out may both be NULL.
+ *   q_norm, k_norm  [128] float32 or NULL: x <- x / sqrt(mean(x^2) + eps) * w,
+ *             per head
+ *   rope      [rope_len][rot_dim] float32 from spin_rope_table, or NULL with
+ *             rot_dim 0: the first rot_dim values of a head are turned in pairs
+ *             (i, i + rot_dim / 2) (interleaved 0) or (2 i, 2 i + 1)
+ *             (interleaved 1) by the row of the token's position, pos0 + place;
+ *             rot_dim a multiple of 16 up to 128.  pos0 is 0, or the length of a
+ *             prefix that lies in other pages (spin_kv_attn_shared).
+ *   K_codes, K_scale, V_codes, V_scale, bits   the cache   UPDATED: codes of
+ *             the keys, y = x . H_128 / sqrt(128) after norm and rotation, and
+ *             of the values as they are, by the rules of spin_kv_quant at 4 and
+ *             spin_kv_quant8 at 8 bits.  y is computed in float64 and rounded
+ *             once to float32, which is what is quantized.
+ *   Q_out     [T][Hq][128] fp16   OUTPUT: the queries, the same way, rounded
+ *             (float32 sums)
+ * A token whose place is negative, beyond its table, or whose position has no
+ * row in rope, is not stored, and its queries are zeros; one whose page is not
+ * in the pool is not stored.
+ * Requirements: T, B >= 0, strides >= the heads' values, multiples of 16 bytes
+ * and at most 2^40, pages as above, at most 2^24 - 1 workgroups of 16 vectors.
+ * Errors: SPIN_ERR_NULL (a Q / Q_out pair with one NULL, rope without rot_dim),
+ * SPIN_ERR_UNSUPPORTED (dtype, bits, interleaved, an eps that is negative or
+ * not finite), SPIN_ERR_BAD_SHAPE, SPIN_ERR_MISALIGNED (every pointer 16 bytes).
+ */
+spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq, int Hkv,
+                           int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_norm,
+                           const float* k_norm, float eps, const float* rope, int rope_len, int rot_dim,
+                           int interleaved, int pos0, int bits, uint8_t* K_codes, uint16_t* K_scale,
+                           uint8_t* V_codes, uint16_t* V_scale, int n_pages, int page_size, int B,
+                           const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                           uint16_t* Q_out, void* stream);
+
+/*
+ * spin_kv_attn — attention of the new tokens of every sequence over its pages
+ * (page "SpinQuant, Reproduced", Q5: queries and keys both carry R3, which
+ * leaves their products unchanged; the values' R2 is undone in o_proj).
+ * Prompts, chunks and single tokens may stand in one batch.
+ *
+ *   Q    [T][Hq][D] fp16 (from spin_kv_append), Hq a multiple of Hkv: query
+ *        head h reads key head h / (Hq / Hkv)
+ *   O    [T][Hq][D] fp16   OUTPUT: sum_j softmax_j(z) v_j over the visible
+ *        tokens j, zeros where none is; k_j and v_j are code * scale
+ *        z_j = scale * (q . k_j)
+ *        z_j <- softcap * tanh(z_j / softcap)   where softcap > 0
+ *        z_j <- z_j - slopes[h] * |p - j|       slopes [Hq] float32 or NULL
+ *        for a query at position p, visible if j < kv_len[b], and
+ *          causal 1: j <= p, or j < bidir_len[b] (bidir_len [B] int32 or NULL:
+ *                    a prefix that every row sees whole); causal 0: any
+ *          window > 0: |p - j| < window
+ *   workspace  device memory of the bytes spin_kv_attn_workspace names (it may
+ *        be NULL if that is 0); its content before and after means nothing,
+ *        and calls that overlap need one each
+ * Scores, maxima and sums are float32; softmax weights are rounded to fp16
+ * (relative to the row's largest weighted term) for the product with the codes,
+ * which are exact.  A row that sees a token whose scale is not finite is NaN;
+ * one that does not is not touched by it.
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (bits, causal, a scale that is
+ * not finite, a softcap that is negative or not finite), SPIN_ERR_BAD_SHAPE
+ * (also a workspace that is too small, and more than 2^24 - 1 workgroups),
+ * SPIN_ERR_MISALIGNED (every pointer 16 bytes).
+ */
+spin_status spin_kv_attn(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                         const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale, int n_pages,
+                         int page_size, int B, const int32_t* q_start, const int32_t* kv_len,
+                         const int32_t* page_table, int max_pages, float scale, float softcap, const float* slopes,
+                         int window, int causal, const int32_t* bidir_len, uint16_t* O, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * spin_kv_attn_shared — spin_kv_attn for sequences that all begin with the
+ * same prefix_len tokens, whose pages prefix_table ([ceil(prefix_len /
+ * page_size)] int32) names once.  Each sequence's own pages hold what follows:
+ * places 0, 1, ... of its table are positions prefix_len, prefix_len + 1, ...
+ * kv_len and the table count own tokens only; positions, window, bias and
+ * bidir_len count from the prefix's first token.  The prefix is read once for
+ * the rows of all sequences together.  The result is that of spin_kv_attn with
+ * the prefix's pages in front of every table, up to rounding.
+ * prefix_len 0 is spin_kv_attn.  Errors as there.
+ */
+spin_status spin_kv_attn_shared(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                                const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale,
+                                int n_pages, int page_size, const int32_t* prefix_table, int prefix_len, int B,
+                                const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                int max_pages, float scale, float softcap, const float* slopes, int window,
+                                int causal, const int32_t* bidir_len, uint16_t* O, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * spin_kv_attn_workspace — bytes of workspace a spin_kv_attn (prefix_len 0) or
+ * spin_kv_attn_shared call of these sizes takes.  It goes by the sizes alone,
+ * not by what the arrays on the device hold.
+ */
+spin_status spin_kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, int prefix_len,
+                                   size_t* bytes);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* spin_status_string(spin_status s);

@@ -7,6 +7,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "spin_internal.h"
 
@@ -110,6 +111,80 @@ int spin::device_cu_count() {
     g_cu_count[dev].store(cus, std::memory_order_relaxed);
     return cus;
 }
+
+namespace {
+
+// What spin_kv_append and the attention calls ask of the paged cache and its batch.
+spin_status paged_ok(int D, int bits, int Hkv, int n_pages, int page_size, int B, int max_pages) {
+    if (bits != 4 && bits != 8) return SPIN_ERR_UNSUPPORTED;
+    if (D != 128 || Hkv < 1 || n_pages < 1 || B < 0 || max_pages < 1) return SPIN_ERR_BAD_SHAPE;
+    if (page_size < SPIN_KV_MIN_PAGE || page_size > SPIN_KV_MAX_PAGE || (page_size & (page_size - 1)) != 0)
+        return SPIN_ERR_BAD_SHAPE;
+    if (static_cast<long long>(max_pages) * page_size > SPIN_KV_MAX_CONTEXT) return SPIN_ERR_BAD_SHAPE;
+    return SPIN_OK;
+}
+
+bool aligned_all(std::initializer_list<const void*> ps) {   // NULL counts as aligned
+    for (const void* p : ps)
+        if (!aligned16(p)) return false;
+    return true;
+}
+
+spin_status kv_attn_impl(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                         const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale, int n_pages,
+                         int page_size, int B, const int32_t* q_start, const int32_t* kv_len,
+                         const int32_t* page_table, int max_pages, const int32_t* prefix_table, int prefix_len,
+                         float scale, float softcap, const float* slopes, int window, int causal,
+                         const int32_t* bidir_len, uint16_t* O, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    if (!Q || !K_codes || !K_scale || !V_codes || !V_scale || !q_start || !kv_len || !page_table || !O)
+        return SPIN_ERR_NULL;
+    if (prefix_len > 0 && !prefix_table) return SPIN_ERR_NULL;
+    if (causal != 0 && causal != 1) return SPIN_ERR_UNSUPPORTED;
+    if (!(scale > -__builtin_inff() && scale < __builtin_inff()) || !(softcap >= 0.0f && softcap < __builtin_inff()))
+        return SPIN_ERR_UNSUPPORTED;
+    const spin_status ok = paged_ok(D, bits, Hkv, n_pages, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (T < 0 || Hq < 1 || Hq % Hkv != 0 || window < 0 || prefix_len < 0 || prefix_len > SPIN_KV_MAX_CONTEXT)
+        return SPIN_ERR_BAD_SHAPE;
+    if (T > 0 && B > 0 && !spin::kv_attn_fits(T, Hq, Hkv, B, max_pages * page_size, prefix_len)) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({Q, K_codes, K_scale, V_codes, V_scale, q_start, kv_len, page_table, prefix_table, slopes, bidir_len, O,
+                      workspace}))
+        return SPIN_ERR_MISALIGNED;
+    if (T == 0 || B == 0) return SPIN_OK;
+    const size_t need = spin::kv_attn_workspace(T, Hq, Hkv, B, max_pages * page_size, prefix_len);
+    if (need > 0 && !workspace) return SPIN_ERR_NULL;
+    if (workspace_bytes < need) return SPIN_ERR_BAD_SHAPE;
+    spin::KvAttnArgs a = {};
+    a.Q = Q;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.K_codes = K_codes;
+    a.K_scale = K_scale;
+    a.V_codes = V_codes;
+    a.V_scale = V_scale;
+    a.n_pages = n_pages;
+    a.page_log2 = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.B = B;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.prefix_table = prefix_table;
+    a.prefix_len = prefix_len;
+    a.scale = scale;
+    a.softcap = softcap;
+    a.slopes = slopes;
+    a.window = window;
+    a.causal = causal == 1;
+    a.bidir_len = bidir_len;
+    a.O = O;
+    a.partial = static_cast<float*>(workspace);
+    return from_hip(spin::launch_kv_attn(a, bits, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -304,6 +379,112 @@ spin_status spin_fold_rotation(const float* W, int K, int N, const float* R, int
     if (N == 0) return SPIN_OK;
     return from_hip(spin::launch_fold_rotation(W, K, N, R, r_block, h, W_rot, Wq, w_scale,
                                                static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_rope_table(const double* inv_freq, int n, int pos0, int P, double attn_scale, float* table,
+                            void* stream) {
+    if (!inv_freq || !table) return SPIN_ERR_NULL;
+    if (n < 1 || n > 64 || pos0 < 0 || P < 0 || static_cast<long long>(pos0) + P > SPIN_KV_MAX_CONTEXT) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned16(inv_freq) || !aligned16(table)) return SPIN_ERR_MISALIGNED;
+    if (P == 0) return SPIN_OK;
+    return from_hip(spin::launch_rope_table(inv_freq, n, pos0, P, attn_scale, table, static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq, int Hkv,
+                           int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_norm,
+                           const float* k_norm, float eps, const float* rope, int rope_len, int rot_dim,
+                           int interleaved, int pos0, int bits, uint8_t* K_codes, uint16_t* K_scale,
+                           uint8_t* V_codes, uint16_t* V_scale, int n_pages, int page_size, int B,
+                           const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                           uint16_t* Q_out, void* stream) {
+    if (!K || !V || !K_codes || !K_scale || !V_codes || !V_scale || !q_start || !kv_len || !page_table)
+        return SPIN_ERR_NULL;
+    if ((Q == nullptr) != (Q_out == nullptr) || (rope == nullptr) != (rot_dim == 0)) return SPIN_ERR_NULL;
+    if (x_dtype != SPIN_F32 && x_dtype != SPIN_F16) return SPIN_ERR_UNSUPPORTED;
+    if (interleaved != 0 && interleaved != 1) return SPIN_ERR_UNSUPPORTED;
+    if ((q_norm || k_norm) && !(eps >= 0.0f && eps < __builtin_inff())) return SPIN_ERR_UNSUPPORTED;
+    const spin_status ok = paged_ok(D, bits, Hkv, n_pages, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (T < 0 || (Q && Hq < 1) || rot_dim < 0 || rot_dim > 128 || rot_dim % 16 != 0 || pos0 < 0 ||
+        pos0 > SPIN_KV_MAX_CONTEXT || (rope && rope_len < 1))
+        return SPIN_ERR_BAD_SHAPE;
+    const int64_t per16 = x_dtype == SPIN_F16 ? 8 : 4;   // values in 16 bytes
+    const int64_t far = int64_t{1} << 40;
+    for (const int64_t s : {Q ? q_stride : k_stride, k_stride, v_stride})
+        if (s < 128 || s > far || s % per16 != 0) return SPIN_ERR_BAD_SHAPE;
+    if (k_stride < int64_t{128} * Hkv || v_stride < int64_t{128} * Hkv || (Q && q_stride < int64_t{128} * Hq))
+        return SPIN_ERR_BAD_SHAPE;
+    if (spin::kv_append_blocks(T, Q ? Hq : 0, Hkv) > (1LL << 24) - 1) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({Q, K, V, q_norm, k_norm, rope, K_codes, K_scale, V_codes, V_scale, q_start, kv_len, page_table, Q_out}))
+        return SPIN_ERR_MISALIGNED;
+    if (T == 0 || B == 0) return SPIN_OK;
+    spin::KvAppendArgs a = {};
+    a.Q = Q;
+    a.K = K;
+    a.V = V;
+    a.T = T;
+    a.Hq = Q ? Hq : 0;
+    a.Hkv = Hkv;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    a.rope = rope;
+    a.rope_len = rope_len;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved == 1;
+    a.pos0 = pos0;
+    a.B = B;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.page_log2 = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.K_codes = K_codes;
+    a.K_scale = K_scale;
+    a.V_codes = V_codes;
+    a.V_scale = V_scale;
+    a.Q_out = Q_out;
+    return from_hip(spin::launch_kv_append(a, x_dtype == SPIN_F16, bits, static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, int prefix_len,
+                                   size_t* bytes) {
+    if (!bytes) return SPIN_ERR_NULL;
+    const spin_status ok = paged_ok(128, 4, Hkv, 1, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (T < 0 || Hq < 1 || Hq % Hkv != 0 || prefix_len < 0 || prefix_len > SPIN_KV_MAX_CONTEXT) return SPIN_ERR_BAD_SHAPE;
+    *bytes = 0;
+    if (T == 0 || B == 0) return SPIN_OK;
+    if (!spin::kv_attn_fits(T, Hq, Hkv, B, max_pages * page_size, prefix_len)) return SPIN_ERR_BAD_SHAPE;
+    *bytes = spin::kv_attn_workspace(T, Hq, Hkv, B, max_pages * page_size, prefix_len);
+    return SPIN_OK;
+}
+
+spin_status spin_kv_attn(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                         const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale, int n_pages,
+                         int page_size, int B, const int32_t* q_start, const int32_t* kv_len,
+                         const int32_t* page_table, int max_pages, float scale, float softcap, const float* slopes,
+                         int window, int causal, const int32_t* bidir_len, uint16_t* O, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return kv_attn_impl(Q, T, Hq, Hkv, D, bits, K_codes, K_scale, V_codes, V_scale, n_pages, page_size, B, q_start,
+                        kv_len, page_table, max_pages, nullptr, 0, scale, softcap, slopes, window, causal, bidir_len,
+                        O, workspace, workspace_bytes, stream);
+}
+
+spin_status spin_kv_attn_shared(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                                const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale,
+                                int n_pages, int page_size, const int32_t* prefix_table, int prefix_len, int B,
+                                const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                int max_pages, float scale, float softcap, const float* slopes, int window,
+                                int causal, const int32_t* bidir_len, uint16_t* O, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    return kv_attn_impl(Q, T, Hq, Hkv, D, bits, K_codes, K_scale, V_codes, V_scale, n_pages, page_size, B, q_start,
+                        kv_len, page_table, max_pages, prefix_table, prefix_len, scale, softcap, slopes, window,
+                        causal, bidir_len, O, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

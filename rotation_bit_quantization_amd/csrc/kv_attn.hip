@@ -1,0 +1,438 @@
+// spin_kv_attn / spin_kv_attn_shared kernels: attention over the paged INT4 or
+// INT8 KV cache (the abstract's 4-bit KV cache; page "SpinQuant, Reproduced",
+// Q5: queries and keys both carry R3, so their products are unchanged).
+//
+// For query row q (one token, one head) over the visible tokens j of its
+// sequence, with integer codes a_j, b_j and fp16 scales ks_j, vs_j
+//   z_j = scale ks_j (q . a_j),  z <- cap tanh(z / cap),  z <- z - slope |pos - j|
+//   o   = sum_j e^(z_j) vs_j b_j / sum_j e^(z_j),   0 where nothing is visible.
+// Codes go into the fp16 matrix cores as the integers they are: exact.  The
+// value scale goes into the exponent,
+//   t_j = z_j log2(e) + log2(vs_j),  M = max t,  w_j = 2^(t_j - M) <= 1,
+//   o   = sum w_j b_j / sum w_j / vs_j,
+// so that the weights that are rounded to fp16 for the second product are at
+// most 1 whatever the scales are (a rounding of half a step, 2^-11 relative, of
+// each weight; weights below 2^-14 lose relative precision, which is 2^-25 of
+// the largest term).  Scores, maxima and sums are float32.
+//
+// Both products are computed transposed: S^T = A Q^T leaves a lane with one
+// query and four tokens of a tile of 16, which is what the second product O^T =
+// B^T W^T takes as its right operand: the weights of two tiles of tokens go
+// from accumulators to operands without leaving the lane, and the rescaling of
+// a row is one multiplication per register.
+#include "kv_batch.h"
+#include "spin_device.h"
+#include "spin_internal.h"
+
+namespace spin {
+namespace {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+constexpr int kAttnThreads = 256;
+constexpr int kAttnWaves = kAttnThreads / 64;
+constexpr int kRows = 16;                 // query rows of a tile
+constexpr int kStep = 32;                 // tokens a wave takes at a time
+constexpr int kSplitMinTokens = 256;      // fewest tokens worth a workgroup of their own
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
+
+union Frag {
+    uint32_t w[4];
+    h8 v;
+};
+
+// Two fp16 integers 1024 + u (u in the low bits of each half) minus `off`: exact.
+__device__ __forceinline__ uint32_t minus(uint32_t x, float off) {
+    const h2 o = {static_cast<_Float16>(-off), static_cast<_Float16>(-off)};
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) + o);
+}
+
+// Eight codes of one token as an operand.  The order of the eight within the
+// operand (order8) is the one that needs fewest instructions; queries are
+// loaded in the same order.
+template <int BITS>
+__device__ __forceinline__ int order8(int i) {
+    // 4 bits: 0 4 1 5 2 6 3 7;  8 bits: 0 2 1 3 4 6 5 7
+    if (BITS == 4) return (i >> 1) + 4 * (i & 1);
+    return (i & 4) + ((i & 2) >> 1) + 2 * (i & 1);
+}
+template <int BITS>
+__device__ __forceinline__ h8 key_operand(const uint32_t* w) {
+    Frag f;
+    if (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.w[i] = minus(((w[0] >> (4 * i)) & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.w[i] = minus(((w[i >> 1] >> (8 * (i & 1))) & 0x00FF00FFu) ^ 0x64806480u, 1152.0f);
+    }
+    return f.v;
+}
+
+// Code j of an octet, of eight tokens: w[BITS / 4 * token + ...], as an operand.
+template <int BITS>
+__device__ __forceinline__ h8 value_operand(const uint32_t* w, int j) {
+    Frag f;
+    constexpr int kW = BITS / 4;   // dwords of an octet
+    const int byte = BITS == 4 ? j >> 1 : j & 3, dw = BITS == 4 ? 0 : j >> 2;
+    const uint32_t sel = 0x0c000c04u + byte * 0x00010001u;   // byte of the first token below, of the second above
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = __builtin_amdgcn_perm(w[kW * (2 * i) + dw], w[kW * (2 * i + 1) + dw], sel);
+        if (BITS == 4)
+            f.w[i] = minus(((j & 1 ? x >> 4 : x) & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
+        else
+            f.w[i] = minus(x ^ 0x64806480u, 1152.0f);
+    }
+    return f.v;
+}
+
+__device__ __forceinline__ float max_over_groups(float v) {   // lanes l, l ^ 16, l ^ 32, l ^ 48
+    u2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __builtin_fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
+    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __builtin_fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
+}
+__device__ __forceinline__ float sum_over_groups(float v) {
+    u2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s.x) + __uint_as_float(s.y);
+    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(s.x) + __uint_as_float(s.y);
+}
+
+// tanh from one exponential: 1 - 2 / (e^(2 x) + 1), right at both infinities.
+__device__ __forceinline__ float tanh_fast(float x) {
+    return 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * kLog2e * x) + 1.0f);
+}
+
+// Tokens of sequence b in its own pages.
+__device__ __forceinline__ int context(const KvAttnArgs& a, int b) {
+    return min(max(a.kv_len[b], 0), a.max_pages << a.page_log2);
+}
+
+// Which tokens a workgroup has.
+struct Span {
+    const int32_t* table;
+    int n_table;        // entries of the table that may be read
+    int tokens;         // tokens the table's pages hold
+    int base;           // position of the first of them
+};
+
+// One tile of 16 query rows of one key head, over a share of the tokens: each
+// wave takes every fourth step of 32 tokens, the waves' results are joined in
+// LDS.  With one share the rows are finished here, otherwise they go to the
+// workspace, [share][T * Hq] rows.
+//
+// Bound at few rows: reading the cache, 2 (16 BITS + 2) bytes a token and head.
+template <int BITS>
+__global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits,
+                                                               int own_tiles, int own_splits) {
+    __shared__ float o_sh[kAttnWaves][kRows][129];
+    __shared__ float m_sh[kAttnWaves][kRows], l_sh[kAttnWaves][kRows];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int h = blockIdx.y, G = a.Hq / a.Hkv;
+    const int prefix_items = prefix_tiles * prefix_splits;
+    const bool shared = static_cast<int>(blockIdx.x) < prefix_items;
+    const int item = shared ? blockIdx.x : blockIdx.x - prefix_items;
+    const int splits = shared ? prefix_splits : own_splits;
+    const int tile = item / splits, split = item - tile * splits;
+    const int first_slot = shared ? 0 : prefix_splits;   // of the workspace
+    const int total_splits = prefix_splits + own_splits;
+
+    // the rows: (token, head of the group) pairs, of one sequence or (prefix) of all
+    Span span;
+    int t, head;             // this lane's row
+    bool valid;
+    int b;
+    if (shared) {
+        const int r = tile * kRows + n;
+        t = r / G;
+        head = h * G + r - t * G;
+        b = t < a.T ? find_sequence(a.q_start, a.B, t) : -1;
+        valid = b >= 0;
+        span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
+    } else {
+        // sequence b's tiles start at tile floor(q_start[b] G / 16) + b: room for each one's ragged last tile
+        int lo = 0, c = a.B;
+        while (c > 1) {
+            const int half = c >> 1;
+            const bool before = static_cast<long long>(a.q_start[lo + half]) * G / kRows + lo + half <= tile;
+            lo += before ? half : 0;
+            c = before ? c - half : half;
+        }
+        b = lo;
+        const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
+        const long long r = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / kRows + b)) * kRows + n;
+        const long long rows = static_cast<long long>(q1 - q0) * G;
+        valid = r >= 0 && r < rows;
+        const int i = valid ? static_cast<int>(r / G) : 0;
+        t = q0 + i;
+        head = h * G + (valid ? static_cast<int>(r - static_cast<long long>(i) * G) : 0);
+        span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
+    }
+    if (__ballot(valid) == 0) return;      // the same 16 rows in every wave: the workgroup leaves together
+
+    int pos = 0, both = 0;                 // the row's position, and the tokens that it sees whatever their order
+    if (valid) {
+        pos = a.prefix_len + context(a, b) - a.q_start[b + 1] + t;
+        if (a.bidir_len) both = a.bidir_len[b];
+    }
+    // the tokens that any of the rows sees
+    int lo = 0, hi = span.tokens;
+    {
+        int pmin = valid ? pos : 0x7FFFFFFF, pmax = valid ? max(pos + 1, both) : -0x7FFFFFFF, wmax = valid ? pos : -0x7FFFFFFF;
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) {
+            pmin = min(pmin, __shfl_xor(pmin, x, 64));
+            pmax = max(pmax, __shfl_xor(pmax, x, 64));
+            wmax = max(wmax, __shfl_xor(wmax, x, 64));
+        }
+        if (a.causal) hi = min(hi, pmax - span.base);
+        if (a.window > 0) {
+            lo = max(lo, static_cast<int>(max(static_cast<long long>(pmin) - a.window + 1 - span.base, 0LL)));
+            hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(wmax) + a.window - span.base));
+        }
+    }
+    int step0 = lo / kStep;
+    const int steps_all = hi > lo ? (hi + kStep - 1) / kStep - step0 : 0;
+    const int share = max((steps_all + splits - 1) / splits, kSplitMinTokens / kStep);
+    step0 += split * share;
+    const int steps = max(0, min(share, steps_all - split * share));
+
+    // queries, in the order of the keys' codes: lane (n, g) holds values 32 g .. 32 g + 31 of row n
+    h8 q[4];
+    {
+        const uint16_t* src = a.Q + (static_cast<long long>(t) * a.Hq + head) * 128 + 32 * g;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            Frag raw, f;
+            const u4 x = valid ? *reinterpret_cast<const u4*>(src + 8 * j) : u4{0, 0, 0, 0};
+            raw.w[0] = x.x; raw.w[1] = x.y; raw.w[2] = x.z; raw.w[3] = x.w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f.v[i] = raw.v[order8<BITS>(i)];
+            q[j] = f.v;
+        }
+    }
+    const float slope = a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+    const float to_log2 = a.softcap > 0.0f ? a.softcap * kLog2e : a.scale * kLog2e;
+    const float to_cap = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
+
+    float M = -__builtin_inff(), l_sum = 0.0f;
+    f4 o[8] = {};
+
+    for (int st = wave; st < steps; st += kAttnWaves) {
+        const int j0 = (step0 + st) * kStep;
+        h8 w_op;
+        uint32_t vcodes[8 * BITS / 4];
+        float tt[8], rvs[8];
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int jt = j0 + 16 * half;
+            // 16 tokens lie in one page; one that is not there counts as no tokens
+            const int entry = __builtin_amdgcn_readfirstlane(min(jt >> a.page_log2, span.n_table - 1));
+            int page = jt < span.tokens ? span.table[entry] : -1;
+            const bool there = page >= 0 && page < a.n_pages;
+            if (!there) page = 0;
+            const int slot = jt & ((1 << a.page_log2) - 1);
+            const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + slot;
+            const uint8_t* kp = a.K_codes + (token + n) * (16 * BITS) + g * (4 * BITS);
+            const uint8_t* vp = a.V_codes + (token + 4 * g) * (16 * BITS) + n * (4 * BITS);
+            uint32_t kw[BITS];
+#pragma unroll
+            for (int i = 0; i < BITS / 4; ++i) {
+                const u4 x = reinterpret_cast<const u4*>(kp)[i];
+                kw[4 * i] = x.x; kw[4 * i + 1] = x.y; kw[4 * i + 2] = x.z; kw[4 * i + 3] = x.w;
+                const u4 y = reinterpret_cast<const u4*>(vp)[i];
+                vcodes[half * BITS + 4 * i] = y.x; vcodes[half * BITS + 4 * i + 1] = y.y;
+                vcodes[half * BITS + 4 * i + 2] = y.z; vcodes[half * BITS + 4 * i + 3] = y.w;
+            }
+            const u2 ksr = *reinterpret_cast<const u2*>(a.K_scale + token + 4 * g);
+            const u2 vsr = *reinterpret_cast<const u2*>(a.V_scale + token + 4 * g);
+            f4 s = {};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS>(kw + j * (BITS / 4)), q[j], s, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float ks = __half2float(__ushort_as_half(static_cast<unsigned short>((r & 2 ? ksr.y : ksr.x) >> (16 * (r & 1)))));
+                const float vs = __half2float(__ushort_as_half(static_cast<unsigned short>((r & 2 ? vsr.y : vsr.x) >> (16 * (r & 1)))));
+                const int j = jt + 4 * g + r;
+                const int dist = pos - (j + span.base);
+                float z = __builtin_fmaf(s[r], ks, ks * 0.0f);   // NaN where ks is not finite, whatever s is
+                z = a.softcap > 0.0f ? tanh_fast(z * to_cap) * to_log2 : z * to_log2;
+                z -= slope * __builtin_fabsf(static_cast<float>(dist));
+                bool seen = there && j < span.tokens;
+                if (a.causal) seen = seen && (dist >= 0 || j + span.base < both);
+                if (a.window > 0) seen = seen && abs(dist) < a.window;
+                // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
+                const float vsf = vs == 0.0f ? 0x1p-24f : vs;
+                const float x = seen ? z + __builtin_amdgcn_logf(vsf) : -__builtin_inff();
+                tt[4 * half + r] = x;
+                rvs[4 * half + r] = vsf <= 65504.0f && seen ? __builtin_amdgcn_rcpf(vsf) : 0.0f;
+                top = __builtin_fmaxf(top, x);
+            }
+        }
+        top = max_over_groups(top);
+        const float M_new = __builtin_fmaxf(M, top);
+        const float M_use = M_new == -__builtin_inff() ? 0.0f : M_new;
+        const float keep = __builtin_amdgcn_exp2f(M - M_use);
+        M = M_new;
+        l_sum *= keep;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f2 w = {__builtin_amdgcn_exp2f(tt[2 * i] - M_use), __builtin_amdgcn_exp2f(tt[2 * i + 1] - M_use)};
+            l_sum = __builtin_fmaf(w.x, rvs[2 * i], __builtin_fmaf(w.y, rvs[2 * i + 1], l_sum));
+            const h2 p = __builtin_convertvector(w, h2);
+            w_op[2 * i] = p.x;
+            w_op[2 * i + 1] = p.y;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<BITS>(vcodes, j), w_op, o[j], 0, 0, 0);
+    }
+
+    // join the waves
+    l_sum = sum_over_groups(l_sum);
+    if (g == 0) m_sh[wave][n] = M;
+    __syncthreads();
+    float M_all = m_sh[0][n];
+#pragma unroll
+    for (int w = 1; w < kAttnWaves; ++w) M_all = __builtin_fmaxf(M_all, m_sh[w][n]);
+    const float f = M == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(M - M_all);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o_sh[wave][n][8 * (4 * g + r) + j] = o[j][r] * f;
+    }
+    if (g == 0) l_sh[wave][n] = l_sum * f;
+    __syncthreads();
+    // 16 threads a row, 8 values each
+    const int row = threadIdx.x >> 4, c = threadIdx.x & 15;
+    const int t_row = __shfl(t, row, 64), head_row = __shfl(head, row, 64);   // lane `row` of every wave has row `row`
+    const bool valid_row = __shfl(static_cast<int>(valid), row, 64) != 0;
+    if (!valid_row) return;
+    float l_all = 0.0f, out[8] = {};
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+        l_all += l_sh[w][row];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] += o_sh[w][row][8 * c + i];
+    }
+    const long long at = static_cast<long long>(t_row) * a.Hq + head_row;
+    if (total_splits == 1) {
+        const float rl = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+        Frag res;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) res.v[i] = static_cast<_Float16>(out[i] * rl);
+        *reinterpret_cast<u4*>(a.O + at * 128 + 8 * c) = u4{res.w[0], res.w[1], res.w[2], res.w[3]};
+    } else {
+        float* p = a.partial + ((first_slot + split) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
+        float M_row = m_sh[0][row];
+#pragma unroll
+        for (int w = 1; w < kAttnWaves; ++w) M_row = __builtin_fmaxf(M_row, m_sh[w][row]);
+        if (l_all != 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<f2*>(p + 8 * c)[i] = f2{out[2 * i], out[2 * i + 1]};
+        }
+        if (c == 0) {
+            p[128] = M_row;
+            p[129] = l_all;
+        }
+    }
+}
+
+// Joins the shares of a row: one wave a row, two values a lane.
+__global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int splits) {
+    const long long rows = static_cast<long long>(a.T) * a.Hq;
+    const long long at = static_cast<long long>(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
+    if (at >= rows) return;
+    const int t = static_cast<int>(at / a.Hq);
+    if (find_sequence(a.q_start, a.B, t) < 0) return;
+    const int lane = threadIdx.x & 63;
+    float M = -__builtin_inff();
+    for (int s = 0; s < splits; ++s) {
+        M = __builtin_fmaxf(M, a.partial[(s * rows + at) * kPartial + 128]);
+    }
+    float l = 0.0f;
+    f2 o = {};
+    for (int s = 0; s < splits; ++s) {
+        const float* p = a.partial + (s * rows + at) * kPartial;
+        if (p[129] == 0.0f) continue;      // no visible token there: the sums are not written
+        const float f = __builtin_amdgcn_exp2f(p[128] - M);
+        const f2 x = reinterpret_cast<const f2*>(p)[lane];
+        l = __builtin_fmaf(p[129], f, l);
+        o.x = __builtin_fmaf(x.x, f, o.x);
+        o.y = __builtin_fmaf(x.y, f, o.y);
+    }
+    const float rl = l == 0.0f ? 0.0f : 1.0f / l;
+    const h2 res = {static_cast<_Float16>(o.x * rl), static_cast<_Float16>(o.y * rl)};
+    reinterpret_cast<h2*>(a.O)[at * 64 + lane] = res;
+}
+
+// Grid of a call: row tiles and the shares their tokens are split into.
+struct Plan {
+    long long prefix_tiles, own_tiles;
+    int prefix_splits, own_splits;
+    size_t workspace;
+};
+
+Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
+    constexpr long long kWanted = 2048;    // workgroups that fill the card
+    const long long G = Hq / Hkv;
+    Plan p = {};
+    p.own_tiles = T * G / kRows + B;
+    p.prefix_tiles = prefix_len > 0 ? (T * G + kRows - 1) / kRows : 0;
+    auto shares = [&](long long tiles, int tokens) {
+        const long long most = (tokens + kSplitMinTokens - 1) / kSplitMinTokens;
+        const long long want = (kWanted + tiles * Hkv - 1) / (tiles * Hkv);
+        return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
+    };
+    p.own_splits = shares(p.own_tiles, max_kv);
+    p.prefix_splits = prefix_len > 0 ? shares(p.prefix_tiles, prefix_len) : 0;
+    const int all = p.own_splits + p.prefix_splits;
+    p.workspace = all > 1 ? static_cast<size_t>(all) * T * Hq * kPartial * sizeof(float) : 0;
+    return p;
+}
+
+}  // namespace
+
+size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
+    return plan(T, Hq, Hkv, B, max_kv, prefix_len).workspace;
+}
+
+bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
+    const Plan p = plan(T, Hq, Hkv, B, max_kv, prefix_len);
+    constexpr long long kMost = (1LL << 24) - 1;   // workgroups of 256 in a launch dimension
+    return p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits <= kMost && Hkv <= 65535 &&
+           (static_cast<long long>(T) * Hq + kAttnWaves - 1) / kAttnWaves <= kMost;
+}
+
+hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s) {
+    const Plan p = plan(a.T, a.Hq, a.Hkv, a.B, a.max_pages << a.page_log2, a.prefix_len);
+    const dim3 grid(static_cast<unsigned>(p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits), a.Hkv);
+    if (bits == 8)
+        hipLaunchKernelGGL(kv_attn_rows16<8>, grid, dim3(kAttnThreads), 0, s, a, static_cast<int>(p.prefix_tiles),
+                           p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
+    else
+        hipLaunchKernelGGL(kv_attn_rows16<4>, grid, dim3(kAttnThreads), 0, s, a, static_cast<int>(p.prefix_tiles),
+                           p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.own_splits + p.prefix_splits == 1) return e;
+    const long long rows = static_cast<long long>(a.T) * a.Hq;
+    hipLaunchKernelGGL(kv_attn_join, dim3(static_cast<unsigned>((rows + kAttnWaves - 1) / kAttnWaves)), dim3(kAttnThreads), 0,
+                       s, a, p.own_splits + p.prefix_splits);
+    return hipGetLastError();
+}
+
+}  // namespace spin

@@ -1,0 +1,45 @@
+// What the kernels on the paged KV cache share: where a query row stands in a
+// batch of sequences.
+//
+// Query rows of all sequences lie behind each other; q_start[0 .. B] are their
+// borders.  Row t belongs to the last sequence whose start is <= t, if t lies
+// before that sequence's end.  Every index that these functions read with is
+// bounded by B alone, so that borders that do not rise give wrong places, and
+// never a read outside the arrays.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace spin {
+
+// The sequence of row t, or -1, found by the 16 lanes of a DPP row together (l
+// = 0 .. 15 its lane, all 16 with the same t): a 16-way search, one load deep
+// per factor of 16 in B.
+__device__ __forceinline__ int find_sequence16(const int32_t* __restrict__ q_start, int B, int t, int l) {
+    int lo = 0, n = B;
+    while (n > 1) {
+        const int step = (n + 15) >> 4;
+        const int at = l * step;
+        const bool before = at < n && q_start[lo + at] <= t;
+        const int seen = __popcll((__ballot(before) >> (threadIdx.x & 48)) & 0xFFFFull);
+        const int skip = max(seen - 1, 0) * step;
+        lo += skip;
+        n = min(step, n - skip);
+    }
+    return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
+}
+
+// The same by one lane alone: a binary search.
+__device__ __forceinline__ int find_sequence(const int32_t* __restrict__ q_start, int B, int t) {
+    int lo = 0, n = B;
+    while (n > 1) {
+        const int half = n >> 1;
+        const bool before = q_start[lo + half] <= t;
+        lo += before ? half : 0;
+        n = before ? n - half : half;
+    }
+    return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
+}
+
+}  // namespace spin

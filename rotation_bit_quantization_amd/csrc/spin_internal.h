@@ -33,6 +33,68 @@ hipError_t launch_kv_qkv(const void* Q, const void* K, const void* V, bool x_f16
                          int bits, float* Q_rot, uint8_t* K_codes, uint16_t* K_scale, float* K_rot,
                          uint8_t* V_codes, uint16_t* V_scale, hipStream_t s);
 
+// cos | sin rows of positions pos0 .. pos0 + P - 1 for n frequencies.
+hipError_t launch_rope_table(const double* inv_freq, int n, int pos0, int P, double attn_scale, float* table,
+                             hipStream_t s);
+
+// Norm + position rotation + R3 of queries and keys, codes of keys and values
+// into the paged cache (include/libspin.h has the layout).
+struct KvAppendArgs {
+    const void* Q;                 // NULL: no queries (Hq is 0)
+    const void* K;
+    const void* V;
+    int T, Hq, Hkv;
+    long long q_stride, k_stride, v_stride;   // values between tokens
+    const float* q_norm;           // [128] or NULL
+    const float* k_norm;
+    double eps;
+    const float* rope;             // [rope_len][rot_dim] cos | sin, NULL with rot_dim 0
+    int rope_len, rot_dim;
+    bool interleaved;
+    int pos0, B;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int max_pages, n_pages, page_log2;
+    uint8_t* K_codes;
+    uint16_t* K_scale;
+    uint8_t* V_codes;
+    uint16_t* V_scale;
+    uint16_t* Q_out;
+    long long kv_blocks;           // set by the launcher
+    float norm;
+};
+hipError_t launch_kv_append(KvAppendArgs a, bool x_f16, int bits, hipStream_t s);
+long long kv_append_blocks(int T, int Hq, int Hkv);
+
+// Attention over the paged cache.
+struct KvAttnArgs {
+    const uint16_t* Q;
+    int T, Hq, Hkv;
+    const uint8_t* K_codes;
+    const uint16_t* K_scale;
+    const uint8_t* V_codes;
+    const uint16_t* V_scale;
+    int n_pages, page_log2, B;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int max_pages;
+    const int32_t* prefix_table;   // [ceil(prefix_len / page)], read if prefix_len > 0
+    int prefix_len;
+    float scale, softcap;
+    const float* slopes;
+    int window;
+    bool causal;
+    const int32_t* bidir_len;
+    uint16_t* O;
+    float* partial;                // the workspace
+};
+// Bytes of workspace the launch needs (0: none), and whether it fits one launch.
+size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len);
+bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len);
+hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s);
+
 // The FP6 matrix-core path of launch_w4a4_gemm (exact for K <= kGemmFp6MaxK).
 constexpr int kGemmFp6MaxK = 65536;
 bool w4a4_gemm_fp6_applies(int M, int N, int K);

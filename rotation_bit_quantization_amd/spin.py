@@ -19,7 +19,8 @@ __all__ = ["SpinError", "load", "library_path", "SPIN_OK", "SPIN_ERR_NULL",
            "SPIN_F32", "SPIN_F16", "spin_status_string", "spin_fold_rotation", "spin_fwht_quant",
            "spin_w4a4_gemm", "spin_kv_quant", "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8",
            "spin_kv_qkv", "spin_w4a4_gemm_ex", "spin_fwht_quant_gemm", "spin_fwht_quant_gemm_noalloc", "spin_fwht_quant_f6", "spin_w4a4_gemm_f6",
-           "spin_codes_f6", "spin_w4a4_gemm_f6f6", "f6_bytes", "SPIN_GEMM_AUTO", "SPIN_GEMM_INT8", "SPIN_GEMM_FP6", "SPIN_GEMM_FP6_SPLITK",
+           "spin_codes_f6", "spin_w4a4_gemm_f6f6", "f6_bytes", "kv_cache", "spin_rope_table", "spin_kv_append",
+           "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace", "SPIN_GEMM_AUTO", "SPIN_GEMM_INT8", "SPIN_GEMM_FP6", "SPIN_GEMM_FP6_SPLITK",
            "EXPORTED_SYMBOLS"]
 
 SPIN_OK, SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE, SPIN_ERR_MISALIGNED, SPIN_ERR_UNSUPPORTED, \
@@ -31,7 +32,8 @@ SPIN_FWHT_QUANT_GEMM_WORKSPACE_WORDS = 1025
 EXPORTED_SYMBOLS = ("spin_fold_rotation", "spin_fwht_quant", "spin_w4a4_gemm", "spin_kv_quant",
                     "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8", "spin_kv_qkv", "spin_w4a4_gemm_ex",
                     "spin_fwht_quant_gemm", "spin_fwht_quant_gemm_noalloc", "spin_fwht_quant_f6",
-                    "spin_w4a4_gemm_f6", "spin_codes_f6", "spin_w4a4_gemm_f6f6",
+                    "spin_w4a4_gemm_f6", "spin_codes_f6", "spin_w4a4_gemm_f6f6", "spin_rope_table", "spin_kv_append",
+                    "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace",
                     "spin_status_string", "spin_version")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -77,6 +79,17 @@ def load():
     lib.spin_w4a8_gemm.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, vp]
     lib.spin_kv_quant8.argtypes = [vp, i, i, i, i, i, vp, vp, vp, vp]
     lib.spin_kv_qkv.argtypes = [vp, vp, vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp]
+    f, q, d, z = ctypes.c_float, ctypes.c_int64, ctypes.c_double, ctypes.c_size_t
+    lib.spin_rope_table.argtypes = [vp, i, i, i, d, vp, vp]
+    lib.spin_kv_append.argtypes = [vp, vp, vp, i, i, i, i, i, q, q, q, vp, vp, f, vp, i, i, i, i, i, vp, vp, vp, vp, i, i,
+                                   i, vp, vp, vp, i, vp, vp]
+    cache = [vp, i, i, i, i, i, vp, vp, vp, vp, i, i]
+    mask = [f, f, vp, i, i, vp, vp, vp, z, vp]
+    lib.spin_kv_attn.argtypes = cache + [i, vp, vp, vp, i] + mask
+    lib.spin_kv_attn_shared.argtypes = cache + [vp, i, i, vp, vp, vp, i] + mask
+    lib.spin_kv_attn_workspace.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(z)]
+    for name in ("spin_rope_table", "spin_kv_append", "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace"):
+        getattr(lib, name).restype = ctypes.c_int
     for name in ("spin_fold_rotation", "spin_fwht_quant", "spin_w4a4_gemm", "spin_kv_quant",
                  "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8", "spin_kv_qkv", "spin_w4a4_gemm_ex", "spin_fwht_quant_gemm",
                  "spin_fwht_quant_gemm_noalloc", "spin_fwht_quant_f6", "spin_w4a4_gemm_f6"):
@@ -499,3 +512,212 @@ def spin_kv_qkv(K, V, Q=None, bits=4, want_k_rot=False, out=None, stream=None):
                             _ptr(res["K_rot"]), _ptr(res["V_codes"]), _ptr(res["V_scale"]), _stream(stream))
     _raise("spin_kv_qkv", st)
     return res
+
+
+# ---------------------------------------------------------------- the paged KV cache
+
+def _launch(fn, tensors, made, stream, args):
+    """Call fn(*args, stream) on the device its tensors live on: on that device's current stream, or on
+    `stream`.  `tensors` have to share one device; `made`, the ones allocated for this call, are kept from
+    reuse until the work on another stream is done."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
+    call = getattr(load(), fn)
+    if _raw_stream is not None and _cur_device is not None and stream is None and _cur_device() == dev.index:
+        st = call(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            here = torch.cuda.current_stream()
+            if stream is None:
+                stream = here
+            elif not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            if stream.device != dev:
+                raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {dev}")
+            st = call(*args, stream.cuda_stream)
+            if st == SPIN_OK and stream != here:
+                for t in made:
+                    t.record_stream(stream)
+    _raise(fn, st)
+
+
+def kv_cache(n_pages, Hkv, page_size, bits=4, device="cuda"):
+    """An empty pool of cache pages: a dict of ``K_codes`` [n_pages, Hkv, page_size, 16 * bits] and ``V_codes``
+    [n_pages, Hkv, page_size / 4, 16, 4, bits] uint8, ``K_scale`` and ``V_scale`` [n_pages, Hkv, page_size] fp16
+    (layouts: include/libspin.h)."""
+    if bits not in (4, 8):
+        raise ValueError("bits must be 4 or 8")
+    if page_size < 16 or page_size & (page_size - 1):
+        raise ValueError("page_size must be a power of two of at least 16")
+    return {"K_codes": torch.zeros((n_pages, Hkv, page_size, 16 * bits), dtype=torch.uint8, device=device),
+            "K_scale": torch.zeros((n_pages, Hkv, page_size), dtype=torch.float16, device=device),
+            "V_codes": torch.zeros((n_pages, Hkv, page_size // 4, 16, 4, bits), dtype=torch.uint8, device=device),
+            "V_scale": torch.zeros((n_pages, Hkv, page_size), dtype=torch.float16, device=device)}
+
+
+def _cache(cache):
+    """Check a cache's four tensors; returns them with (n_pages, Hkv, page_size, bits)."""
+    kc, ks, vc, vs = (cache[name] for name in ("K_codes", "K_scale", "V_codes", "V_scale"))
+    _check(kc, "K_codes", (torch.uint8,))
+    if kc.dim() != 4 or kc.shape[3] not in (64, 128):
+        raise ValueError(f"K_codes has shape {tuple(kc.shape)}, expected [n_pages, Hkv, page_size, 64 or 128]")
+    n_pages, Hkv, page, width = kc.shape
+    bits = width // 16
+    _check(ks, "K_scale", (torch.float16,), (n_pages, Hkv, page))
+    _check(vc, "V_codes", (torch.uint8,), (n_pages, Hkv, page // 4, 16, 4, bits))
+    _check(vs, "V_scale", (torch.float16,), (n_pages, Hkv, page))
+    return (kc, ks, vc, vs), (n_pages, Hkv, page, bits)
+
+
+def _batch(page_table, q_start, kv_len):
+    """Check a batch's three arrays; returns (B, max_pages)."""
+    _check(page_table, "page_table", (torch.int32,))
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [B, max_pages]")
+    B, max_pages = page_table.shape
+    _check(q_start, "q_start", (torch.int32,), (B + 1,))
+    _check(kv_len, "kv_len", (torch.int32,), (B,))
+    return B, max_pages
+
+
+def _rows(x, name, dtype, T):
+    """Check [T, H, 128] rows whose heads lie beside each other; returns (H, values from a token to the next)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.shape[0] != T or x.shape[2] != 128:
+        raise ValueError(f"{name} must be a [{T}, H, 128] tensor")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got {x.device})")
+    if x.dtype != dtype or dtype not in (torch.float16, torch.float32):
+        raise TypeError(f"{name} has dtype {x.dtype}, expected float16 or float32, the same for all")
+    H = x.shape[1]
+    if x.numel() and (x.stride(2) != 1 or (H > 1 and x.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must lie beside each other (strides {x.stride()})")
+    return H, x.stride(0) if T > 1 else max(128 * H, 128)
+
+
+def spin_rope_table(inv_freq, n_pos, pos0=0, attn_scale=1.0, table=None, stream=None):
+    """inv_freq [n] float64 -> table [n_pos, 2 n] fp32: n cosines, then n sines of (pos0 + p) * inv_freq."""
+    _check(inv_freq, "inv_freq", (torch.float64,))
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [n]")
+    n = inv_freq.shape[0]
+    made = []
+    if table is None:
+        table = torch.empty((n_pos, 2 * n), dtype=torch.float32, device=inv_freq.device)
+        made.append(table)
+    _check(table, "table", (torch.float32,), (n_pos, 2 * n))
+    if n_pos == 0:                  # an empty tensor has no address to pass
+        return table
+    _launch("spin_rope_table", (inv_freq, table), made, stream,
+            (_ptr(inv_freq), n, int(pos0), n_pos, float(attn_scale), _ptr(table)))
+    return table
+
+
+def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, interleaved=False, q_norm=None, k_norm=None,
+                   eps=1e-6, pos0=0, Q_out=None, stream=None):
+    """Rows of qkv_proj (Q [T, Hq, 128] or None, K and V [T, Hkv, 128], fp16 / fp32, views of one product are
+    fine) -> Q_out [T, Hq, 128] fp16 (or None); the codes of K and V go into the pages of ``cache``.
+
+    ``rope`` is a spin_rope_table of the rotated part of a head; ``q_norm`` and ``k_norm`` are [128] fp32 weights."""
+    tensors, (n_pages, Hkv, page, bits) = _cache(cache)
+    B, max_pages = _batch(page_table, q_start, kv_len)
+    if not isinstance(K, torch.Tensor):
+        raise TypeError("K must be a torch.Tensor")
+    T = K.shape[0]
+    hk, k_stride = _rows(K, "K", K.dtype, T)
+    hv, v_stride = _rows(V, "V", K.dtype, T)
+    if hk != Hkv or hv != Hkv:
+        raise ValueError(f"K has {hk} and V {hv} heads, the cache {Hkv}")
+    Hq, q_stride, made = 0, 0, []
+    if Q is not None:
+        Hq, q_stride = _rows(Q, "Q", K.dtype, T)
+        if Q_out is None:
+            Q_out = torch.empty((T, Hq, 128), dtype=torch.float16, device=Q.device)
+            made.append(Q_out)
+        _check(Q_out, "Q_out", (torch.float16,), (T, Hq, 128))
+    elif Q_out is not None:
+        raise ValueError("Q_out without Q")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _check(w, name, (torch.float32,), (128,))
+    rope_len = rot_dim = 0
+    if rope is not None:
+        _check(rope, "rope", (torch.float32,))
+        rope_len, rot_dim = rope.shape
+    if T == 0 or B == 0:            # an empty tensor has no address to pass
+        return Q_out
+    kc, ks, vc, vs = tensors
+    _launch("spin_kv_append", (K, V, Q, Q_out, q_norm, k_norm, rope, page_table, q_start, kv_len, *tensors), made, stream,
+            (_ptr(Q), _ptr(K), _ptr(V), _dtype_code(K), T, Hq, Hkv, 128, q_stride, k_stride, v_stride, _ptr(q_norm),
+             _ptr(k_norm), float(eps), _ptr(rope), rope_len, rot_dim, int(interleaved), int(pos0), bits, _ptr(kc), _ptr(ks),
+             _ptr(vc), _ptr(vs), n_pages, page, B, _ptr(q_start), _ptr(kv_len), _ptr(page_table), max_pages,
+             _ptr(Q_out)))
+    return Q_out
+
+
+def spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len=0):
+    """Bytes of workspace that spin_kv_attn (spin_kv_attn_shared with a prefix) takes at these sizes."""
+    n = ctypes.c_size_t(0)
+    _raise("spin_kv_attn_workspace", load().spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len,
+                                                                   ctypes.byref(n)))
+    return n.value
+
+
+def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O,
+          workspace, stream):
+    tensors, (n_pages, Hkv, page, bits) = _cache(cache)
+    B, max_pages = _batch(page_table, q_start, kv_len)
+    _check(Q, "Q", (torch.float16,))
+    if Q.dim() != 3 or Q.shape[2] != 128:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, 128]")
+    T, Hq = Q.shape[0], Q.shape[1]
+    prefix_table, prefix_len = prefix if prefix is not None else (None, 0)
+    if slopes is not None:
+        _check(slopes, "slopes", (torch.float32,), (Hq,))
+    if bidir_len is not None:
+        _check(bidir_len, "bidir_len", (torch.int32,), (B,))
+    made = []
+    if O is None:
+        O = torch.empty((T, Hq, 128), dtype=torch.float16, device=Q.device)
+        made.append(O)
+    _check(O, "O", (torch.float16,), (T, Hq, 128))
+    if T == 0 or B == 0:            # an empty tensor has no address to pass
+        return O
+    need = spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page, prefix_len)
+    if workspace is None:
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=Q.device)
+            made.append(workspace)
+    else:
+        _check(workspace, "workspace", (torch.uint8,))
+    kc, ks, vc, vs = tensors
+    _launch(fn, (Q, O, workspace, slopes, bidir_len, prefix_table, page_table, q_start, kv_len, *tensors), made, stream,
+            (_ptr(Q), T, Hq, Hkv, 128, bits, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages, page,
+             *(() if prefix is None else (_ptr(prefix_table), prefix_len)), B, _ptr(q_start), _ptr(kv_len),
+             _ptr(page_table), max_pages, 128 ** -0.5 if scale is None else float(scale), float(softcap), _ptr(slopes),
+             int(window), int(causal), _ptr(bidir_len), _ptr(O), _ptr(workspace),
+             0 if workspace is None else workspace.numel()))
+    return O
+
+
+def spin_kv_attn(Q, cache, page_table, q_start, kv_len, scale=None, softcap=0.0, slopes=None, window=0, causal=True,
+                 bidir_len=None, O=None, workspace=None, stream=None):
+    """Q [T, Hq, 128] fp16 (from spin_kv_append) over the pages of each sequence -> O [T, Hq, 128] fp16.
+
+    ``scale`` is 1 / sqrt(128) by default.  ``workspace`` (uint8, spin_kv_attn_workspace bytes) is allocated if
+    it is not given."""
+    return _attn("spin_kv_attn", Q, cache, None, page_table, q_start, kv_len, scale, softcap, slopes, window, causal,
+                 bidir_len, O, workspace, stream)
+
+
+def spin_kv_attn_shared(Q, cache, prefix_table, prefix_len, page_table, q_start, kv_len, scale=None, softcap=0.0,
+                        slopes=None, window=0, causal=True, bidir_len=None, O=None, workspace=None, stream=None):
+    """spin_kv_attn where the first ``prefix_len`` tokens of every sequence lie in the pages ``prefix_table``
+    names ([ceil(prefix_len / page_size)] int32) and ``page_table`` and ``kv_len`` count what follows."""
+    _check(prefix_table, "prefix_table", (torch.int32,))
+    page = cache["K_codes"].shape[2]
+    if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-int(prefix_len) // page):
+        raise ValueError(f"prefix_table has shape {tuple(prefix_table.shape)}, too few pages for {prefix_len} tokens")
+    return _attn("spin_kv_attn_shared", Q, cache, (prefix_table, int(prefix_len)), page_table, q_start, kv_len, scale,
+                 softcap, slopes, window, causal, bidir_len, O, workspace, stream)
