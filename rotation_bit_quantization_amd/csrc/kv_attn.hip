@@ -40,6 +40,8 @@ constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
 constexpr int kSplitMinTokens = 256;      // fewest tokens worth a workgroup of their own
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kManyRows = 32;             // rows on the same tokens from which tiles of 128, 256 rows are taken
+constexpr int kWideRows = 512;
 constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
 
 union Frag {
@@ -352,6 +354,418 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int
     }
 }
 
+// ---------------------------------------------------------------------------------------------- many rows
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr int kTileTokens = 64;            // tokens staged at a time
+constexpr float kNone = -1e30f;            // "no token yet": below every score, and finite
+constexpr float kSlack = 8.0f;             // a row's maximum may lag by this many powers of two
+
+// Four tokens' code j of an octet (w: BITS / 4 dwords a token) as fp16.
+template <int BITS>
+__device__ __forceinline__ u2 value_quad(const uint32_t* w, int j) {
+    constexpr int kW = BITS / 4;
+    const int byte = BITS == 4 ? j >> 1 : j & 3, dw = BITS == 4 ? 0 : j >> 2;
+    const uint32_t sel = 0x0c000c04u + byte * 0x00010001u;
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = __builtin_amdgcn_perm(w[kW * (2 * i) + dw], w[kW * (2 * i + 1) + dw], sel);
+        r[i] = BITS == 4 ? minus(((j & 1 ? x >> 4 : x) & 0x000F000Fu) ^ 0x64086408u, 1032.0f) : minus(x ^ 0x64806480u, 1152.0f);
+    }
+    return u2{r[0], r[1]};
+}
+
+__device__ __forceinline__ float swap_halves_max(float v) {
+    const u2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __builtin_fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
+}
+__device__ __forceinline__ float swap_halves_sum(float v) {
+    const u2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(s.x) + __uint_as_float(s.y);
+}
+
+// The same for tiles of 128 R rows (R = 1, 2): four waves of 32 R rows share 64
+// tokens at a time, which the workgroup turns into fp16 codes in LDS once,
+// keys as [token][d] and values as [d][token], while it computes on the 64
+// before (two buffers, one barrier a step).
+template <int BITS, int R, bool FANCY>
+__global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
+                                                                            int own_tiles, int own_splits) {
+    constexpr int kTileRows = 128 * R;
+    __shared__ u4 k_sh[2][kTileTokens * 16];       // 16 chunks of 8 values a token, chunk c at c ^ (token & 7)
+    __shared__ u4 v_sh[2][128 * 8];                // 8 chunks of 8 tokens a value, chunk c at c ^ ((d ^ d / 8) & 7)
+    __shared__ f4 f_sh[2][3][kTileTokens / 4];     // per token: key factor, log2 of the value scale, its reciprocal
+    __shared__ int range_sh[kAttnWaves][3];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = lane & 31, hf = lane >> 5;
+    const int G = a.Hq / a.Hkv;
+    // key heads alternate fastest: with 8 of them a head stays on one XCD; late tiles, the long ones, come first
+    const int h = blockIdx.x % a.Hkv;
+    const int prefix_items = prefix_tiles * prefix_splits;
+    const int index = blockIdx.x / a.Hkv;
+    const bool shared = index < prefix_items;
+    const int item = shared ? index : prefix_items + own_tiles * own_splits - 1 - index;
+    const int splits = shared ? prefix_splits : own_splits;
+    const int tile = item / splits, split = item - tile * splits;
+    const int first_slot = shared ? 0 : prefix_splits;
+    const int total_splits = prefix_splits + own_splits;
+
+    Span span;
+    int t[R], head[R], pos[R], both[R];
+    bool valid[R];
+    bool any = false;
+    if (shared) {
+        span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            const long long r = static_cast<long long>(tile) * kTileRows + wave * 32 * R + x * 32 + n;
+            const long long tt = r / G;
+            t[x] = static_cast<int>(tt);
+            head[x] = h * G + static_cast<int>(r - tt * G);
+            const int b = tt < a.T ? find_sequence(a.q_start, a.B, t[x]) : -1;
+            valid[x] = b >= 0;
+            pos[x] = both[x] = 0;
+            if (valid[x]) {
+                pos[x] = a.prefix_len + context(a, b) - a.q_start[b + 1] + t[x];
+                if (a.bidir_len) both[x] = a.bidir_len[b];
+            }
+        }
+    } else {
+        int lo = 0, c = a.B;
+        while (c > 1) {
+            const int half = c >> 1;
+            const bool before = static_cast<long long>(a.q_start[lo + half]) * G / kTileRows + lo + half <= tile;
+            lo += before ? half : 0;
+            c = before ? c - half : half;
+        }
+        const int b = lo;
+        const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
+        const long long first = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / kTileRows + b)) * kTileRows;
+        const long long rows = static_cast<long long>(q1 - q0) * G;
+        span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            const long long r = first + wave * 32 * R + x * 32 + n;
+            valid[x] = r >= 0 && r < rows;
+            const int i = valid[x] ? static_cast<int>(r / G) : 0;
+            t[x] = q0 + i;
+            head[x] = h * G + (valid[x] ? static_cast<int>(r - static_cast<long long>(i) * G) : 0);
+            pos[x] = valid[x] ? a.prefix_len + span.tokens - a.q_start[b + 1] + t[x] : 0;
+            both[x] = valid[x] && a.bidir_len ? a.bidir_len[b] : 0;
+        }
+    }
+    // positions of the wave's rows, then of the workgroup's: which tokens any of them sees
+    int pmin = 0x7FFFFFFF, pmax = -0x7FFFFFFF, bmax = -0x7FFFFFFF, bmin = 0x7FFFFFFF;
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+        any = any || valid[x];
+        pmin = min(pmin, valid[x] ? pos[x] : pmin);
+        pmax = max(pmax, valid[x] ? pos[x] : pmax);
+        bmax = max(bmax, valid[x] ? both[x] : bmax);
+        bmin = min(bmin, valid[x] ? both[x] : bmin);
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        pmin = min(pmin, __shfl_xor(pmin, m, 64));
+        pmax = max(pmax, __shfl_xor(pmax, m, 64));
+        bmax = max(bmax, __shfl_xor(bmax, m, 64));
+        bmin = min(bmin, __shfl_xor(bmin, m, 64));
+    }
+    pmin = __builtin_amdgcn_readfirstlane(pmin);
+    pmax = __builtin_amdgcn_readfirstlane(pmax);
+    bmax = __builtin_amdgcn_readfirstlane(bmax);
+    bmin = __builtin_amdgcn_readfirstlane(bmin);
+    const bool wave_any = __ballot(any) != 0;
+    if (lane == 0) {
+        range_sh[wave][0] = pmin;
+        range_sh[wave][1] = pmax;
+        range_sh[wave][2] = max(pmax == -0x7FFFFFFF ? pmax : pmax + 1, bmax);
+    }
+    __syncthreads();
+    int lo = 0, hi = span.tokens;
+    {
+        int gmin = range_sh[0][0], gmax = range_sh[0][1], gend = range_sh[0][2];
+#pragma unroll
+        for (int w = 1; w < kAttnWaves; ++w) {
+            gmin = min(gmin, range_sh[w][0]);
+            gmax = max(gmax, range_sh[w][1]);
+            gend = max(gend, range_sh[w][2]);
+        }
+        if (gmin == 0x7FFFFFFF) return;    // no row of a sequence: the workgroup leaves together
+        if (a.causal) hi = min(hi, gend - span.base);
+        if (a.window > 0) {
+            lo = static_cast<int>(max(static_cast<long long>(gmin) - a.window + 1 - span.base, 0LL));
+            hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(gmax) + a.window - span.base));
+        }
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    int step0 = lo / kTileTokens;
+    const int steps_all = hi > lo ? (hi + kTileTokens - 1) / kTileTokens - step0 : 0;
+    const int share = max((steps_all + splits - 1) / splits, kSplitMinTokens / kTileTokens);
+    step0 += split * share;
+    const int steps = max(0, min(share, steps_all - split * share));
+
+    // queries: lane (n, hf) holds values 16 k + 8 hf .. + 7 of its row, k = 0 .. 7, in the order of the keys' codes
+    h8 q[R][8];
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+        const uint16_t* src = a.Q + (static_cast<long long>(t[x]) * a.Hq + head[x]) * 128 + 8 * hf;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            Frag raw, f;
+            const u4 y = valid[x] ? *reinterpret_cast<const u4*>(src + 16 * k) : u4{0, 0, 0, 0};
+            raw.w[0] = y.x; raw.w[1] = y.y; raw.w[2] = y.z; raw.w[3] = y.w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f.v[i] = raw.v[order8<BITS>(i)];
+            q[x][k] = f.v;
+        }
+    }
+    float slope[R];
+#pragma unroll
+    for (int x = 0; x < R; ++x) slope[x] = FANCY && a.slopes && valid[x] ? a.slopes[head[x]] * kLog2e : 0.0f;
+    const bool capped = FANCY && a.softcap > 0.0f;
+    const float key_factor = capped ? a.scale / a.softcap : a.scale * kLog2e;
+    const float to_log2 = a.softcap * kLog2e;
+
+    // what this thread stages of a step: 32 codes of one token's key, one octet of four tokens' values, one scale
+    uint32_t kraw[BITS], vraw[BITS];
+    uint16_t sraw = 0;
+    bool s_there = false;
+    const int k_token = threadIdx.x >> 2, k_part = threadIdx.x & 3;
+    const int v_quad = threadIdx.x >> 4, v_octet = threadIdx.x & 15;
+    auto page_of = [&](int j) {     // page of token j, -1 if it has none
+        if (j >= span.tokens) return -1;
+        const int p = span.table[min(j >> a.page_log2, span.n_table - 1)];
+        return p >= 0 && p < a.n_pages ? p : -1;
+    };
+    auto slot_of = [&](int page, int j) {
+        return ((static_cast<long long>(max(page, 0)) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+    };
+    auto fetch = [&](int st) {
+        const int j0 = (step0 + st) * kTileTokens;
+        const u4* kp = reinterpret_cast<const u4*>(a.K_codes + slot_of(page_of(j0 + k_token), j0 + k_token) * (16 * BITS) + k_part * (4 * BITS));
+        const u4* vp = reinterpret_cast<const u4*>(a.V_codes + slot_of(page_of(j0 + 4 * v_quad), j0 + 4 * v_quad) * (16 * BITS) + v_octet * (4 * BITS));
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) {
+            const u4 x = kp[i], y = vp[i];
+            kraw[4 * i] = x.x; kraw[4 * i + 1] = x.y; kraw[4 * i + 2] = x.z; kraw[4 * i + 3] = x.w;
+            vraw[4 * i] = y.x; vraw[4 * i + 1] = y.y; vraw[4 * i + 2] = y.z; vraw[4 * i + 3] = y.w;
+        }
+        if (wave < 2) {
+            const int j = j0 + lane;
+            const int page = page_of(j);
+            s_there = page >= 0;
+            sraw = (wave == 0 ? a.K_scale : a.V_scale)[slot_of(page, j)];
+        }
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Frag f;
+            f.v = key_operand<BITS>(kraw + i * (BITS / 4));
+            k_sh[buf][k_token * 16 + ((4 * k_part + i) ^ (k_token & 7))] = u4{f.w[0], f.w[1], f.w[2], f.w[3]};
+        }
+        const int chunk = 2 * (v_quad >> 2) + (v_quad & 1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u2* p = reinterpret_cast<u2*>(&v_sh[buf][(8 * v_octet + j) * 8 + (chunk ^ ((j ^ v_octet) & 7))]);
+            p[(v_quad >> 1) & 1] = value_quad<BITS>(vraw, j);
+        }
+        const float s = __half2float(__ushort_as_half(sraw));
+        float* f = reinterpret_cast<float*>(f_sh[buf]);
+        if (wave == 0) {
+            f[lane] = s_there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;    // NaN where s is not finite
+        } else if (wave == 1) {
+            const float vs = s == 0.0f ? 0x1p-24f : s;
+            f[kTileTokens + lane] = s_there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
+            f[2 * kTileTokens + lane] = s_there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
+        }
+    };
+
+    float M[R], l_sum[R];
+    f16v o[R][4];
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+        M[x] = kNone;
+        l_sum[x] = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[x][m] = f16v{};
+    }
+
+    if (steps > 0) {
+        fetch(0);
+        stage(0);
+        if (steps > 1) fetch(1);
+    }
+    __syncthreads();
+    for (int st = 0; st < steps; ++st) {
+        const int buf = st & 1;
+        const int j0 = (step0 + st) * kTileTokens + span.base;     // position of the first token
+        if (st + 1 < steps) {
+            stage(buf ^ 1);
+            if (st + 2 < steps) fetch(st + 2);
+        }
+        const int last = j0 + kTileTokens - 1;
+        // does any row of the wave see any of the tokens; does every row see all of them
+        bool some = wave_any, whole = true;
+        if (a.causal) {
+            some = some && j0 < max(pmax + 1, bmax);
+            whole = whole && (last <= pmin || last < bmin);
+        }
+        if (a.window > 0) {
+            some = some && static_cast<long long>(last) > static_cast<long long>(pmin) - a.window && static_cast<long long>(j0) < static_cast<long long>(pmax) + a.window;
+            whole = whole && static_cast<long long>(pmax) - j0 < a.window && static_cast<long long>(last) - pmin < a.window;
+        }
+        if (some) {
+            h8 w[R][4];
+            float tt[R][2][16];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                f16v s[R];
+#pragma unroll
+                for (int x = 0; x < R; ++x) s[x] = f16v{};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int token = 32 * mt + n;
+                    Frag f;
+                    const u4 y = k_sh[buf][token * 16 + ((2 * k + hf) ^ (token & 7))];
+                    f.w[0] = y.x; f.w[1] = y.y; f.w[2] = y.z; f.w[3] = y.w;
+#pragma unroll
+                    for (int x = 0; x < R; ++x) s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.v, q[x][k], s[x], 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f4 kf = f_sh[buf][0][8 * mt + 2 * i + hf], vl = f_sh[buf][1][8 * mt + 2 * i + hf];
+#pragma unroll
+                    for (int x = 0; x < R; ++x) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            float z = s[x][4 * i + r];
+                            if (capped) {
+                                z = tanh_fast(z * kf[r]) * to_log2 + vl[r];
+                            } else {
+                                z = __builtin_fmaf(z, kf[r], vl[r]);
+                            }
+                            if (FANCY) z = __builtin_fmaf(-slope[x], __builtin_fabsf(static_cast<float>(pos[x] - (j0 + 32 * mt + 8 * i + 4 * hf + r))), z);
+                            tt[x][mt][4 * i + r] = z;
+                        }
+                    }
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int j = j0 + 32 * (e >> 4) + 8 * ((e >> 2) & 3) + 4 * hf + (e & 3);
+                        const int dist = pos[x] - j;
+                        bool seen = true;
+                        if (a.causal) seen = dist >= 0 || j < both[x];
+                        if (a.window > 0) seen = seen && abs(dist) < a.window;
+                        tt[x][e >> 4][e & 15] = seen ? tt[x][e >> 4][e & 15] : -__builtin_inff();
+                    }
+                }
+            }
+            bool grew = false;
+            float top[R];
+#pragma unroll
+            for (int x = 0; x < R; ++x) {
+                top[x] = kNone;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top[x] = __builtin_fmaxf(top[x], tt[x][e >> 4][e & 15]);
+                top[x] = swap_halves_max(top[x]);
+                grew = grew || top[x] > M[x] + kSlack;
+            }
+            if (__ballot(grew) != 0) {
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+                    const float M_new = __builtin_fmaxf(M[x], top[x]);
+                    const float keep = __builtin_amdgcn_exp2f(M[x] - M_new);
+                    M[x] = M_new;
+                    l_sum[x] *= keep;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) o[x][m] *= keep;
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f4 rv = f_sh[buf][2][8 * mt + 2 * i + hf];
+#pragma unroll
+                    for (int x = 0; x < R; ++x) {
+                        float e[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            e[r] = __builtin_amdgcn_exp2f(tt[x][mt][4 * i + r] - M[x]);
+                            l_sum[x] = __builtin_fmaf(e[r], rv[r], l_sum[x]);
+                        }
+                        const h2 p0 = __builtin_convertvector((f2{e[0], e[1]}), h2), p1 = __builtin_convertvector((f2{e[2], e[3]}), h2);
+                        h8& d = w[x][2 * mt + (i >> 1)];
+                        d[4 * (i & 1)] = p0.x;
+                        d[4 * (i & 1) + 1] = p0.y;
+                        d[4 * (i & 1) + 2] = p1.x;
+                        d[4 * (i & 1) + 3] = p1.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int d = 32 * m + n;
+                    Frag f;
+                    const u4 y = v_sh[buf][d * 8 + ((2 * kk + hf) ^ ((d ^ (d >> 3)) & 7))];
+                    f.w[0] = y.x; f.w[1] = y.y; f.w[2] = y.z; f.w[3] = y.w;
+#pragma unroll
+                    for (int x = 0; x < R; ++x) o[x][m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.v, w[x][kk], o[x][m], 0, 0, 0);
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+        const float l = swap_halves_sum(l_sum[x]);
+        if (!valid[x]) continue;
+        const long long at = static_cast<long long>(t[x]) * a.Hq + head[x];
+        if (total_splits == 1) {
+            const float rl = l == 0.0f ? 0.0f : 1.0f / l;
+            uint16_t* out = a.O + at * 128 + 4 * hf;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f16v& v = o[x][m];
+                    const h2 p0 = __builtin_convertvector((f2{v[4 * i] * rl, v[4 * i + 1] * rl}), h2);
+                    const h2 p1 = __builtin_convertvector((f2{v[4 * i + 2] * rl, v[4 * i + 3] * rl}), h2);
+                    *reinterpret_cast<u2*>(out + 32 * m + 8 * i) = u2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
+                }
+            }
+        } else {
+            float* p = a.partial + ((first_slot + split) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
+            if (l != 0.0f) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f2* dst = reinterpret_cast<f2*>(p + 32 * m + 8 * i + 4 * hf);
+                        const f16v& v = o[x][m];
+                        dst[0] = f2{v[4 * i], v[4 * i + 1]};
+                        dst[1] = f2{v[4 * i + 2], v[4 * i + 3]};
+                    }
+                }
+            }
+            if (hf == 0) *reinterpret_cast<f2*>(p + 128) = f2{l == 0.0f ? -__builtin_inff() : M[x], l};
+        }
+    }
+}
+
 // Joins the shares of a row: one wave a row, two values a lane.
 __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int splits) {
     const long long rows = static_cast<long long>(a.T) * a.Hq;
@@ -380,22 +794,26 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int s
     reinterpret_cast<h2*>(a.O)[at * 64 + lane] = res;
 }
 
-// Grid of a call: row tiles and the shares their tokens are split into.
+// Grid of a call: rows of a tile, tiles, and the shares their tokens are split into.
 struct Plan {
+    int rows;                      // 16: kv_attn_rows16; 128, 256: kv_attn_tile
     long long prefix_tiles, own_tiles;
     int prefix_splits, own_splits;
     size_t workspace;
 };
 
 Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
-    constexpr long long kWanted = 2048;    // workgroups that fill the card
     const long long G = Hq / Hkv;
     Plan p = {};
-    p.own_tiles = T * G / kRows + B;
-    p.prefix_tiles = prefix_len > 0 ? (T * G + kRows - 1) / kRows : 0;
+    // rows that read the same tokens: of a sequence on average, of all sequences in a shared prefix
+    const long long together = prefix_len > 0 ? T * G : T * G / B;
+    p.rows = together >= kWideRows ? 256 : together >= kManyRows ? 128 : kRows;
+    const long long wanted = p.rows == kRows ? 2048 : 512;      // workgroups that fill the card
+    p.own_tiles = T * G / p.rows + B;
+    p.prefix_tiles = prefix_len > 0 ? (T * G + p.rows - 1) / p.rows : 0;
     auto shares = [&](long long tiles, int tokens) {
         const long long most = (tokens + kSplitMinTokens - 1) / kSplitMinTokens;
-        const long long want = (kWanted + tiles * Hkv - 1) / (tiles * Hkv);
+        const long long want = (wanted + tiles * Hkv - 1) / (tiles * Hkv);
         return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
     };
     p.own_splits = shares(p.own_tiles, max_kv);
@@ -403,6 +821,24 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const int all = p.own_splits + p.prefix_splits;
     p.workspace = all > 1 ? static_cast<size_t>(all) * T * Hq * kPartial * sizeof(float) : 0;
     return p;
+}
+
+template <int BITS, int R>
+void launch_tile(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(items * a.Hkv));
+    const int pt = static_cast<int>(p.prefix_tiles), ot = static_cast<int>(p.own_tiles);
+    if (a.softcap > 0.0f || a.slopes)
+        hipLaunchKernelGGL((kv_attn_tile<BITS, R, true>), grid, dim3(kAttnThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+    else
+        hipLaunchKernelGGL((kv_attn_tile<BITS, R, false>), grid, dim3(kAttnThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+}
+
+template <int BITS>
+void launch_rows(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
+    if (p.rows == 256) return launch_tile<BITS, 2>(a, p, items, s);
+    if (p.rows == 128) return launch_tile<BITS, 1>(a, p, items, s);
+    hipLaunchKernelGGL(kv_attn_rows16<BITS>, dim3(static_cast<unsigned>(items), a.Hkv), dim3(kAttnThreads), 0, s, a,
+                       static_cast<int>(p.prefix_tiles), p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
 }
 
 }  // namespace
@@ -414,19 +850,14 @@ size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_l
 bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const Plan p = plan(T, Hq, Hkv, B, max_kv, prefix_len);
     constexpr long long kMost = (1LL << 24) - 1;   // workgroups of 256 in a launch dimension
-    return p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits <= kMost && Hkv <= 65535 &&
+    return (p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits) * Hkv <= kMost && Hkv <= 65535 &&
            (static_cast<long long>(T) * Hq + kAttnWaves - 1) / kAttnWaves <= kMost;
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s) {
     const Plan p = plan(a.T, a.Hq, a.Hkv, a.B, a.max_pages << a.page_log2, a.prefix_len);
-    const dim3 grid(static_cast<unsigned>(p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits), a.Hkv);
-    if (bits == 8)
-        hipLaunchKernelGGL(kv_attn_rows16<8>, grid, dim3(kAttnThreads), 0, s, a, static_cast<int>(p.prefix_tiles),
-                           p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
-    else
-        hipLaunchKernelGGL(kv_attn_rows16<4>, grid, dim3(kAttnThreads), 0, s, a, static_cast<int>(p.prefix_tiles),
-                           p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
+    const long long items = p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits;
+    bits == 8 ? launch_rows<8>(a, p, items, s) : launch_rows<4>(a, p, items, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.own_splits + p.prefix_splits == 1) return e;
     const long long rows = static_cast<long long>(a.T) * a.Hq;
