@@ -359,7 +359,6 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int kTileTokens = 64;            // tokens staged at a time
-constexpr float kNone = -1e30f;            // "no token yet": below every score, and finite
 constexpr float kSlack = 8.0f;             // a row's maximum may lag by this many powers of two
 
 // Four tokens' code j of an octet (w: BITS / 4 dwords a token) as fp16.
@@ -386,20 +385,28 @@ __device__ __forceinline__ float swap_halves_sum(float v) {
     return __uint_as_float(s.x) + __uint_as_float(s.y);
 }
 
-// The same for tiles of 128 R rows (R = 1, 2): four waves of 32 R rows share 64
-// tokens at a time, which the workgroup turns into fp16 codes in LDS once,
-// keys as [token][d] and values as [d][token], while it computes on the 64
-// before (two buffers, one barrier a step).
-template <int BITS, int R, bool FANCY>
-__global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
-                                                                            int own_tiles, int own_splits) {
-    constexpr int kTileRows = 128 * R;
-    __shared__ u4 k_sh[2][kTileTokens * 16];       // 16 chunks of 8 values a token, chunk c at c ^ (token & 7)
-    __shared__ u4 v_sh[2][128 * 8];                // 8 chunks of 8 tokens a value, chunk c at c ^ ((d ^ d / 8) & 7)
-    __shared__ f4 f_sh[2][3][kTileTokens / 4];     // per token: key factor, log2 of the value scale, its reciprocal
-    __shared__ int range_sh[kAttnWaves][3];
+template <int N>
+__device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes of a row, for all of them
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
+}
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The same for tiles of 32 WAVES rows, 32 a wave.  The waves share 64 tokens at
+// a time, which the workgroup turns into fp16 codes in LDS once, keys as
+// [token][d] and values as [d][token].  A wave takes 32 tokens at a time, and
+// computes the scores of the next 32 before it turns to the weights of these,
+// so that the matrix cores have work while the exponentials are computed.
+template <int BITS, int WAVES, bool FANCY>
+__global__ __launch_bounds__(64 * WAVES, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
+                                                              int own_tiles, int own_splits) {
+    constexpr int kTileRows = 32 * WAVES;
+    // Rows of one chunk more than they hold, so that eight rows' same chunk lies in different banks and every address
+    // is a base and a constant.  Value d is row 16 (d % 8) + d / 8.
+    __shared__ u4 k_sh[2][kTileTokens * 17];       // 16 chunks of 8 values a token
+    __shared__ u4 v_sh[2][128 * 9];                // 8 chunks of 8 tokens a value
+    __shared__ f4 f_sh[2][3][kTileTokens / 4];     // per token: key factor, log2 of the value scale, its reciprocal
+    __shared__ int range_sh[WAVES][3];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const int G = a.Hq / a.Hkv;
     // key heads alternate fastest: with 8 of them a head stays on one XCD; late tiles, the long ones, come first
@@ -414,26 +421,22 @@ __global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvA
     const int total_splits = prefix_splits + own_splits;
 
     Span span;
-    int t[R], head[R], pos[R], both[R];
-    bool valid[R];
-    bool any = false;
+    int t, head, pos = 0, both = 0;
+    bool valid;
     if (shared) {
         span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
-#pragma unroll
-        for (int x = 0; x < R; ++x) {
-            const long long r = static_cast<long long>(tile) * kTileRows + wave * 32 * R + x * 32 + n;
-            const long long tt = r / G;
-            t[x] = static_cast<int>(tt);
-            head[x] = h * G + static_cast<int>(r - tt * G);
-            const int b = tt < a.T ? find_sequence(a.q_start, a.B, t[x]) : -1;
-            valid[x] = b >= 0;
-            pos[x] = both[x] = 0;
-            if (valid[x]) {
-                pos[x] = a.prefix_len + context(a, b) - a.q_start[b + 1] + t[x];
-                if (a.bidir_len) both[x] = a.bidir_len[b];
-            }
+        const long long r = static_cast<long long>(tile) * kTileRows + wave * 32 + n;
+        const long long tt = r / G;
+        t = static_cast<int>(tt);
+        head = h * G + static_cast<int>(r - tt * G);
+        const int b = tt < a.T ? find_sequence(a.q_start, a.B, t) : -1;
+        valid = b >= 0;
+        if (valid) {
+            pos = a.prefix_len + context(a, b) - a.q_start[b + 1] + t;
+            if (a.bidir_len) both = a.bidir_len[b];
         }
     } else {
+        // sequence b's tiles start at tile floor(q_start[b] G / rows) + b: room for each one's ragged last tile
         int lo = 0, c = a.B;
         while (c > 1) {
             const int half = c >> 1;
@@ -446,27 +449,19 @@ __global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvA
         const long long first = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / kTileRows + b)) * kTileRows;
         const long long rows = static_cast<long long>(q1 - q0) * G;
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
-#pragma unroll
-        for (int x = 0; x < R; ++x) {
-            const long long r = first + wave * 32 * R + x * 32 + n;
-            valid[x] = r >= 0 && r < rows;
-            const int i = valid[x] ? static_cast<int>(r / G) : 0;
-            t[x] = q0 + i;
-            head[x] = h * G + (valid[x] ? static_cast<int>(r - static_cast<long long>(i) * G) : 0);
-            pos[x] = valid[x] ? a.prefix_len + span.tokens - a.q_start[b + 1] + t[x] : 0;
-            both[x] = valid[x] && a.bidir_len ? a.bidir_len[b] : 0;
+        const long long r = first + wave * 32 + n;
+        valid = r >= 0 && r < rows;
+        const int i = valid ? static_cast<int>(r / G) : 0;
+        t = q0 + i;
+        head = h * G + (valid ? static_cast<int>(r - static_cast<long long>(i) * G) : 0);
+        if (valid) {
+            pos = a.prefix_len + span.tokens - a.q_start[b + 1] + t;
+            if (a.bidir_len) both = a.bidir_len[b];
         }
     }
     // positions of the wave's rows, then of the workgroup's: which tokens any of them sees
-    int pmin = 0x7FFFFFFF, pmax = -0x7FFFFFFF, bmax = -0x7FFFFFFF, bmin = 0x7FFFFFFF;
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-        any = any || valid[x];
-        pmin = min(pmin, valid[x] ? pos[x] : pmin);
-        pmax = max(pmax, valid[x] ? pos[x] : pmax);
-        bmax = max(bmax, valid[x] ? both[x] : bmax);
-        bmin = min(bmin, valid[x] ? both[x] : bmin);
-    }
+    int pmin = valid ? pos : 0x7FFFFFFF, pmax = valid ? pos : -0x7FFFFFFF;
+    int bmin = valid ? both : 0x7FFFFFFF, bmax = valid ? both : -0x7FFFFFFF;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         pmin = min(pmin, __shfl_xor(pmin, m, 64));
@@ -478,7 +473,7 @@ __global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvA
     pmax = __builtin_amdgcn_readfirstlane(pmax);
     bmax = __builtin_amdgcn_readfirstlane(bmax);
     bmin = __builtin_amdgcn_readfirstlane(bmin);
-    const bool wave_any = __ballot(any) != 0;
+    const bool wave_any = __ballot(valid) != 0;
     if (lane == 0) {
         range_sh[wave][0] = pmin;
         range_sh[wave][1] = pmax;
@@ -489,7 +484,7 @@ __global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvA
     {
         int gmin = range_sh[0][0], gmax = range_sh[0][1], gend = range_sh[0][2];
 #pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w) {
+        for (int w = 1; w < WAVES; ++w) {
             gmin = min(gmin, range_sh[w][0]);
             gmax = max(gmax, range_sh[w][1]);
             gend = max(gend, range_sh[w][2]);
@@ -506,264 +501,320 @@ __global__ __launch_bounds__(kAttnThreads, R == 1 ? 2 : 1) void kv_attn_tile(KvA
     int step0 = lo / kTileTokens;
     const int steps_all = hi > lo ? (hi + kTileTokens - 1) / kTileTokens - step0 : 0;
     const int share = max((steps_all + splits - 1) / splits, kSplitMinTokens / kTileTokens);
-    step0 += split * share;
-    const int steps = max(0, min(share, steps_all - split * share));
+    const int steps = __builtin_amdgcn_readfirstlane(max(0, min(share, steps_all - split * share)));
+    step0 = __builtin_amdgcn_readfirstlane(step0 + split * share);
 
     // queries: lane (n, hf) holds values 16 k + 8 hf .. + 7 of its row, k = 0 .. 7, in the order of the keys' codes
-    h8 q[R][8];
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-        const uint16_t* src = a.Q + (static_cast<long long>(t[x]) * a.Hq + head[x]) * 128 + 8 * hf;
+    h8 q[8];
+    {
+        const uint16_t* src = a.Q + (static_cast<long long>(t) * a.Hq + head) * 128 + 8 * hf;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             Frag raw, f;
-            const u4 y = valid[x] ? *reinterpret_cast<const u4*>(src + 16 * k) : u4{0, 0, 0, 0};
+            const u4 y = valid ? *reinterpret_cast<const u4*>(src + 16 * k) : u4{0, 0, 0, 0};
             raw.w[0] = y.x; raw.w[1] = y.y; raw.w[2] = y.z; raw.w[3] = y.w;
 #pragma unroll
             for (int i = 0; i < 8; ++i) f.v[i] = raw.v[order8<BITS>(i)];
-            q[x][k] = f.v;
+            q[k] = f.v;
         }
     }
-    float slope[R];
-#pragma unroll
-    for (int x = 0; x < R; ++x) slope[x] = FANCY && a.slopes && valid[x] ? a.slopes[head[x]] * kLog2e : 0.0f;
+    const int at_row = valid ? t * a.Hq + head : -1;       // T * Hq is below 2^26
+    const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
     const bool capped = FANCY && a.softcap > 0.0f;
     const float key_factor = capped ? a.scale / a.softcap : a.scale * kLog2e;
     const float to_log2 = a.softcap * kLog2e;
 
-    // what this thread stages of a step: 32 codes of one token's key, one octet of four tokens' values, one scale
+    // What a wave stages of a step: 16 tokens (a quarter, so that they lie in one page), their keys and key scales
+    // (the upper half of 8 waves, or every one of 4), their values and value scales (the lower half, or every one).
+    // Codes are loaded two steps ahead, the page's number three.
+    const bool keys = WAVES == 4 || wave >= 4, values = WAVES == 4 || wave < 4;
+    const int quarter = 16 * (wave & 3);
+    // Lanes are dealt out so that eight (16) of them write to different banks: eight tokens' same chunk of a key,
+    // eight octets of the two quads that share a chunk of the values.
+    const int k_own = (lane & 7) + 8 * (lane >> 5), k_part = (lane >> 3) & 3, k_token = quarter + k_own;
+    const int v_own = ((lane >> 3) & 1) * 2 + ((lane >> 4) & 1), v_octet = (lane & 7) + 8 * (lane >> 5);
+    const int v_quad = (wave & 3) * 4 + v_own;
+    const int k_unit = k_own * 4 + k_part, v_unit = v_own * 16 + v_octet;      // of the 64 units of 4 BITS bytes
     uint32_t kraw[BITS], vraw[BITS];
-    uint16_t sraw = 0;
-    bool s_there = false;
-    const int k_token = threadIdx.x >> 2, k_part = threadIdx.x & 3;
-    const int v_quad = threadIdx.x >> 4, v_octet = threadIdx.x & 15;
-    auto page_of = [&](int j) {     // page of token j, -1 if it has none
-        if (j >= span.tokens) return -1;
-        const int p = span.table[min(j >> a.page_log2, span.n_table - 1)];
-        return p >= 0 && p < a.n_pages ? p : -1;
+    uint32_t sraw = 0;
+    bool there = false;
+    int pages = -1;
+    auto load_pages = [&](int st) __attribute__((always_inline)) {      // of the wave's tokens in steps st .. st + 63
+        const long long j = static_cast<long long>(step0 + st + lane) * kTileTokens + quarter;
+        pages = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
     };
-    auto slot_of = [&](int page, int j) {
-        return ((static_cast<long long>(max(page, 0)) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
-    };
-    auto fetch = [&](int st) {
-        const int j0 = (step0 + st) * kTileTokens;
-        const u4* kp = reinterpret_cast<const u4*>(a.K_codes + slot_of(page_of(j0 + k_token), j0 + k_token) * (16 * BITS) + k_part * (4 * BITS));
-        const u4* vp = reinterpret_cast<const u4*>(a.V_codes + slot_of(page_of(j0 + 4 * v_quad), j0 + 4 * v_quad) * (16 * BITS) + v_octet * (4 * BITS));
+    auto fetch = [&](int st) __attribute__((always_inline)) {
+        const int page = __builtin_amdgcn_readlane(pages, st & 63);
+        const int j = (step0 + st) * kTileTokens + quarter;
+        const bool good = page >= 0 && page < a.n_pages;
+        const long long token = ((static_cast<long long>(good ? page : 0) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+        if (keys) {
+            const u4* kp = reinterpret_cast<const u4*>(a.K_codes + token * (16 * BITS));
 #pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) {
-            const u4 x = kp[i], y = vp[i];
-            kraw[4 * i] = x.x; kraw[4 * i + 1] = x.y; kraw[4 * i + 2] = x.z; kraw[4 * i + 3] = x.w;
-            vraw[4 * i] = y.x; vraw[4 * i + 1] = y.y; vraw[4 * i + 2] = y.z; vraw[4 * i + 3] = y.w;
+            for (int i = 0; i < BITS / 4; ++i) {
+                const u4 y = kp[k_unit * (BITS / 4) + i];
+                kraw[4 * i] = y.x; kraw[4 * i + 1] = y.y; kraw[4 * i + 2] = y.z; kraw[4 * i + 3] = y.w;
+            }
         }
-        if (wave < 2) {
-            const int j = j0 + lane;
-            const int page = page_of(j);
-            s_there = page >= 0;
-            sraw = (wave == 0 ? a.K_scale : a.V_scale)[slot_of(page, j)];
+        if (values) {
+            const u4* vp = reinterpret_cast<const u4*>(a.V_codes + token * (16 * BITS));
+#pragma unroll
+            for (int i = 0; i < BITS / 4; ++i) {
+                const u4 y = vp[v_unit * (BITS / 4) + i];
+                vraw[4 * i] = y.x; vraw[4 * i + 1] = y.y; vraw[4 * i + 2] = y.z; vraw[4 * i + 3] = y.w;
+            }
+        }
+        // lanes 0 .. 15 the key scales, 16 .. 31 the value scales
+        if (WAVES == 4)
+            sraw = ((lane & 16) == 0 ? a.K_scale : a.V_scale)[token + (lane & 15)];
+        else
+            sraw = ((wave >= 4 ? a.K_scale : a.V_scale) + token)[lane & 15];
+        there = good && j + (lane & 15) < span.tokens;
+    };
+    auto stage = [&](int buf) __attribute__((always_inline)) {
+        if (keys) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Frag f;
+                f.v = key_operand<BITS>(kraw + i * (BITS / 4));
+                k_sh[buf][k_token * 17 + 4 * k_part + i] = u4{f.w[0], f.w[1], f.w[2], f.w[3]};
+            }
+        }
+        if (values) {
+            const int chunk = 2 * (v_quad >> 2) + (v_quad & 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                u2* p = reinterpret_cast<u2*>(&v_sh[buf][(16 * j + v_octet) * 9 + chunk]);
+                p[(v_quad >> 1) & 1] = value_quad<BITS>(vraw, j);
+            }
+        }
+        const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sraw)));
+        float* f = reinterpret_cast<float*>(f_sh[buf]) + quarter + (lane & 15);
+        if (keys && lane < 16) f[0] = there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;    // NaN where s is not finite
+        if (values && (WAVES == 4 ? lane >= 16 && lane < 32 : lane < 16)) {
+            // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
+            const float vs = s == 0.0f ? 0x1p-24f : s;
+            f[kTileTokens] = there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
+            f[2 * kTileTokens] = there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
         }
     };
-    auto stage = [&](int buf) {
+
+    // M: what a row's exponents are relative to.  It follows the row's maximum by more than kSlack powers of two, up, and
+    // is set to it with the row's first token (`low` is infinite until then).
+    float M = 0.0f, low = __builtin_inff(), l_sum = 0.0f;
+    f16v o[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) o[m] = f16v{};
+
+    f16v s;            // products of 32 tokens with their codes, then their exponents
+    h8 w[2];           // their weights
+    u4 kc[8];          // keys of the 32 tokens behind them
+    f4 kf[4], rv[4];   // factors of the tokens: key, reciprocal value scale,
+    float lv;          // log2 of the value scale, lane c of 16 for the lane's token c
+
+    // does any row of the wave see any token of a step; does every row see all of them
+    auto seen_some = [&](int j0) __attribute__((always_inline)) {
+        bool some = wave_any;
+        const int last = j0 + kTileTokens - 1;
+        if (a.causal) some = some && j0 < max(pmax + 1, bmax);
+        if (a.window > 0)
+            some = some && static_cast<long long>(last) > static_cast<long long>(pmin) - a.window &&
+                   static_cast<long long>(j0) < static_cast<long long>(pmax) + a.window;
+        return some;
+    };
+    auto seen_whole = [&](int j0) __attribute__((always_inline)) {
+        bool whole = true;
+        const int last = j0 + kTileTokens - 1;
+        if (a.causal) whole = last <= pmin || last < bmin;
+        if (a.window > 0) whole = whole && static_cast<long long>(pmax) - j0 < a.window && static_cast<long long>(last) - pmin < a.window;
+        return whole;
+    };
+    auto key_chunk = [&](int buf, int sub, int k) __attribute__((always_inline)) {
+        const int token = 32 * sub + n;
+        return k_sh[buf][token * 17 + 2 * k + hf];
+    };
+    auto value_chunk = [&](int buf, int sub, int i) __attribute__((always_inline)) {      // i = 4 kk + m
+        return v_sh[buf][(32 * (i & 3) + n) * 9 + 4 * sub + 2 * (i >> 2) + hf];
+    };
+    auto load_factors = [&](int buf, int sub) __attribute__((always_inline)) {
+        lv = reinterpret_cast<const float*>(f_sh[buf][1])[32 * sub + 8 * ((lane & 15) >> 2) + 4 * hf + (lane & 3)];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            Frag f;
-            f.v = key_operand<BITS>(kraw + i * (BITS / 4));
-            k_sh[buf][k_token * 16 + ((4 * k_part + i) ^ (k_token & 7))] = u4{f.w[0], f.w[1], f.w[2], f.w[3]};
+            kf[i] = f_sh[buf][0][8 * sub + 2 * i + hf];
+            rv[i] = f_sh[buf][2][8 * sub + 2 * i + hf];
         }
-        const int chunk = 2 * (v_quad >> 2) + (v_quad & 1);
+    };
+    // products to exponents of the tokens at positions j0 .. j0 + 31, relative to M
+    auto exponents = [&](int j0) __attribute__((always_inline)) {
+        auto one = [&](int e, float lm) __attribute__((always_inline)) {
+            if (FANCY) {
+                float z = s[e] * kf[e >> 2][e & 3];
+                if (capped) z = tanh_fast(z) * to_log2;
+                z = __builtin_fmaf(-slope, __builtin_fabsf(static_cast<float>(pos - (j0 + 8 * (e >> 2) + 4 * hf + (e & 3)))), z);
+                s[e] = z + lm;
+            } else {
+                s[e] = __builtin_fmaf(s[e], kf[e >> 2][e & 3], lm);
+            }
+        };
+#define SPIN_ONE(N) one(N, row_lane<N>(lv) - M);
+        SPIN_ONE(0) SPIN_ONE(1) SPIN_ONE(2) SPIN_ONE(3) SPIN_ONE(4) SPIN_ONE(5) SPIN_ONE(6) SPIN_ONE(7)
+        SPIN_ONE(8) SPIN_ONE(9) SPIN_ONE(10) SPIN_ONE(11) SPIN_ONE(12) SPIN_ONE(13) SPIN_ONE(14) SPIN_ONE(15)
+#undef SPIN_ONE
+    };
+    auto mask = [&](int j0) __attribute__((always_inline)) {
+        // token c of the lane's half (c = 8 i + r): the row's last token in order, and its window, counted from there
+        const int rel = pos - j0 - 4 * hf;
+        const int end = a.causal ? max(rel, both - j0 - 4 * hf - 1) : 32;
+        const int off = a.window > 0 ? rel + a.window - 1 : 32;
+        const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            u2* p = reinterpret_cast<u2*>(&v_sh[buf][(8 * v_octet + j) * 8 + (chunk ^ ((j ^ v_octet) & 7))]);
-            p[(v_quad >> 1) & 1] = value_quad<BITS>(vraw, j);
+        for (int e = 0; e < 16; ++e) {
+            const int c = 8 * (e >> 2) + (e & 3);
+            const bool seen = (end >= c) & (static_cast<uint32_t>(off - c) < wide);
+            s[e] = seen ? s[e] : -__builtin_inff();
         }
-        const float s = __half2float(__ushort_as_half(sraw));
-        float* f = reinterpret_cast<float*>(f_sh[buf]);
-        if (wave == 0) {
-            f[lane] = s_there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;    // NaN where s is not finite
-        } else if (wave == 1) {
-            const float vs = s == 0.0f ? 0x1p-24f : s;
-            f[kTileTokens + lane] = s_there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
-            f[2 * kTileTokens + lane] = s_there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
+    };
+    // masks the exponents, and moves M where it has to
+    auto settle = [&](int j0, bool whole) __attribute__((always_inline)) {
+        if (!whole) {
+            asm volatile("" ::: "memory");     // keeps this a branch: the selects are not worth it elsewhere
+            mask(j0);
+        }
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = __builtin_fmaxf(top, s[e]);
+        top = swap_halves_max(top);
+        if (__ballot(top > kSlack || top < low) != 0) {
+            const bool none = top == -__builtin_inff(), first = low > 0.0f;
+            const float up = none ? 0.0f : first ? top : __builtin_fmaxf(top, 0.0f);
+            const float keep = first ? 0.0f : __builtin_amdgcn_exp2f(-up);     // nothing is kept of nothing, whatever up is
+            low = none ? low : -__builtin_inff();
+            M += up;
+            l_sum *= keep;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) o[m] *= keep;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] -= up;
+        }
+    };
+    // Vector work on 32 tokens at positions j0 ..: their exponents, M, their weights
+    auto vector_part = [&](int j0, bool whole) __attribute__((always_inline)) {
+        exponents(j0);
+        settle(j0, whole);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float e[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                e[r] = __builtin_amdgcn_exp2f(s[4 * i + r]);
+                l_sum = __builtin_fmaf(e[r], rv[i][r], l_sum);
+            }
+            const h2 p0 = __builtin_convertvector((f2{e[0], e[1]}), h2), p1 = __builtin_convertvector((f2{e[2], e[3]}), h2);
+            h8& d = w[i >> 1];
+            d[4 * (i & 1)] = p0.x;
+            d[4 * (i & 1) + 1] = p0.y;
+            d[4 * (i & 1) + 2] = p1.x;
+            d[4 * (i & 1) + 3] = p1.y;
+        }
+    };
+    auto load_keys = [&](int buf, int sub) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) kc[k] = key_chunk(buf, sub, k);
+    };
+    auto next_products = [&]() __attribute__((always_inline)) {
+        s = f16v{};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kc[k]), q[k], s, 0, 0, 0);
+    };
+    // Matrix work: the products of the next 32 tokens, and these 32 tokens' (buf, sub) weighted values
+    auto matrix_part = [&](int buf, int sub, int next_buf, int next_sub, bool some) __attribute__((always_inline)) {
+        u4 vc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vc[i] = value_chunk(buf, sub, i);
+        load_factors(next_buf, next_sub);
+        next_products();
+        if (some) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, vc[i]), w[i >> 2], o[i & 3], 0, 0, 0);
         }
     };
 
-    float M[R], l_sum[R];
-    f16v o[R][4];
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-        M[x] = kNone;
-        l_sum[x] = 0.0f;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) o[x][m] = f16v{};
-    }
-
     if (steps > 0) {
+        load_pages(0);
         fetch(0);
         stage(0);
         if (steps > 1) fetch(1);
     }
     __syncthreads();
+    const int base = step0 * kTileTokens + span.base;
+    if (steps > 0) {
+        load_keys(0, 0);
+        load_factors(0, 0);
+        next_products();
+    }
+    // Two waves share a SIMD, one of each half of the workgroup.  The upper half runs a part behind the lower one, so
+    // that of the two waves one has matrix and one has vector work, always:
+    //   lower   V0  M0  V1  M1  V0 ..        V: exponents and weights, M: the two products, of 32 tokens (0, 1)
+    //   upper       V0  M0  V1  M1 ..
+    // The next step's tokens go into the other buffer, which the upper half's M1 reads last, in the time of the lower
+    // half's V0: the upper half writes (keys) in its V0, the lower (values) in its V1, both before the lower half's M1.
+    // Four waves have a SIMD each, run together, and write both in V0.
+    const bool upper = WAVES == 8 && wave >= 4;
+    if (upper) __syncthreads();
     for (int st = 0; st < steps; ++st) {
         const int buf = st & 1;
-        const int j0 = (step0 + st) * kTileTokens + span.base;     // position of the first token
-        if (st + 1 < steps) {
-            stage(buf ^ 1);
-            if (st + 2 < steps) fetch(st + 2);
-        }
-        const int last = j0 + kTileTokens - 1;
-        // does any row of the wave see any of the tokens; does every row see all of them
-        bool some = wave_any, whole = true;
-        if (a.causal) {
-            some = some && j0 < max(pmax + 1, bmax);
-            whole = whole && (last <= pmin || last < bmin);
-        }
-        if (a.window > 0) {
-            some = some && static_cast<long long>(last) > static_cast<long long>(pmin) - a.window && static_cast<long long>(j0) < static_cast<long long>(pmax) + a.window;
-            whole = whole && static_cast<long long>(pmax) - j0 < a.window && static_cast<long long>(last) - pmin < a.window;
-        }
-        if (some) {
-            h8 w[R][4];
-            float tt[R][2][16];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                f16v s[R];
-#pragma unroll
-                for (int x = 0; x < R; ++x) s[x] = f16v{};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int token = 32 * mt + n;
-                    Frag f;
-                    const u4 y = k_sh[buf][token * 16 + ((2 * k + hf) ^ (token & 7))];
-                    f.w[0] = y.x; f.w[1] = y.y; f.w[2] = y.z; f.w[3] = y.w;
-#pragma unroll
-                    for (int x = 0; x < R; ++x) s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.v, q[x][k], s[x], 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f4 kf = f_sh[buf][0][8 * mt + 2 * i + hf], vl = f_sh[buf][1][8 * mt + 2 * i + hf];
-#pragma unroll
-                    for (int x = 0; x < R; ++x) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            float z = s[x][4 * i + r];
-                            if (capped) {
-                                z = tanh_fast(z * kf[r]) * to_log2 + vl[r];
-                            } else {
-                                z = __builtin_fmaf(z, kf[r], vl[r]);
-                            }
-                            if (FANCY) z = __builtin_fmaf(-slope[x], __builtin_fabsf(static_cast<float>(pos[x] - (j0 + 32 * mt + 8 * i + 4 * hf + r))), z);
-                            tt[x][mt][4 * i + r] = z;
-                        }
-                    }
-                }
+        const int j0 = base + st * kTileTokens;     // position of the first token
+        const bool some = seen_some(j0), whole = seen_whole(j0);
+        const bool more = st + 1 < steps;
+        auto turn = [&]() __attribute__((always_inline)) {
+            if (more) stage(buf ^ 1);
+            if (st + 2 < steps) {
+                if (((st + 2) & 63) == 0) load_pages(st + 2);
+                fetch(st + 2);
             }
-            if (!whole) {
-#pragma unroll
-                for (int x = 0; x < R; ++x) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int j = j0 + 32 * (e >> 4) + 8 * ((e >> 2) & 3) + 4 * hf + (e & 3);
-                        const int dist = pos[x] - j;
-                        bool seen = true;
-                        if (a.causal) seen = dist >= 0 || j < both[x];
-                        if (a.window > 0) seen = seen && abs(dist) < a.window;
-                        tt[x][e >> 4][e & 15] = seen ? tt[x][e >> 4][e & 15] : -__builtin_inff();
-                    }
-                }
-            }
-            bool grew = false;
-            float top[R];
-#pragma unroll
-            for (int x = 0; x < R; ++x) {
-                top[x] = kNone;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) top[x] = __builtin_fmaxf(top[x], tt[x][e >> 4][e & 15]);
-                top[x] = swap_halves_max(top[x]);
-                grew = grew || top[x] > M[x] + kSlack;
-            }
-            if (__ballot(grew) != 0) {
-#pragma unroll
-                for (int x = 0; x < R; ++x) {
-                    const float M_new = __builtin_fmaxf(M[x], top[x]);
-                    const float keep = __builtin_amdgcn_exp2f(M[x] - M_new);
-                    M[x] = M_new;
-                    l_sum[x] *= keep;
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) o[x][m] *= keep;
-                }
-            }
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f4 rv = f_sh[buf][2][8 * mt + 2 * i + hf];
-#pragma unroll
-                    for (int x = 0; x < R; ++x) {
-                        float e[4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            e[r] = __builtin_amdgcn_exp2f(tt[x][mt][4 * i + r] - M[x]);
-                            l_sum[x] = __builtin_fmaf(e[r], rv[r], l_sum[x]);
-                        }
-                        const h2 p0 = __builtin_convertvector((f2{e[0], e[1]}), h2), p1 = __builtin_convertvector((f2{e[2], e[3]}), h2);
-                        h8& d = w[x][2 * mt + (i >> 1)];
-                        d[4 * (i & 1)] = p0.x;
-                        d[4 * (i & 1) + 1] = p0.y;
-                        d[4 * (i & 1) + 2] = p1.x;
-                        d[4 * (i & 1) + 3] = p1.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int d = 32 * m + n;
-                    Frag f;
-                    const u4 y = v_sh[buf][d * 8 + ((2 * kk + hf) ^ ((d ^ (d >> 3)) & 7))];
-                    f.w[0] = y.x; f.w[1] = y.y; f.w[2] = y.z; f.w[3] = y.w;
-#pragma unroll
-                    for (int x = 0; x < R; ++x) o[x][m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.v, w[x][kk], o[x][m], 0, 0, 0);
-                }
-            }
-        }
+        };
+        if (some) vector_part(j0, whole);
+        load_keys(buf, 1);
+        if (WAVES == 4 || upper) turn();
+        __syncthreads();
+        matrix_part(buf, 0, buf, 1, some);
+        __syncthreads();
+        if (some) vector_part(j0 + 32, whole);
+        load_keys(buf ^ 1, 0);      // behind the last step of whatever is there, for nothing
+        if (WAVES == 8 && !upper) turn();
+        __syncthreads();
+        matrix_part(buf, 1, buf ^ 1, 0, some);
         __syncthreads();
     }
+    if (WAVES == 8 && !upper) __syncthreads();
 
+    const float l = swap_halves_sum(l_sum);
+    if (at_row < 0) return;
+    const long long at = at_row;
+    // the lane's values 8 c .. 8 c + 7, c = 8 (i & 1) + 4 hf + r, are rows 16 v + c: register 4 i + r of o[v / 2], i = 2 (v & 1) + (c > 7)
+    float* partial = a.partial + ((first_slot + split) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
+    const float rl = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int x = 0; x < R; ++x) {
-        const float l = swap_halves_sum(l_sum[x]);
-        if (!valid[x]) continue;
-        const long long at = static_cast<long long>(t[x]) * a.Hq + head[x];
-        if (total_splits == 1) {
-            const float rl = l == 0.0f ? 0.0f : 1.0f / l;
-            uint16_t* out = a.O + at * 128 + 4 * hf;
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
+        for (int r = 0; r < 4; ++r) {
+            const int c = 8 * i + 4 * hf + r;
+            float v[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f16v& v = o[x][m];
-                    const h2 p0 = __builtin_convertvector((f2{v[4 * i] * rl, v[4 * i + 1] * rl}), h2);
-                    const h2 p1 = __builtin_convertvector((f2{v[4 * i + 2] * rl, v[4 * i + 3] * rl}), h2);
-                    *reinterpret_cast<u2*>(out + 32 * m + 8 * i) = u2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
-                }
+            for (int e = 0; e < 8; ++e) v[e] = o[e >> 1][4 * (2 * (e & 1) + i) + r];
+            if (total_splits == 1) {
+                Frag f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f.v[e] = static_cast<_Float16>(v[e] * rl);
+                *reinterpret_cast<u4*>(a.O + at * 128 + 8 * c) = u4{f.w[0], f.w[1], f.w[2], f.w[3]};
+            } else if (l != 0.0f) {
+                f2* dst = reinterpret_cast<f2*>(partial + 8 * c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = f2{v[2 * e], v[2 * e + 1]};
             }
-        } else {
-            float* p = a.partial + ((first_slot + split) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
-            if (l != 0.0f) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f2* dst = reinterpret_cast<f2*>(p + 32 * m + 8 * i + 4 * hf);
-                        const f16v& v = o[x][m];
-                        dst[0] = f2{v[4 * i], v[4 * i + 1]};
-                        dst[1] = f2{v[4 * i + 2], v[4 * i + 3]};
-                    }
-                }
-            }
-            if (hf == 0) *reinterpret_cast<f2*>(p + 128) = f2{l == 0.0f ? -__builtin_inff() : M[x], l};
         }
     }
+    if (total_splits > 1 && hf == 0) *reinterpret_cast<f2*>(partial + 128) = f2{l == 0.0f ? -__builtin_inff() : M, l};
 }
 
 // Joins the shares of a row: one wave a row, two values a lane.
@@ -811,7 +862,7 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const long long wanted = p.rows == kRows ? 2048 : 512;      // workgroups that fill the card
     p.own_tiles = T * G / p.rows + B;
     p.prefix_tiles = prefix_len > 0 ? (T * G + p.rows - 1) / p.rows : 0;
-    auto shares = [&](long long tiles, int tokens) {
+    auto shares = [&](long long tiles, int tokens) __attribute__((always_inline)) {
         const long long most = (tokens + kSplitMinTokens - 1) / kSplitMinTokens;
         const long long want = (wanted + tiles * Hkv - 1) / (tiles * Hkv);
         return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
@@ -823,20 +874,20 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     return p;
 }
 
-template <int BITS, int R>
+template <int BITS, int WAVES>
 void launch_tile(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(items * a.Hkv));
     const int pt = static_cast<int>(p.prefix_tiles), ot = static_cast<int>(p.own_tiles);
     if (a.softcap > 0.0f || a.slopes)
-        hipLaunchKernelGGL((kv_attn_tile<BITS, R, true>), grid, dim3(kAttnThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
     else
-        hipLaunchKernelGGL((kv_attn_tile<BITS, R, false>), grid, dim3(kAttnThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
 }
 
 template <int BITS>
 void launch_rows(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
-    if (p.rows == 256) return launch_tile<BITS, 2>(a, p, items, s);
-    if (p.rows == 128) return launch_tile<BITS, 1>(a, p, items, s);
+    if (p.rows == 256) return launch_tile<BITS, 8>(a, p, items, s);
+    if (p.rows == 128) return launch_tile<BITS, 4>(a, p, items, s);
     hipLaunchKernelGGL(kv_attn_rows16<BITS>, dim3(static_cast<unsigned>(items), a.Hkv), dim3(kAttnThreads), 0, s, a,
                        static_cast<int>(p.prefix_tiles), p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
 }
