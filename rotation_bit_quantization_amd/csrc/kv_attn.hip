@@ -40,8 +40,8 @@ constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
 constexpr int kSplitMinTokens = 256;      // fewest tokens worth a workgroup of their own
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kManyRows = 32;             // rows on the same tokens from which tiles of 128, 256 rows are taken
-constexpr int kWideRows = 512;
+constexpr int kTileRows = 256;            // rows of a tile where there are many
+constexpr int kManyRows = 32;             // rows on the same tokens from which those tiles are taken
 constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
 
 union Frag {
@@ -358,22 +358,17 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 
+constexpr int kTileThreads = 512;
+constexpr int kTileWaves = kTileThreads / 64;
 constexpr int kTileTokens = 64;            // tokens staged at a time
 constexpr float kSlack = 8.0f;             // a row's maximum may lag by this many powers of two
 
-// Four tokens' code j of an octet (w: BITS / 4 dwords a token) as fp16.
+// Two tokens' code j of an octet (w: BITS / 4 dwords a token) as fp16.
 template <int BITS>
-__device__ __forceinline__ u2 value_quad(const uint32_t* w, int j) {
-    constexpr int kW = BITS / 4;
+__device__ __forceinline__ uint32_t value_pair(const uint32_t* w, int j) {
     const int byte = BITS == 4 ? j >> 1 : j & 3, dw = BITS == 4 ? 0 : j >> 2;
-    const uint32_t sel = 0x0c000c04u + byte * 0x00010001u;
-    uint32_t r[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t x = __builtin_amdgcn_perm(w[kW * (2 * i) + dw], w[kW * (2 * i + 1) + dw], sel);
-        r[i] = BITS == 4 ? minus(((j & 1 ? x >> 4 : x) & 0x000F000Fu) ^ 0x64086408u, 1032.0f) : minus(x ^ 0x64806480u, 1152.0f);
-    }
-    return u2{r[0], r[1]};
+    const uint32_t x = __builtin_amdgcn_perm(w[dw], w[BITS / 4 + dw], 0x0c000c04u + byte * 0x00010001u);
+    return BITS == 4 ? minus(((j & 1 ? x >> 4 : x) & 0x000F000Fu) ^ 0x64086408u, 1032.0f) : minus(x ^ 0x64806480u, 1152.0f);
 }
 
 __device__ __forceinline__ float swap_halves_max(float v) {
@@ -390,21 +385,18 @@ __device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
 }
 
-// The same for tiles of 32 WAVES rows, 32 a wave.  The waves share 64 tokens at
-// a time, which the workgroup turns into fp16 codes in LDS once, keys as
-// [token][d] and values as [d][token].  A wave takes 32 tokens at a time, and
-// computes the scores of the next 32 before it turns to the weights of these,
-// so that the matrix cores have work while the exponentials are computed.
-template <int BITS, int WAVES, bool FANCY>
-__global__ __launch_bounds__(64 * WAVES, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
-                                                              int own_tiles, int own_splits) {
-    constexpr int kTileRows = 32 * WAVES;
+// The same for tiles of 256 rows, 32 a wave.  The waves share 64 tokens at a
+// time, which the workgroup turns into fp16 codes in LDS once, keys as
+// [token][d] and values as [d][token].
+template <int BITS, bool FANCY>
+__global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
+                                                                int own_tiles, int own_splits) {
     // Rows of one chunk more than they hold, so that eight rows' same chunk lies in different banks and every address
     // is a base and a constant.  Value d is row 16 (d % 8) + d / 8.
     __shared__ u4 k_sh[2][kTileTokens * 17];       // 16 chunks of 8 values a token
     __shared__ u4 v_sh[2][128 * 9];                // 8 chunks of 8 tokens a value
     __shared__ f4 f_sh[2][3][kTileTokens / 4];     // per token: key factor, log2 of the value scale, its reciprocal
-    __shared__ int range_sh[WAVES][3];
+    __shared__ int range_sh[kTileWaves][3];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
@@ -484,7 +476,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_attn_tile(KvAttnArgs a, int 
     {
         int gmin = range_sh[0][0], gmax = range_sh[0][1], gend = range_sh[0][2];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) {
+        for (int w = 1; w < kTileWaves; ++w) {
             gmin = min(gmin, range_sh[w][0]);
             gmax = max(gmax, range_sh[w][1]);
             gend = max(gend, range_sh[w][2]);
@@ -524,78 +516,64 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_attn_tile(KvAttnArgs a, int 
     const float key_factor = capped ? a.scale / a.softcap : a.scale * kLog2e;
     const float to_log2 = a.softcap * kLog2e;
 
-    // What a wave stages of a step: 16 tokens (a quarter, so that they lie in one page), their keys and key scales
-    // (the upper half of 8 waves, or every one of 4), their values and value scales (the lower half, or every one).
-    // Codes are loaded two steps ahead, the page's number three.
-    const bool keys = WAVES == 4 || wave >= 4, values = WAVES == 4 || wave < 4;
-    const int quarter = 16 * (wave & 3);
-    // Lanes are dealt out so that eight (16) of them write to different banks: eight tokens' same chunk of a key,
-    // eight octets of the two quads that share a chunk of the values.
-    const int k_own = (lane & 7) + 8 * (lane >> 5), k_part = (lane >> 3) & 3, k_token = quarter + k_own;
-    const int v_own = ((lane >> 3) & 1) * 2 + ((lane >> 4) & 1), v_octet = (lane & 7) + 8 * (lane >> 5);
-    const int v_quad = (wave & 3) * 4 + v_own;
-    const int k_unit = k_own * 4 + k_part, v_unit = v_own * 16 + v_octet;      // of the 64 units of 4 BITS bytes
-    uint32_t kraw[BITS], vraw[BITS];
+    // What a wave stages of a step: eight tokens' keys, eight tokens' values and eight tokens' scales of both, all of the
+    // same 16 tokens, which lie in one page.  The keys are tokens 8 w .. 8 w + 7 of the step, the values those of two
+    // quads that share a chunk.  Codes are loaded a step ahead, the numbers of 64 steps' pages at once, a lane each.
+    // Lanes are dealt out so that those that write at one time write to different banks.
+    const int group = 16 * (wave >> 1);
+    const int k_token = 8 * wave + (lane & 7), k_part = lane >> 3;
+    const int v_octet = (lane & 7) + 8 * (lane >> 5), v_pair = (lane >> 3) & 1, v_half = (lane >> 4) & 1;
+    const int k_at = ((k_token & 15) * 8 + k_part) * 2 * BITS;                                 // bytes within the 16 tokens
+    const int v_at = ((((wave & 1) + 2 * v_half) * 16 + v_octet) * 2 + v_pair) * 2 * BITS;
+    const uint16_t* const scales = lane & 8 ? a.V_scale : a.K_scale;                           // lanes 0 .. 7 keys', 8 .. 15 values'
+    const int s_token = 8 * wave + (lane & 7);
+    uint32_t kraw[BITS / 2], vraw[BITS / 2];
     uint32_t sraw = 0;
     bool there = false;
     int pages = -1;
     auto load_pages = [&](int st) __attribute__((always_inline)) {      // of the wave's tokens in steps st .. st + 63
-        const long long j = static_cast<long long>(step0 + st + lane) * kTileTokens + quarter;
+        const long long j = static_cast<long long>(step0 + st + lane) * kTileTokens + group;
         pages = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
     };
     auto fetch = [&](int st) __attribute__((always_inline)) {
         const int page = __builtin_amdgcn_readlane(pages, st & 63);
-        const int j = (step0 + st) * kTileTokens + quarter;
+        const int j = (step0 + st) * kTileTokens + group;
         const bool good = page >= 0 && page < a.n_pages;
         const long long token = ((static_cast<long long>(good ? page : 0) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
-        if (keys) {
-            const u4* kp = reinterpret_cast<const u4*>(a.K_codes + token * (16 * BITS));
-#pragma unroll
-            for (int i = 0; i < BITS / 4; ++i) {
-                const u4 y = kp[k_unit * (BITS / 4) + i];
-                kraw[4 * i] = y.x; kraw[4 * i + 1] = y.y; kraw[4 * i + 2] = y.z; kraw[4 * i + 3] = y.w;
-            }
+        const uint8_t* kp = a.K_codes + token * (16 * BITS);
+        const uint8_t* vp = a.V_codes + token * (16 * BITS);
+        if (BITS == 4) {
+            const u2 x = *reinterpret_cast<const u2*>(kp + k_at), y = *reinterpret_cast<const u2*>(vp + v_at);
+            kraw[0] = x.x; kraw[1] = x.y;
+            vraw[0] = y.x; vraw[1] = y.y;
+        } else {
+            const u4 x = *reinterpret_cast<const u4*>(kp + k_at), y = *reinterpret_cast<const u4*>(vp + v_at);
+            kraw[0] = x.x; kraw[1] = x.y; kraw[BITS / 2 - 2] = x.z; kraw[BITS / 2 - 1] = x.w;
+            vraw[0] = y.x; vraw[1] = y.y; vraw[BITS / 2 - 2] = y.z; vraw[BITS / 2 - 1] = y.w;
         }
-        if (values) {
-            const u4* vp = reinterpret_cast<const u4*>(a.V_codes + token * (16 * BITS));
-#pragma unroll
-            for (int i = 0; i < BITS / 4; ++i) {
-                const u4 y = vp[v_unit * (BITS / 4) + i];
-                vraw[4 * i] = y.x; vraw[4 * i + 1] = y.y; vraw[4 * i + 2] = y.z; vraw[4 * i + 3] = y.w;
-            }
-        }
-        // lanes 0 .. 15 the key scales, 16 .. 31 the value scales
-        if (WAVES == 4)
-            sraw = ((lane & 16) == 0 ? a.K_scale : a.V_scale)[token + (lane & 15)];
-        else
-            sraw = ((wave >= 4 ? a.K_scale : a.V_scale) + token)[lane & 15];
-        there = good && j + (lane & 15) < span.tokens;
+        sraw = scales[token + (s_token & 15)];
+        there = good && j + (s_token & 15) < span.tokens;
     };
-    auto stage = [&](int buf) __attribute__((always_inline)) {
-        if (keys) {
+    auto stage_keys = [&](int buf, int part) __attribute__((always_inline)) {          // part 0, 1: eight codes each
+        k_sh[buf][k_token * 17 + 2 * k_part + part] = __builtin_bit_cast(u4, key_operand<BITS>(kraw + part * (BITS / 4)));
+    };
+    auto stage_values = [&](int buf, int part) __attribute__((always_inline)) {        // part 0 .. 3: two values of two tokens
+        uint32_t* p = reinterpret_cast<uint32_t*>(&v_sh[buf][v_octet * 9 + wave]) + 2 * v_half + v_pair;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Frag f;
-                f.v = key_operand<BITS>(kraw + i * (BITS / 4));
-                k_sh[buf][k_token * 17 + 4 * k_part + i] = u4{f.w[0], f.w[1], f.w[2], f.w[3]};
+        for (int j = 2 * part; j < 2 * part + 2; ++j) p[j * 576] = value_pair<BITS>(vraw, j);
+    };
+    auto stage_scales = [&](int buf) __attribute__((always_inline)) {
+        if (lane < 16) {
+            const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sraw)));
+            float* f = reinterpret_cast<float*>(f_sh[buf]) + s_token;
+            if (lane < 8) {
+                f[0] = there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;         // NaN where s is not finite
+            } else {
+                // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
+                const float vs = s == 0.0f ? 0x1p-24f : s;
+                f[kTileTokens] = there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
+                f[2 * kTileTokens] = there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
             }
-        }
-        if (values) {
-            const int chunk = 2 * (v_quad >> 2) + (v_quad & 1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                u2* p = reinterpret_cast<u2*>(&v_sh[buf][(16 * j + v_octet) * 9 + chunk]);
-                p[(v_quad >> 1) & 1] = value_quad<BITS>(vraw, j);
-            }
-        }
-        const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sraw)));
-        float* f = reinterpret_cast<float*>(f_sh[buf]) + quarter + (lane & 15);
-        if (keys && lane < 16) f[0] = there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;    // NaN where s is not finite
-        if (values && (WAVES == 4 ? lane >= 16 && lane < 32 : lane < 16)) {
-            // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
-            const float vs = s == 0.0f ? 0x1p-24f : s;
-            f[kTileTokens] = there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
-            f[2 * kTileTokens] = there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
         }
     };
 
@@ -608,7 +586,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_attn_tile(KvAttnArgs a, int 
 
     f16v s;            // products of 32 tokens with their codes, then their exponents
     h8 w[2];           // their weights
-    u4 kc[8];          // keys of the 32 tokens behind them
+    u4 vc[8];          // the tokens' values
     f4 kf[4], rv[4];   // factors of the tokens: key, reciprocal value scale,
     float lv;          // log2 of the value scale, lane c of 16 for the lane's token c
 
@@ -717,76 +695,85 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_attn_tile(KvAttnArgs a, int 
             d[4 * (i & 1) + 3] = p1.y;
         }
     };
-    auto load_keys = [&](int buf, int sub) __attribute__((always_inline)) {
+    auto load_values = [&](int buf, int sub) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) kc[k] = key_chunk(buf, sub, k);
+        for (int c = 0; c < 8; ++c) vc[c] = value_chunk(buf, sub, c);
     };
-    auto next_products = [&]() __attribute__((always_inline)) {
+    auto next_products = [&](const u4* kc) __attribute__((always_inline)) {
         s = f16v{};
 #pragma unroll
         for (int k = 0; k < 8; ++k) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kc[k]), q[k], s, 0, 0, 0);
     };
-    // Matrix work: the products of the next 32 tokens, and these 32 tokens' (buf, sub) weighted values
-    auto matrix_part = [&](int buf, int sub, int next_buf, int next_sub, bool some) __attribute__((always_inline)) {
-        u4 vc[8];
+    // Matrix work: 32 tokens' weighted values, and the products of the next 32 (buf, sub); if STAGE, between the matrix
+    // instructions, which the wave would wait for, what it stages of the next step into buf ^ 1
+    auto matrix_part = [&](int buf, int sub, bool STAGE) __attribute__((always_inline)) {
+        u4 kc[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) vc[i] = value_chunk(buf, sub, i);
-        load_factors(next_buf, next_sub);
-        next_products();
-        if (some) {
+        for (int k = 0; k < 8; ++k) kc[k] = key_chunk(buf, sub, k);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, vc[i]), w[i >> 2], o[i & 3], 0, 0, 0);
+        for (int c = 0; c < 8; ++c) {
+            o[c & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, vc[c]), w[c >> 2], o[c & 3], 0, 0, 0);
+            if (STAGE && c < 4) stage_values(buf ^ 1, c);
+            if (STAGE && (c == 4 || c == 6)) stage_keys(buf ^ 1, (c - 4) / 2);
+            if (STAGE) __builtin_amdgcn_sched_barrier(0);
         }
+        load_factors(buf, sub);
+        next_products(kc);
     };
 
     if (steps > 0) {
         load_pages(0);
         fetch(0);
-        stage(0);
+        stage_keys(0, 0);
+        stage_keys(0, 1);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) stage_values(0, c);
+        stage_scales(0);
         if (steps > 1) fetch(1);
     }
     __syncthreads();
     const int base = step0 * kTileTokens + span.base;
     if (steps > 0) {
-        load_keys(0, 0);
+        u4 kc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) kc[k] = key_chunk(0, 0, k);
         load_factors(0, 0);
-        next_products();
+        next_products(kc);
     }
     // Two waves share a SIMD, one of each half of the workgroup.  The upper half runs a part behind the lower one, so
     // that of the two waves one has matrix and one has vector work, always:
     //   lower   V0  M0  V1  M1  V0 ..        V: exponents and weights, M: the two products, of 32 tokens (0, 1)
     //   upper       V0  M0  V1  M1 ..
-    // The next step's tokens go into the other buffer, which the upper half's M1 reads last, in the time of the lower
-    // half's V0: the upper half writes (keys) in its V0, the lower (values) in its V1, both before the lower half's M1.
-    // Four waves have a SIMD each, run together, and write both in V0.
-    const bool upper = WAVES == 8 && wave >= 4;
+    // The next step's tokens go into the other buffer in each half's M0: the upper half's V1 reads that buffer last, two
+    // parts before the lower half writes, and the lower half's M1 reads it first, a part after the upper half has written.
+    const bool upper = wave >= kTileWaves / 2;
     if (upper) __syncthreads();
     for (int st = 0; st < steps; ++st) {
         const int buf = st & 1;
         const int j0 = base + st * kTileTokens;     // position of the first token
         const bool some = seen_some(j0), whole = seen_whole(j0);
-        const bool more = st + 1 < steps;
-        auto turn = [&]() __attribute__((always_inline)) {
-            if (more) stage(buf ^ 1);
-            if (st + 2 < steps) {
-                if (((st + 2) & 63) == 0) load_pages(st + 2);
-                fetch(st + 2);
-            }
-        };
-        if (some) vector_part(j0, whole);
-        load_keys(buf, 1);
-        if (WAVES == 4 || upper) turn();
+        load_values(buf, 0);
+        if (some) {
+            vector_part(j0, whole);
+        } else {
+            w[0] = w[1] = h8{};
+        }
         __syncthreads();
-        matrix_part(buf, 0, buf, 1, some);
+        matrix_part(buf, 1, true);      // behind the last step what is staged is of no use, and does no harm
+        stage_scales(buf ^ 1);
+        if (st + 2 < steps) {
+            if (((st + 2) & 63) == 0) load_pages(st + 2);
+            fetch(st + 2);
+        }
         __syncthreads();
+        load_values(buf, 1);
         if (some) vector_part(j0 + 32, whole);
-        load_keys(buf ^ 1, 0);      // behind the last step of whatever is there, for nothing
-        if (WAVES == 8 && !upper) turn();
         __syncthreads();
-        matrix_part(buf, 1, buf ^ 1, 0, some);
+        matrix_part(buf ^ 1, 0, false);
         __syncthreads();
     }
-    if (WAVES == 8 && !upper) __syncthreads();
+    if (!upper) __syncthreads();
 
     const float l = swap_halves_sum(l_sum);
     if (at_row < 0) return;
@@ -847,7 +834,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int s
 
 // Grid of a call: rows of a tile, tiles, and the shares their tokens are split into.
 struct Plan {
-    int rows;                      // 16: kv_attn_rows16; 128, 256: kv_attn_tile
+    int rows;                      // kRows: kv_attn_rows16; kTileRows: kv_attn_tile
     long long prefix_tiles, own_tiles;
     int prefix_splits, own_splits;
     size_t workspace;
@@ -858,7 +845,7 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     Plan p = {};
     // rows that read the same tokens: of a sequence on average, of all sequences in a shared prefix
     const long long together = prefix_len > 0 ? T * G : T * G / B;
-    p.rows = together >= kWideRows ? 256 : together >= kManyRows ? 128 : kRows;
+    p.rows = together >= kManyRows ? kTileRows : kRows;
     const long long wanted = p.rows == kRows ? 2048 : 512;      // workgroups that fill the card
     p.own_tiles = T * G / p.rows + B;
     p.prefix_tiles = prefix_len > 0 ? (T * G + p.rows - 1) / p.rows : 0;
@@ -874,20 +861,19 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     return p;
 }
 
-template <int BITS, int WAVES>
+template <int BITS>
 void launch_tile(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(items * a.Hkv));
     const int pt = static_cast<int>(p.prefix_tiles), ot = static_cast<int>(p.own_tiles);
     if (a.softcap > 0.0f || a.slopes)
-        hipLaunchKernelGGL((kv_attn_tile<BITS, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, true>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
     else
-        hipLaunchKernelGGL((kv_attn_tile<BITS, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, false>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
 }
 
 template <int BITS>
 void launch_rows(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
-    if (p.rows == 256) return launch_tile<BITS, 8>(a, p, items, s);
-    if (p.rows == 128) return launch_tile<BITS, 4>(a, p, items, s);
+    if (p.rows == kTileRows) return launch_tile<BITS>(a, p, items, s);
     hipLaunchKernelGGL(kv_attn_rows16<BITS>, dim3(static_cast<unsigned>(items), a.Hkv), dim3(kAttnThreads), 0, s, a,
                        static_cast<int>(p.prefix_tiles), p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
 }
