@@ -40,8 +40,8 @@ constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
 constexpr int kSplitMinTokens = 256;      // fewest tokens worth a workgroup of their own
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTileRows = 256;            // rows of a tile where there are many
-constexpr int kManyRows = 32;             // rows on the same tokens from which those tiles are taken
+constexpr int kManyRows = 32;             // rows on the same tokens from which tiles of 128, 256 rows are taken
+constexpr int kWideRows = 1024;
 constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
 
 union Frag {
@@ -385,21 +385,35 @@ __device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
 }
 
-// The same for tiles of 256 rows, 32 a wave.  The waves share 64 tokens at a
-// time, which the workgroup turns into fp16 codes in LDS once, keys as
-// [token][d] and values as [d][token].
-template <int BITS, bool FANCY>
+// A barrier that orders the waves, and keeps the compiler's order, without waiting for loads in flight.
+__device__ __forceinline__ void part_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// The same for tiles of ROWS = 256 rows, 32 a wave, or of 128, 32 for two waves
+// that take half of the tokens each.  The waves share 64 tokens at a time,
+// which the workgroup turns into fp16 codes in LDS once, keys as [token][d] and
+// values as [d][token].
+template <int BITS, int ROWS, bool FANCY>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
                                                                 int own_tiles, int own_splits) {
+    constexpr bool kPair = ROWS == 128;            // two waves a row
+    constexpr int kBuffers = kPair ? 3 : 2;
     // Rows of one chunk more than they hold, so that eight rows' same chunk lies in different banks and every address
     // is a base and a constant.  Value d is row 16 (d % 8) + d / 8.
-    __shared__ u4 k_sh[2][kTileTokens * 17];       // 16 chunks of 8 values a token
-    __shared__ u4 v_sh[2][128 * 9];                // 8 chunks of 8 tokens a value
-    __shared__ f4 f_sh[2][3][kTileTokens / 4];     // per token: key factor, log2 of the value scale, its reciprocal
+    struct Step {
+        u4 k[kTileTokens * 17];                    // 16 chunks of 8 values a token
+        u4 v[128 * 9];                             // 8 chunks of 8 tokens a value
+        f4 f[3][kTileTokens / 4];                  // per token: key factor, log2 of the value scale, its reciprocal
+    };
+    __shared__ Step sh[kBuffers];
     __shared__ int range_sh[kTileWaves][3];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
+    const int row_wave = kPair ? wave & 3 : wave;
     const int G = a.Hq / a.Hkv;
     // key heads alternate fastest: with 8 of them a head stays on one XCD; late tiles, the long ones, come first
     const int h = blockIdx.x % a.Hkv;
@@ -417,7 +431,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     bool valid;
     if (shared) {
         span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
-        const long long r = static_cast<long long>(tile) * kTileRows + wave * 32 + n;
+        const long long r = static_cast<long long>(tile) * ROWS + row_wave * 32 + n;
         const long long tt = r / G;
         t = static_cast<int>(tt);
         head = h * G + static_cast<int>(r - tt * G);
@@ -432,16 +446,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         int lo = 0, c = a.B;
         while (c > 1) {
             const int half = c >> 1;
-            const bool before = static_cast<long long>(a.q_start[lo + half]) * G / kTileRows + lo + half <= tile;
+            const bool before = static_cast<long long>(a.q_start[lo + half]) * G / ROWS + lo + half <= tile;
             lo += before ? half : 0;
             c = before ? c - half : half;
         }
         const int b = lo;
         const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
-        const long long first = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / kTileRows + b)) * kTileRows;
+        const long long first = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / ROWS + b)) * ROWS;
         const long long rows = static_cast<long long>(q1 - q0) * G;
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
-        const long long r = first + wave * 32 + n;
+        const long long r = first + row_wave * 32 + n;
         valid = r >= 0 && r < rows;
         const int i = valid ? static_cast<int>(r / G) : 0;
         t = q0 + i;
@@ -525,21 +539,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const int v_octet = (lane & 7) + 8 * (lane >> 5), v_pair = (lane >> 3) & 1, v_half = (lane >> 4) & 1;
     const int k_at = ((k_token & 15) * 8 + k_part) * 2 * BITS;                                 // bytes within the 16 tokens
     const int v_at = ((((wave & 1) + 2 * v_half) * 16 + v_octet) * 2 + v_pair) * 2 * BITS;
-    const uint16_t* const scales = lane & 8 ? a.V_scale : a.K_scale;                           // lanes 0 .. 7 keys', 8 .. 15 values'
+    const bool s_values = (lane & 8) != 0;                  // of 16 lanes 0 .. 7 stage key, 8 .. 15 value scales, four times over
+    const uint16_t* const scales = s_values ? a.V_scale : a.K_scale;
     const int s_token = 8 * wave + (lane & 7);
     uint32_t kraw[BITS / 2], vraw[BITS / 2];
     uint32_t sraw = 0;
     bool there = false;
-    int pages = -1;
-    auto load_pages = [&](int st) __attribute__((always_inline)) {      // of the wave's tokens in steps st .. st + 63
+    // Of steps st .. st + 63, a lane each: where the wave's 16 tokens lie, as the number of the first, ~0 if nowhere.
+    uint32_t place_lo = 0, place_hi = 0;
+    auto load_places = [&](int st) __attribute__((always_inline)) {
         const long long j = static_cast<long long>(step0 + st + lane) * kTileTokens + group;
-        pages = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
+        const int page = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
+        const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+        const bool good = page >= 0 && page < a.n_pages;
+        place_lo = good ? static_cast<uint32_t>(token) : ~0u;
+        place_hi = good ? static_cast<uint32_t>(token >> 32) : ~0u;
     };
     auto fetch = [&](int st) __attribute__((always_inline)) {
-        const int page = __builtin_amdgcn_readlane(pages, st & 63);
-        const int j = (step0 + st) * kTileTokens + group;
-        const bool good = page >= 0 && page < a.n_pages;
-        const long long token = ((static_cast<long long>(good ? page : 0) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+        const uint32_t lo = __builtin_amdgcn_readlane(place_lo, st & 63), hi = __builtin_amdgcn_readlane(place_hi, st & 63);
+        const bool good = hi != ~0u;
+        const unsigned long long token = good ? (static_cast<unsigned long long>(hi) << 32) | lo : static_cast<unsigned long long>(h) << a.page_log2;
         const uint8_t* kp = a.K_codes + token * (16 * BITS);
         const uint8_t* vp = a.V_codes + token * (16 * BITS);
         if (BITS == 4) {
@@ -552,29 +571,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
             vraw[0] = y.x; vraw[1] = y.y; vraw[BITS / 2 - 2] = y.z; vraw[BITS / 2 - 1] = y.w;
         }
         sraw = scales[token + (s_token & 15)];
-        there = good && j + (s_token & 15) < span.tokens;
+        there = good && (step0 + st) * kTileTokens + s_token < span.tokens;
     };
     auto stage_keys = [&](int buf, int part) __attribute__((always_inline)) {          // part 0, 1: eight codes each
-        k_sh[buf][k_token * 17 + 2 * k_part + part] = __builtin_bit_cast(u4, key_operand<BITS>(kraw + part * (BITS / 4)));
+        sh[buf].k[k_token * 17 + 2 * k_part + part] = __builtin_bit_cast(u4, key_operand<BITS>(kraw + part * (BITS / 4)));
     };
     auto stage_values = [&](int buf, int part) __attribute__((always_inline)) {        // part 0 .. 3: two values of two tokens
-        uint32_t* p = reinterpret_cast<uint32_t*>(&v_sh[buf][v_octet * 9 + wave]) + 2 * v_half + v_pair;
+        uint32_t* p = reinterpret_cast<uint32_t*>(&sh[buf].v[v_octet * 9 + wave]) + 2 * v_half + v_pair;
 #pragma unroll
         for (int j = 2 * part; j < 2 * part + 2; ++j) p[j * 576] = value_pair<BITS>(vraw, j);
     };
     auto stage_scales = [&](int buf) __attribute__((always_inline)) {
-        if (lane < 16) {
-            const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sraw)));
-            float* f = reinterpret_cast<float*>(f_sh[buf]) + s_token;
-            if (lane < 8) {
-                f[0] = there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;         // NaN where s is not finite
-            } else {
-                // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
-                const float vs = s == 0.0f ? 0x1p-24f : s;
-                f[kTileTokens] = there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
-                f[2 * kTileTokens] = there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
-            }
-        }
+        const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sraw)));
+        // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
+        const float vs = s == 0.0f ? 0x1p-24f : s;
+        const float key = there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;      // NaN where s is not finite
+        const float log_v = there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
+        const float rcp_v = there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
+        float* f = reinterpret_cast<float*>(sh[buf].f) + s_token;
+        f[s_values ? kTileTokens : 0] = s_values ? log_v : key;
+        f[s_values ? 2 * kTileTokens : 0] = s_values ? rcp_v : key;
     };
 
     // M: what a row's exponents are relative to.  It follows the row's maximum by more than kSlack powers of two, up, and
@@ -609,17 +625,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     };
     auto key_chunk = [&](int buf, int sub, int k) __attribute__((always_inline)) {
         const int token = 32 * sub + n;
-        return k_sh[buf][token * 17 + 2 * k + hf];
+        return sh[buf].k[token * 17 + 2 * k + hf];
     };
     auto value_chunk = [&](int buf, int sub, int i) __attribute__((always_inline)) {      // i = 4 kk + m
-        return v_sh[buf][(32 * (i & 3) + n) * 9 + 4 * sub + 2 * (i >> 2) + hf];
+        return sh[buf].v[(32 * (i & 3) + n) * 9 + 4 * sub + 2 * (i >> 2) + hf];
     };
     auto load_factors = [&](int buf, int sub) __attribute__((always_inline)) {
-        lv = reinterpret_cast<const float*>(f_sh[buf][1])[32 * sub + 8 * ((lane & 15) >> 2) + 4 * hf + (lane & 3)];
+        lv = reinterpret_cast<const float*>(sh[buf].f[1])[32 * sub + 8 * ((lane & 15) >> 2) + 4 * hf + (lane & 3)];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            kf[i] = f_sh[buf][0][8 * sub + 2 * i + hf];
-            rv[i] = f_sh[buf][2][8 * sub + 2 * i + hf];
+            kf[i] = sh[buf].f[0][8 * sub + 2 * i + hf];
+            rv[i] = sh[buf].f[2][8 * sub + 2 * i + hf];
         }
     };
     // products to exponents of the tokens at positions j0 .. j0 + 31, relative to M
@@ -699,81 +715,148 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
 #pragma unroll
         for (int c = 0; c < 8; ++c) vc[c] = value_chunk(buf, sub, c);
     };
-    auto next_products = [&](const u4* kc) __attribute__((always_inline)) {
-        s = f16v{};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kc[k]), q[k], s, 0, 0, 0);
-    };
-    // Matrix work: 32 tokens' weighted values, and the products of the next 32 (buf, sub); if STAGE, between the matrix
-    // instructions, which the wave would wait for, what it stages of the next step into buf ^ 1
-    auto matrix_part = [&](int buf, int sub, bool STAGE) __attribute__((always_inline)) {
+    // Matrix work: 32 tokens' weighted values, and the products of the next 32 (buf, sub), in turn, since the latter depend
+    // on each other; if STAGE, between them, where the wave would wait, what it stages of a later step into buffer `to`
+    auto matrix_part = [&](int buf, int sub, bool STAGE, int to) __attribute__((always_inline)) {
         u4 kc[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) kc[k] = key_chunk(buf, sub, k);
+        s = f16v{};
+        auto weighted = [&](int c) __attribute__((always_inline)) {
+            o[c & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, vc[c]), w[c >> 2], o[c & 3], 0, 0, 0);
+        };
+        auto product = [&](int k) __attribute__((always_inline)) {
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kc[k]), q[k], s, 0, 0, 0);
+        };
+        __builtin_amdgcn_s_setprio(1);      // before the other wave's vector work: prompt of 8192 tokens 785 -> 737 us
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            o[c & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, vc[c]), w[c >> 2], o[c & 3], 0, 0, 0);
-            if (STAGE && c < 4) stage_values(buf ^ 1, c);
-            if (STAGE && (c == 4 || c == 6)) stage_keys(buf ^ 1, (c - 4) / 2);
-            if (STAGE) __builtin_amdgcn_sched_barrier(0);
+        for (int c = 0; c < 4; ++c) {
+            weighted(c);
+            if (STAGE) stage_values(to, c);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            product(c);
+            if (STAGE && c < 2) stage_keys(to, c);
+            if (STAGE && c == 2) stage_scales(to);
+            __builtin_amdgcn_sched_barrier(0);
+            weighted(4 + c);
+            __builtin_amdgcn_sched_barrier(0);
         }
         load_factors(buf, sub);
-        next_products(kc);
+#pragma unroll
+        for (int k = 4; k < 8; ++k) product(k);
+        __builtin_amdgcn_s_setprio(0);
     };
 
-    if (steps > 0) {
-        load_pages(0);
-        fetch(0);
-        stage_keys(0, 0);
-        stage_keys(0, 1);
+    auto stage_all = [&](int buf) __attribute__((always_inline)) {
+        stage_keys(buf, 0);
+        stage_keys(buf, 1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) stage_values(0, c);
-        stage_scales(0);
-        if (steps > 1) fetch(1);
-    }
-    __syncthreads();
-    const int base = step0 * kTileTokens + span.base;
-    if (steps > 0) {
-        u4 kc[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) kc[k] = key_chunk(0, 0, k);
-        load_factors(0, 0);
-        next_products(kc);
-    }
+        for (int c = 0; c < 4; ++c) stage_values(buf, c);
+        stage_scales(buf);
+    };
+    auto fetch_later = [&](int st) __attribute__((always_inline)) {       // nothing, past the last step
+        if ((st & 63) == 0) load_places(st);
+        fetch(st);
+    };
     // Two waves share a SIMD, one of each half of the workgroup.  The upper half runs a part behind the lower one, so
     // that of the two waves one has matrix and one has vector work, always:
     //   lower   V0  M0  V1  M1  V0 ..        V: exponents and weights, M: the two products, of 32 tokens (0, 1)
     //   upper       V0  M0  V1  M1 ..
-    // The next step's tokens go into the other buffer in each half's M0: the upper half's V1 reads that buffer last, two
-    // parts before the lower half writes, and the lower half's M1 reads it first, a part after the upper half has written.
+    // 256 rows: the next step's tokens go into the other buffer in each half's M0.  The upper half's V1 reads that buffer
+    // last, two parts before the lower half writes, and the lower half's M1 reads it first, a part after the upper half
+    // has written.  128 rows: the lower half has a step's first 32 tokens, the upper the others,
+    //   lower   V  M  V  M ..
+    //   upper      V  M  V ..
+    // and the tokens of the step after the next go into a third buffer in M, which the upper half's V read last, two
+    // parts before, and the lower half's M reads first, a part after.
+    // What a part reads of LDS is waited for in the part behind it at the latest, two before it is written again: only
+    // a barrier behind writes, which publishes them, has to wait for the LDS.
     const bool upper = wave >= kTileWaves / 2;
-    if (upper) __syncthreads();
+    const int own_sub = kPair && upper ? 1 : 0;
+    const int base = step0 * kTileTokens + span.base;
+    if (steps > 0) {
+        load_places(0);
+        fetch(0);
+        stage_all(0);
+        fetch(1);
+        if (kPair) {
+            stage_all(1);
+            fetch(2);
+        }
+    }
+    __syncthreads();
+    if (steps > 0) {
+        load_factors(0, own_sub);
+        s = f16v{};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, key_chunk(0, own_sub, k)), q[k], s, 0, 0, 0);
+    }
+    if (upper) part_barrier();
+    int buf = 0;
     for (int st = 0; st < steps; ++st) {
-        const int buf = st & 1;
         const int j0 = base + st * kTileTokens;     // position of the first token
         const bool some = seen_some(j0), whole = seen_whole(j0);
-        load_values(buf, 0);
+        const int next = buf + 1 == kBuffers ? 0 : buf + 1;
+        load_values(buf, own_sub);
         if (some) {
-            vector_part(j0, whole);
+            vector_part(j0 + 32 * own_sub, whole);
         } else {
             w[0] = w[1] = h8{};
         }
+        part_barrier();
+        // behind the last step what is staged is of no use, and does no harm
+        if (kPair) {
+            const int after = next + 1 == kBuffers ? 0 : next + 1;
+            matrix_part(next, own_sub, true, after);
+            fetch_later(st + 3);
+        } else {
+            matrix_part(buf, 1, true, next);
+            fetch_later(st + 2);
+            __syncthreads();
+            load_values(buf, 1);
+            if (some) vector_part(j0 + 32, whole);
+            part_barrier();
+            matrix_part(next, 0, false, 0);
+        }
+        if (kPair)
+            __syncthreads();
+        else
+            part_barrier();
+        buf = next;
+    }
+    if (!upper) part_barrier();
+
+    if (kPair) {
+        // the upper half's sums, to the lower half's lane of the same row
+        u4* slot = reinterpret_cast<u4*>(sh) + row_wave * 17 * 64 + lane;
         __syncthreads();
-        matrix_part(buf, 1, true);      // behind the last step what is staged is of no use, and does no harm
-        stage_scales(buf ^ 1);
-        if (st + 2 < steps) {
-            if (((st + 2) & 63) == 0) load_pages(st + 2);
-            fetch(st + 2);
+        if (upper) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                slot[64 * c] = __builtin_bit_cast(u4, (f4{o[c >> 2][4 * (c & 3)], o[c >> 2][4 * (c & 3) + 1], o[c >> 2][4 * (c & 3) + 2], o[c >> 2][4 * (c & 3) + 3]}));
+            slot[64 * 16] = __builtin_bit_cast(u4, (f4{M, l_sum, low, 0.0f}));
         }
         __syncthreads();
-        load_values(buf, 1);
-        if (some) vector_part(j0 + 32, whole);
-        __syncthreads();
-        matrix_part(buf ^ 1, 0, false);
-        __syncthreads();
+        if (upper) return;
+        const f4 other = __builtin_bit_cast(f4, slot[64 * 16]);
+        const bool mine_none = low > 0.0f, other_none = other.z > 0.0f;
+        const float M_all = mine_none ? other.x : other_none ? M : __builtin_fmaxf(M, other.x);
+        const float f_mine = mine_none ? 0.0f : __builtin_amdgcn_exp2f(M - M_all);
+        const float f_other = other_none ? 0.0f : __builtin_amdgcn_exp2f(other.x - M_all);
+        l_sum = l_sum * f_mine + other.y * f_other;
+        M = M_all;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const f4 y = __builtin_bit_cast(f4, slot[64 * c]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[c >> 2][4 * (c & 3) + r] = o[c >> 2][4 * (c & 3) + r] * f_mine + y[r] * f_other;
+        }
     }
-    if (!upper) __syncthreads();
 
     const float l = swap_halves_sum(l_sum);
     if (at_row < 0) return;
@@ -834,7 +917,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int s
 
 // Grid of a call: rows of a tile, tiles, and the shares their tokens are split into.
 struct Plan {
-    int rows;                      // kRows: kv_attn_rows16; kTileRows: kv_attn_tile
+    int rows;                      // kRows: kv_attn_rows16; ROWS: kv_attn_tile
     long long prefix_tiles, own_tiles;
     int prefix_splits, own_splits;
     size_t workspace;
@@ -845,7 +928,7 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     Plan p = {};
     // rows that read the same tokens: of a sequence on average, of all sequences in a shared prefix
     const long long together = prefix_len > 0 ? T * G : T * G / B;
-    p.rows = together >= kManyRows ? kTileRows : kRows;
+    p.rows = together >= kWideRows ? 256 : together >= kManyRows ? 128 : kRows;
     const long long wanted = p.rows == kRows ? 2048 : 512;      // workgroups that fill the card
     p.own_tiles = T * G / p.rows + B;
     p.prefix_tiles = prefix_len > 0 ? (T * G + p.rows - 1) / p.rows : 0;
@@ -861,19 +944,20 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     return p;
 }
 
-template <int BITS>
+template <int BITS, int ROWS>
 void launch_tile(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(items * a.Hkv));
     const int pt = static_cast<int>(p.prefix_tiles), ot = static_cast<int>(p.own_tiles);
     if (a.softcap > 0.0f || a.slopes)
-        hipLaunchKernelGGL((kv_attn_tile<BITS, true>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, true>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
     else
-        hipLaunchKernelGGL((kv_attn_tile<BITS, false>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, false>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
 }
 
 template <int BITS>
 void launch_rows(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
-    if (p.rows == kTileRows) return launch_tile<BITS>(a, p, items, s);
+    if (p.rows == 256) return launch_tile<BITS, 256>(a, p, items, s);
+    if (p.rows == 128) return launch_tile<BITS, 128>(a, p, items, s);
     hipLaunchKernelGGL(kv_attn_rows16<BITS>, dim3(static_cast<unsigned>(items), a.Hkv), dim3(kAttnThreads), 0, s, a,
                        static_cast<int>(p.prefix_tiles), p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
 }
