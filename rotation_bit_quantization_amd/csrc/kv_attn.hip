@@ -38,7 +38,11 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
-constexpr int kSplitMinTokens = 256;      // fewest tokens worth a workgroup of their own
+// Workgroups that fill the card, and the fewest tokens worth one, of the two kernels; the most shares of a row's tokens.
+constexpr int kRowsWanted = 1536, kRowsLeast = 256;
+constexpr int kTilesWanted = 256, kTilesLeast = 256;
+constexpr int kMostSplits = 256;
+constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kManyRows = 32;             // rows on the same tokens from which tiles of 128, 256 rows are taken
 constexpr int kWideRows = 1024;
@@ -108,6 +112,11 @@ __device__ __forceinline__ float sum_over_groups(float v) {
     return __uint_as_float(s.x) + __uint_as_float(s.y);
 }
 
+template <int N>
+__device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes of a row, for all of them
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
+}
+
 // tanh from one exponential: 1 - 2 / (e^(2 x) + 1), right at both infinities.
 __device__ __forceinline__ float tanh_fast(float x) {
     return 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * kLog2e * x) + 1.0f);
@@ -132,13 +141,13 @@ struct Span {
 // workspace, [share][T * Hq] rows.
 //
 // Bound at few rows: reading the cache, 2 (16 BITS + 2) bytes a token and head.
-template <int BITS>
-__global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits,
-                                                               int own_tiles, int own_splits) {
+template <int BITS, bool FANCY>
+__global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
+                                                                  int own_tiles, int own_splits, int own_chunk) {
     __shared__ float o_sh[kAttnWaves][kRows][129];
     __shared__ float m_sh[kAttnWaves][kRows], l_sh[kAttnWaves][kRows];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int h = blockIdx.y, G = a.Hq / a.Hkv;
     const int prefix_items = prefix_tiles * prefix_splits;
@@ -189,25 +198,34 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int
     }
     // the tokens that any of the rows sees
     int lo = 0, hi = span.tokens;
-    {
-        int pmin = valid ? pos : 0x7FFFFFFF, pmax = valid ? max(pos + 1, both) : -0x7FFFFFFF, wmax = valid ? pos : -0x7FFFFFFF;
+    int pmin = valid ? pos : 0x7FFFFFFF, pmax = valid ? max(pos + 1, both) : -0x7FFFFFFF, wmax = valid ? pos : -0x7FFFFFFF;
+    int bmin = valid ? both : 0x7FFFFFFF;
 #pragma unroll
-        for (int x = 1; x < 16; x <<= 1) {
-            pmin = min(pmin, __shfl_xor(pmin, x, 64));
-            pmax = max(pmax, __shfl_xor(pmax, x, 64));
-            wmax = max(wmax, __shfl_xor(wmax, x, 64));
-        }
-        if (a.causal) hi = min(hi, pmax - span.base);
-        if (a.window > 0) {
-            lo = max(lo, static_cast<int>(max(static_cast<long long>(pmin) - a.window + 1 - span.base, 0LL)));
-            hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(wmax) + a.window - span.base));
-        }
+    for (int x = 1; x < 16; x <<= 1) {
+        pmin = min(pmin, __shfl_xor(pmin, x, 64));
+        pmax = max(pmax, __shfl_xor(pmax, x, 64));
+        wmax = max(wmax, __shfl_xor(wmax, x, 64));
+        bmin = min(bmin, __shfl_xor(bmin, x, 64));
+    }
+    if (a.causal) hi = min(hi, pmax - span.base);
+    if (a.window > 0) {
+        lo = static_cast<int>(max(static_cast<long long>(pmin) - a.window + 1 - span.base, 0LL));
+        hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(wmax) + a.window - span.base));
     }
     int step0 = lo / kStep;
     const int steps_all = hi > lo ? (hi + kStep - 1) / kStep - step0 : 0;
-    const int share = max((steps_all + splits - 1) / splits, kSplitMinTokens / kStep);
-    step0 += split * share;
-    const int steps = max(0, min(share, steps_all - split * share));
+    const int share = max((steps_all + splits - 1) / splits, (shared ? prefix_chunk : own_chunk) / kStep);
+    const int steps = __builtin_amdgcn_readfirstlane(max(0, min(share, steps_all - split * share)));
+    step0 = __builtin_amdgcn_readfirstlane(step0 + split * share);
+    // every row sees every token of the steps whole0 .. whole1 - 1
+    int whole0 = 0, whole1 = span.tokens;
+    if (a.causal) whole1 = min(whole1, max(pmin + 1, bmin) - span.base);
+    if (a.window > 0) {
+        whole0 = static_cast<int>(max(static_cast<long long>(wmax) - a.window + 1 - span.base, 0LL));
+        whole1 = static_cast<int>(min(static_cast<long long>(whole1), static_cast<long long>(pmin) + a.window - span.base));
+    }
+    whole0 = __builtin_amdgcn_readfirstlane((whole0 + kStep - 1) / kStep);
+    whole1 = __builtin_amdgcn_readfirstlane(whole1 >= 0 ? whole1 / kStep : -1);
 
     // queries, in the order of the keys' codes: lane (n, g) holds values 32 g .. 32 g + 31 of row n
     h8 q[4];
@@ -223,86 +241,162 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_rows16(KvAttnArgs a, int
             q[j] = f.v;
         }
     }
-    const float slope = a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
-    const float to_log2 = a.softcap > 0.0f ? a.softcap * kLog2e : a.scale * kLog2e;
-    const float to_cap = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
+    const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+    const bool capped = FANCY && a.softcap > 0.0f;
+    const float key_factor = capped ? a.scale / a.softcap : a.scale * kLog2e;
+    const float to_log2 = a.softcap * kLog2e;
 
-    float M = -__builtin_inff(), l_sum = 0.0f;
-    f4 o[8] = {};
-
-    for (int st = wave; st < steps; st += kAttnWaves) {
-        const int j0 = (step0 + st) * kStep;
-        h8 w_op;
-        uint32_t vcodes[8 * BITS / 4];
-        float tt[8], rvs[8];
-        float top = -__builtin_inff();
+    // Of the wave's next 32 steps, a lane each and half of a step: where the 16 tokens lie, as the number of the first, ~0
+    // if nowhere.
+    uint32_t place_lo = 0, place_hi = 0;
+    auto load_places = [&](int i) __attribute__((always_inline)) {      // the wave's steps i .. i + 31
+        const long long j = static_cast<long long>(step0 + wave + kAttnWaves * (i + (lane >> 1))) * kStep + 16 * (lane & 1);
+        const int page = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
+        const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+        const bool good = page >= 0 && page < a.n_pages;
+        place_lo = good ? static_cast<uint32_t>(token) : ~0u;
+        place_hi = good ? static_cast<uint32_t>(token >> 32) : ~0u;
+    };
+    // A step's codes and scales, loaded a step ahead.  Lane (n, g) takes 32 codes of token n of each 16 and an octet of
+    // tokens 4 g .. 4 g + 3, and the scales of one token: of lanes 0 .. 7 of a row of 16 lanes token 4 g + l of the first
+    // 16 (l < 4) or 4 g + l - 4 of the second, lanes 8 .. 15 again.
+    uint32_t kraw[2][BITS], vraw[2 * BITS];
+    uint32_t ks_raw = 0, vs_raw = 0;
+    bool there = false;
+    const int s_half = (n >> 2) & 1, s_token = 4 * g + (n & 3);
+    auto fetch = [&](int i) __attribute__((always_inline)) {
+        const int j0 = (step0 + wave + kAttnWaves * i) * kStep;
+        unsigned long long token[2];
+        bool good[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int jt = j0 + 16 * half;
-            // 16 tokens lie in one page; one that is not there counts as no tokens
-            const int entry = __builtin_amdgcn_readfirstlane(min(jt >> a.page_log2, span.n_table - 1));
-            int page = jt < span.tokens ? span.table[entry] : -1;
-            const bool there = page >= 0 && page < a.n_pages;
-            if (!there) page = 0;
-            const int slot = jt & ((1 << a.page_log2) - 1);
-            const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + slot;
-            const uint8_t* kp = a.K_codes + (token + n) * (16 * BITS) + g * (4 * BITS);
-            const uint8_t* vp = a.V_codes + (token + 4 * g) * (16 * BITS) + n * (4 * BITS);
-            uint32_t kw[BITS];
+            const uint32_t lo_ = __builtin_amdgcn_readlane(place_lo, 2 * (i & 31) + half);
+            const uint32_t hi_ = __builtin_amdgcn_readlane(place_hi, 2 * (i & 31) + half);
+            good[half] = hi_ != ~0u;
+            token[half] = good[half] ? (static_cast<unsigned long long>(hi_) << 32) | lo_ : static_cast<unsigned long long>(h) << a.page_log2;
+            const u4* kp = reinterpret_cast<const u4*>(a.K_codes + token[half] * (16 * BITS));
+            const u4* vp = reinterpret_cast<const u4*>(a.V_codes + token[half] * (16 * BITS));
 #pragma unroll
-            for (int i = 0; i < BITS / 4; ++i) {
-                const u4 x = reinterpret_cast<const u4*>(kp)[i];
-                kw[4 * i] = x.x; kw[4 * i + 1] = x.y; kw[4 * i + 2] = x.z; kw[4 * i + 3] = x.w;
-                const u4 y = reinterpret_cast<const u4*>(vp)[i];
-                vcodes[half * BITS + 4 * i] = y.x; vcodes[half * BITS + 4 * i + 1] = y.y;
-                vcodes[half * BITS + 4 * i + 2] = y.z; vcodes[half * BITS + 4 * i + 3] = y.w;
+            for (int x = 0; x < BITS / 4; ++x) {
+                const u4 y = kp[(n * 4 + g) * (BITS / 4) + x], z = vp[(g * 16 + n) * (BITS / 4) + x];
+                kraw[half][4 * x] = y.x; kraw[half][4 * x + 1] = y.y; kraw[half][4 * x + 2] = y.z; kraw[half][4 * x + 3] = y.w;
+                vraw[half * BITS + 4 * x] = z.x; vraw[half * BITS + 4 * x + 1] = z.y;
+                vraw[half * BITS + 4 * x + 2] = z.z; vraw[half * BITS + 4 * x + 3] = z.w;
             }
-            const u2 ksr = *reinterpret_cast<const u2*>(a.K_scale + token + 4 * g);
-            const u2 vsr = *reinterpret_cast<const u2*>(a.V_scale + token + 4 * g);
+        }
+        const unsigned long long at = (s_half ? token[1] : token[0]) + s_token;
+        ks_raw = a.K_scale[at];
+        vs_raw = a.V_scale[at];
+        there = (s_half ? good[1] : good[0]) && j0 + 16 * s_half + s_token < span.tokens;
+    };
+
+    // M: what a row's exponents are relative to.  It follows the row's maximum by more than kSlack powers of two, up, and
+    // is set to it with the row's first token (`low` is infinite until then).
+    float M = 0.0f, low = __builtin_inff(), l_sum = 0.0f;
+    f4 o[8] = {};
+
+    const int turns = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
+    if (turns > 0) {
+        load_places(0);
+        fetch(0);
+    }
+    for (int i = 0; i < turns; ++i) {
+        uint32_t kc[2][BITS], vc[2 * BITS];
+#pragma unroll
+        for (int x = 0; x < BITS; ++x) {
+            kc[0][x] = kraw[0][x];
+            kc[1][x] = kraw[1][x];
+            vc[x] = vraw[x];
+            vc[BITS + x] = vraw[BITS + x];
+        }
+        const float ks = __half2float(__ushort_as_half(static_cast<unsigned short>(ks_raw)));
+        const float vs = __half2float(__ushort_as_half(static_cast<unsigned short>(vs_raw)));
+        const bool here = there;
+        if (i + 1 < turns) {
+            if (((i + 1) & 31) == 0) load_places(i + 1);
+            fetch(i + 1);
+        }
+        // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
+        const float vsf = vs == 0.0f ? 0x1p-24f : vs;
+        const float kf = here ? __builtin_fmaf(ks, key_factor, ks * 0.0f) : 0.0f;      // NaN where ks is not finite
+        const float lv = here ? __builtin_amdgcn_logf(vsf) : -__builtin_inff();
+        const float rv = here && vsf <= 65504.0f ? __builtin_amdgcn_rcpf(vsf) : 0.0f;
+        const int st = step0 + wave + kAttnWaves * i;
+        const int j0 = st * kStep + span.base;
+
+        float x[8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
             f4 s = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS>(kw + j * (BITS / 4)), q[j], s, 0, 0, 0);
+                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS>(kc[half] + j * (BITS / 4)), q[j], s, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float ks = __half2float(__ushort_as_half(static_cast<unsigned short>((r & 2 ? ksr.y : ksr.x) >> (16 * (r & 1)))));
-                const float vs = __half2float(__ushort_as_half(static_cast<unsigned short>((r & 2 ? vsr.y : vsr.x) >> (16 * (r & 1)))));
-                const int j = jt + 4 * g + r;
-                const int dist = pos - (j + span.base);
-                float z = __builtin_fmaf(s[r], ks, ks * 0.0f);   // NaN where ks is not finite, whatever s is
-                z = a.softcap > 0.0f ? tanh_fast(z * to_cap) * to_log2 : z * to_log2;
-                z -= slope * __builtin_fabsf(static_cast<float>(dist));
-                bool seen = there && j < span.tokens;
-                if (a.causal) seen = seen && (dist >= 0 || j + span.base < both);
-                if (a.window > 0) seen = seen && abs(dist) < a.window;
-                // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
-                const float vsf = vs == 0.0f ? 0x1p-24f : vs;
-                const float x = seen ? z + __builtin_amdgcn_logf(vsf) : -__builtin_inff();
-                tt[4 * half + r] = x;
-                rvs[4 * half + r] = vsf <= 65504.0f && seen ? __builtin_amdgcn_rcpf(vsf) : 0.0f;
-                top = __builtin_fmaxf(top, x);
+            for (int r = 0; r < 4; ++r) x[4 * half + r] = s[r];
+        }
+        auto exponent = [&](int e, float k, float lm) __attribute__((always_inline)) {
+            if (FANCY) {
+                float z = x[e] * k;
+                if (capped) z = tanh_fast(z) * to_log2;
+                z = __builtin_fmaf(-slope, __builtin_fabsf(static_cast<float>(pos - (j0 + 16 * (e >> 2) + 4 * g + (e & 3)))), z);
+                x[e] = z + lm;
+            } else {
+                x[e] = __builtin_fmaf(x[e], k, lm);
+            }
+        };
+        exponent(0, row_lane<0>(kf), row_lane<0>(lv) - M);
+        exponent(1, row_lane<1>(kf), row_lane<1>(lv) - M);
+        exponent(2, row_lane<2>(kf), row_lane<2>(lv) - M);
+        exponent(3, row_lane<3>(kf), row_lane<3>(lv) - M);
+        exponent(4, row_lane<4>(kf), row_lane<4>(lv) - M);
+        exponent(5, row_lane<5>(kf), row_lane<5>(lv) - M);
+        exponent(6, row_lane<6>(kf), row_lane<6>(lv) - M);
+        exponent(7, row_lane<7>(kf), row_lane<7>(lv) - M);
+        if (st < whole0 || st >= whole1) {
+            asm volatile("" ::: "memory");     // keeps this a branch
+            const int rel = pos - j0 - 4 * g;
+            const int end = a.causal ? max(rel, both - j0 - 4 * g - 1) : 32;
+            const int off = a.window > 0 ? rel + a.window - 1 : 32;
+            const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = 16 * (e >> 2) + (e & 3);
+                const bool seen = (end >= c) & (static_cast<uint32_t>(off - c) < wide);
+                x[e] = seen ? x[e] : -__builtin_inff();
             }
         }
+        float top = x[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = __builtin_fmaxf(top, x[e]);
         top = max_over_groups(top);
-        const float M_new = __builtin_fmaxf(M, top);
-        const float M_use = M_new == -__builtin_inff() ? 0.0f : M_new;
-        const float keep = __builtin_amdgcn_exp2f(M - M_use);
-        M = M_new;
-        l_sum *= keep;
+        if (__ballot(top > kSlack || top < low) != 0) {
+            const bool none = top == -__builtin_inff(), first = low > 0.0f;
+            const float up = none ? 0.0f : first ? top : __builtin_fmaxf(top, 0.0f);
+            const float keep = first ? 0.0f : __builtin_amdgcn_exp2f(-up);     // nothing is kept of nothing, whatever up is
+            low = none ? low : -__builtin_inff();
+            M += up;
+            l_sum *= keep;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] *= keep;
+            for (int j = 0; j < 8; ++j) o[j] *= keep;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f2 w = {__builtin_amdgcn_exp2f(tt[2 * i] - M_use), __builtin_amdgcn_exp2f(tt[2 * i + 1] - M_use)};
-            l_sum = __builtin_fmaf(w.x, rvs[2 * i], __builtin_fmaf(w.y, rvs[2 * i + 1], l_sum));
+            for (int e = 0; e < 8; ++e) x[e] -= up;
+        }
+        const float r8[8] = {row_lane<0>(rv), row_lane<1>(rv), row_lane<2>(rv), row_lane<3>(rv),
+                             row_lane<4>(rv), row_lane<5>(rv), row_lane<6>(rv), row_lane<7>(rv)};
+        h8 w_op;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f2 w = {__builtin_amdgcn_exp2f(x[2 * e]), __builtin_amdgcn_exp2f(x[2 * e + 1])};
+            l_sum = __builtin_fmaf(w.x, r8[2 * e], __builtin_fmaf(w.y, r8[2 * e + 1], l_sum));
             const h2 p = __builtin_convertvector(w, h2);
-            w_op[2 * i] = p.x;
-            w_op[2 * i + 1] = p.y;
+            w_op[2 * e] = p.x;
+            w_op[2 * e + 1] = p.y;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<BITS>(vcodes, j), w_op, o[j], 0, 0, 0);
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<BITS>(vc, j), w_op, o[j], 0, 0, 0);
     }
+    if (low > 0.0f) M = -__builtin_inff();     // no token seen
 
     // join the waves
     l_sum = sum_over_groups(l_sum);
@@ -361,7 +455,6 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / 64;
 constexpr int kTileTokens = 64;            // tokens staged at a time
-constexpr float kSlack = 8.0f;             // a row's maximum may lag by this many powers of two
 
 // Two tokens' code j of an octet (w: BITS / 4 dwords a token) as fp16.
 template <int BITS>
@@ -380,11 +473,6 @@ __device__ __forceinline__ float swap_halves_sum(float v) {
     return __uint_as_float(s.x) + __uint_as_float(s.y);
 }
 
-template <int N>
-__device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes of a row, for all of them
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
-}
-
 // A barrier that orders the waves, and keeps the compiler's order, without waiting for loads in flight.
 __device__ __forceinline__ void part_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -397,8 +485,8 @@ __device__ __forceinline__ void part_barrier() {
 // which the workgroup turns into fp16 codes in LDS once, keys as [token][d] and
 // values as [d][token].
 template <int BITS, int ROWS, bool FANCY>
-__global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits,
-                                                                int own_tiles, int own_splits) {
+__global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
+                                                                int own_tiles, int own_splits, int own_chunk) {
     constexpr bool kPair = ROWS == 128;            // two waves a row
     constexpr int kBuffers = kPair ? 3 : 2;
     // Rows of one chunk more than they hold, so that eight rows' same chunk lies in different banks and every address
@@ -506,7 +594,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     hi = __builtin_amdgcn_readfirstlane(hi);
     int step0 = lo / kTileTokens;
     const int steps_all = hi > lo ? (hi + kTileTokens - 1) / kTileTokens - step0 : 0;
-    const int share = max((steps_all + splits - 1) / splits, kSplitMinTokens / kTileTokens);
+    const int share = max((steps_all + splits - 1) / splits, (shared ? prefix_chunk : own_chunk) / kTileTokens);
     const int steps = __builtin_amdgcn_readfirstlane(max(0, min(share, steps_all - split * share)));
     step0 = __builtin_amdgcn_readfirstlane(step0 + split * share);
 
@@ -887,79 +975,130 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     if (total_splits > 1 && hf == 0) *reinterpret_cast<f2*>(partial + 128) = f2{l == 0.0f ? -__builtin_inff() : M, l};
 }
 
-// Joins the shares of a row: one wave a row, two values a lane.
+// Joins the shares of a row: one wave a row, two values a lane, eight shares'
+// sums in flight.  Shares without a visible token have not written their sums,
+// and are not read.
 __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int splits) {
     const long long rows = static_cast<long long>(a.T) * a.Hq;
     const long long at = static_cast<long long>(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
     if (at >= rows) return;
-    const int t = static_cast<int>(at / a.Hq);
-    if (find_sequence(a.q_start, a.B, t) < 0) return;
     const int lane = threadIdx.x & 63;
-    float M = -__builtin_inff();
-    for (int s = 0; s < splits; ++s) {
-        M = __builtin_fmaxf(M, a.partial[(s * rows + at) * kPartial + 128]);
-    }
-    float l = 0.0f;
+    if (find_sequence(a.q_start, a.B, static_cast<int>(at / a.Hq)) < 0) return;
+    const float* row = a.partial + at * kPartial;
+    float M = -__builtin_inff(), l = 0.0f;
     f2 o = {};
-    for (int s = 0; s < splits; ++s) {
-        const float* p = a.partial + (s * rows + at) * kPartial;
-        if (p[129] == 0.0f) continue;      // no visible token there: the sums are not written
-        const float f = __builtin_amdgcn_exp2f(p[128] - M);
-        const f2 x = reinterpret_cast<const f2*>(p)[lane];
-        l = __builtin_fmaf(p[129], f, l);
-        o.x = __builtin_fmaf(x.x, f, o.x);
-        o.y = __builtin_fmaf(x.y, f, o.y);
+    for (int s0 = 0; s0 < splits; s0 += 64) {
+        // 64 shares' maxima and sums at once, a lane each
+        f2 ml = {-__builtin_inff(), 0.0f};
+        if (s0 + lane < splits) ml = *reinterpret_cast<const f2*>(row + (s0 + lane) * rows * kPartial + 128);
+        float top = max_over_groups(ml.x);
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
+        const float M_new = __builtin_fmaxf(M, top);
+        if (M_new == -__builtin_inff() && __ballot(ml.y != 0.0f) == 0) continue;
+        const float keep = M == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(M - M_new);
+        l *= keep;
+        o *= keep;
+        M = M_new;
+        const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);
+        unsigned long long left = __ballot(ml.y != 0.0f);
+        while (left != 0) {
+            f2 y[8];
+            float fs[8], ls[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool any = left != 0;
+                const int s = any ? __builtin_ctzll(left) : 0;
+                left &= left - 1;
+                fs[i] = any ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s)) : 0.0f;
+                ls[i] = any ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml.y), s)) : 0.0f;
+                y[i] = any ? reinterpret_cast<const f2*>(row + (s0 + s) * rows * kPartial)[lane] : f2{};
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                l = __builtin_fmaf(ls[i], fs[i], l);
+                o.x = __builtin_fmaf(y[i].x, fs[i], o.x);
+                o.y = __builtin_fmaf(y[i].y, fs[i], o.y);
+            }
+        }
     }
     const float rl = l == 0.0f ? 0.0f : 1.0f / l;
     const h2 res = {static_cast<_Float16>(o.x * rl), static_cast<_Float16>(o.y * rl)};
     reinterpret_cast<h2*>(a.O)[at * 64 + lane] = res;
 }
 
-// Grid of a call: rows of a tile, tiles, and the shares their tokens are split into.
+// How the rows on one stretch of tokens, a shared prefix or the sequences' own, are dealt out: rows of a tile, tiles,
+// shares of the tokens and the fewest tokens of one.
+struct Part {
+    int rows;                      // 16: kv_attn_rows16; 128, 256: kv_attn_tile; 0: no tokens
+    long long tiles;
+    int splits, chunk;
+};
+
 struct Plan {
-    int rows;                      // kRows: kv_attn_rows16; ROWS: kv_attn_tile
-    long long prefix_tiles, own_tiles;
-    int prefix_splits, own_splits;
+    Part prefix, own;
+    int splits;
     size_t workspace;
 };
 
-Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
-    const long long G = Hq / Hkv;
-    Plan p = {};
-    // rows that read the same tokens: of a sequence on average, of all sequences in a shared prefix
-    const long long together = prefix_len > 0 ? T * G : T * G / B;
+// `together`: rows on the same tokens; `ragged`: every group's rows begin a tile; `groups`: stretches of tokens (sequences, or one prefix); `tokens`: the most of one
+Part deal(long long rows, long long groups, long long together, bool ragged, int Hkv, int tokens) {
+    Part p = {};
+    if (tokens <= 0) return p;
     p.rows = together >= kWideRows ? 256 : together >= kManyRows ? 128 : kRows;
-    const long long wanted = p.rows == kRows ? 2048 : 512;      // workgroups that fill the card
-    p.own_tiles = T * G / p.rows + B;
-    p.prefix_tiles = prefix_len > 0 ? (T * G + p.rows - 1) / p.rows : 0;
-    auto shares = [&](long long tiles, int tokens) __attribute__((always_inline)) {
-        const long long most = (tokens + kSplitMinTokens - 1) / kSplitMinTokens;
-        const long long want = (wanted + tiles * Hkv - 1) / (tiles * Hkv);
-        return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
-    };
-    p.own_splits = shares(p.own_tiles, max_kv);
-    p.prefix_splits = prefix_len > 0 ? shares(p.prefix_tiles, prefix_len) : 0;
-    const int all = p.own_splits + p.prefix_splits;
-    p.workspace = all > 1 ? static_cast<size_t>(all) * T * Hq * kPartial * sizeof(float) : 0;
+    p.tiles = ragged ? rows / p.rows + groups : (rows + p.rows - 1) / p.rows;
+    const long long busy = (rows / p.rows > groups ? rows / p.rows : groups) * Hkv;     // workgroups with rows
+    const long long wanted = p.rows == kRows ? kRowsWanted : kTilesWanted;
+    const int least = p.rows == kRows ? kRowsLeast : kTilesLeast;
+    long long splits = (wanted + busy - 1) / busy;
+    if (splits * least > tokens) splits = (tokens + least - 1) / least;
+    if (splits > kMostSplits) splits = kMostSplits;
+    p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    // many sequences: shares of one size, so that a long one does not hold up the rest; few: equal shares of each
+    const int even = (tokens + p.splits - 1) / p.splits;
+    p.chunk = groups * Hkv >= kRowsWanted / 4 && even > least ? even : least;
     return p;
 }
 
-template <int BITS, int ROWS>
-void launch_tile(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(items * a.Hkv));
-    const int pt = static_cast<int>(p.prefix_tiles), ot = static_cast<int>(p.own_tiles);
-    if (a.softcap > 0.0f || a.slopes)
-        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, true>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
+    const long long rows = static_cast<long long>(T) * (Hq / Hkv);
+    Plan p = {};
+    p.prefix = deal(rows, 1, rows, false, Hkv, prefix_len);
+    p.own = deal(rows, B, rows / B, true, Hkv, max_kv);
+    p.splits = p.prefix.splits + p.own.splits;
+    p.workspace = p.splits > 1 ? static_cast<size_t>(p.splits) * T * Hq * kPartial * sizeof(float) : 0;
+    return p;
+}
+
+template <int BITS, int ROWS, bool FANCY>
+hipError_t launch_part(const KvAttnArgs& a, const Part& prefix, const Part& own, hipStream_t s) {
+    const unsigned items = static_cast<unsigned>(prefix.tiles * prefix.splits + own.tiles * own.splits);
+    const int pt = static_cast<int>(prefix.tiles), ot = static_cast<int>(own.tiles);
+    if constexpr (ROWS == kRows)
+        hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY>), dim3(items, a.Hkv), dim3(kAttnThreads), 0, s, a, pt, prefix.splits,
+                           prefix.chunk, ot, own.splits, own.chunk);
     else
-        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, false>), grid, dim3(kTileThreads), 0, s, a, pt, p.prefix_splits, ot, p.own_splits);
+        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, FANCY>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
+                           prefix.splits, prefix.chunk, ot, own.splits, own.chunk);
+    return hipGetLastError();
+}
+
+template <int BITS, int ROWS>
+hipError_t launch_rows(const KvAttnArgs& a, Part prefix, Part own, hipStream_t s) {
+    // a part with another tile has a launch of its own; its share of the workspace stays where it is
+    if (prefix.rows != ROWS) prefix.tiles = 0;
+    if (own.rows != ROWS) own.tiles = 0;
+    if (prefix.tiles == 0 && own.tiles == 0) return hipSuccess;
+    return a.softcap > 0.0f || a.slopes ? launch_part<BITS, ROWS, true>(a, prefix, own, s)
+                                        : launch_part<BITS, ROWS, false>(a, prefix, own, s);
 }
 
 template <int BITS>
-void launch_rows(const KvAttnArgs& a, const Plan& p, long long items, hipStream_t s) {
-    if (p.rows == 256) return launch_tile<BITS, 256>(a, p, items, s);
-    if (p.rows == 128) return launch_tile<BITS, 128>(a, p, items, s);
-    hipLaunchKernelGGL(kv_attn_rows16<BITS>, dim3(static_cast<unsigned>(items), a.Hkv), dim3(kAttnThreads), 0, s, a,
-                       static_cast<int>(p.prefix_tiles), p.prefix_splits, static_cast<int>(p.own_tiles), p.own_splits);
+hipError_t launch_bits(const KvAttnArgs& a, const Plan& p, hipStream_t s) {
+    hipError_t e = launch_rows<BITS, 256>(a, p.prefix, p.own, s);
+    if (e == hipSuccess) e = launch_rows<BITS, 128>(a, p.prefix, p.own, s);
+    if (e == hipSuccess) e = launch_rows<BITS, kRows>(a, p.prefix, p.own, s);
+    return e;
 }
 
 }  // namespace
@@ -970,20 +1109,18 @@ size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_l
 
 bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const Plan p = plan(T, Hq, Hkv, B, max_kv, prefix_len);
-    constexpr long long kMost = (1LL << 24) - 1;   // workgroups of 256 in a launch dimension
-    return (p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits) * Hkv <= kMost && Hkv <= 65535 &&
+    constexpr long long kMost = (1LL << 23) - 1;   // workgroups of 512 in a launch dimension
+    return (p.prefix.tiles * p.prefix.splits + p.own.tiles * p.own.splits) * Hkv <= kMost && Hkv <= 65535 &&
            (static_cast<long long>(T) * Hq + kAttnWaves - 1) / kAttnWaves <= kMost;
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s) {
     const Plan p = plan(a.T, a.Hq, a.Hkv, a.B, a.max_pages << a.page_log2, a.prefix_len);
-    const long long items = p.prefix_tiles * p.prefix_splits + p.own_tiles * p.own_splits;
-    bits == 8 ? launch_rows<8>(a, p, items, s) : launch_rows<4>(a, p, items, s);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.own_splits + p.prefix_splits == 1) return e;
+    const hipError_t e = bits == 8 ? launch_bits<8>(a, p, s) : launch_bits<4>(a, p, s);
+    if (e != hipSuccess || p.splits == 1) return e;
     const long long rows = static_cast<long long>(a.T) * a.Hq;
     hipLaunchKernelGGL(kv_attn_join, dim3(static_cast<unsigned>((rows + kAttnWaves - 1) / kAttnWaves)), dim3(kAttnThreads), 0,
-                       s, a, p.own_splits + p.prefix_splits);
+                       s, a, p.splits);
     return hipGetLastError();
 }
 
