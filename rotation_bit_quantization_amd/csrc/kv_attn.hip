@@ -39,7 +39,8 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
 // Workgroups that fill the card, and the fewest tokens worth one, of the two kernels; the most shares of a row's tokens.
-constexpr int kRowsWanted = 1536, kRowsLeast = 256;
+constexpr int kRowsWanted = 1024, kRowsWantedUneven = 2304, kRowsLeast = 128;
+constexpr int kManyGroups = 384;          // (sequence, head) pairs from which shares have one size for all sequences
 constexpr int kTilesWanted = 256, kTilesLeast = 256;
 constexpr int kMostSplits = 256;
 constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
@@ -81,7 +82,21 @@ __device__ __forceinline__ h8 key_operand(const uint32_t* w) {
     return f.v;
 }
 
-// Code j of an octet, of eight tokens: w[BITS / 4 * token + ...], as an operand.
+// The same without the subtraction: u = code + 8 (128) as the fp16 number u 2^-24, subnormal, which the matrix cores
+// take as it is.  The sum over a query is then 2^-24 (sum q code + 8 sum q): the second term goes into the accumulator
+// that the sum starts from.
+template <int BITS>
+__device__ __forceinline__ h8 key_operand_small(const uint32_t* w) {
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f.w[i] = BITS == 4 ? ((w[0] >> (4 * i)) & 0x000F000Fu) ^ 0x00080008u
+                           : ((w[i >> 1] >> (8 * (i & 1))) & 0x00FF00FFu) ^ 0x00800080u;
+    return f.v;
+}
+
+// Code j of an octet, of eight tokens: w[BITS / 4 * token + ...], as an operand; 16 times the code for odd j at 4 bits,
+// where it is not shifted down.
 template <int BITS>
 __device__ __forceinline__ h8 value_operand(const uint32_t* w, int j) {
     Frag f;
@@ -92,7 +107,7 @@ __device__ __forceinline__ h8 value_operand(const uint32_t* w, int j) {
     for (int i = 0; i < 4; ++i) {
         const uint32_t x = __builtin_amdgcn_perm(w[kW * (2 * i) + dw], w[kW * (2 * i + 1) + dw], sel);
         if (BITS == 4)
-            f.w[i] = minus(((j & 1 ? x >> 4 : x) & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
+            f.w[i] = j & 1 ? minus((x & 0x00F000F0u) ^ 0x64806480u, 1152.0f) : minus((x & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
         else
             f.w[i] = minus(x ^ 0x64806480u, 1152.0f);
     }
@@ -149,10 +164,15 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int h = blockIdx.y, G = a.Hq / a.Hkv;
+    const int G = a.Hq / a.Hkv;
+    // Workgroup L runs on XCD L % 8: the heads of an item follow each other on one, so that the lines that hold several
+    // heads' scales come into one L2.
+    const int h = (blockIdx.x >> 3) % a.Hkv;
+    const int index = (blockIdx.x >> 3) / a.Hkv * 8 + (blockIdx.x & 7);
     const int prefix_items = prefix_tiles * prefix_splits;
-    const bool shared = static_cast<int>(blockIdx.x) < prefix_items;
-    const int item = shared ? blockIdx.x : blockIdx.x - prefix_items;
+    if (index >= prefix_items + own_tiles * own_splits) return;
+    const bool shared = index < prefix_items;
+    const int item = shared ? index : index - prefix_items;
     const int splits = shared ? prefix_splits : own_splits;
     const int tile = item / splits, split = item - tile * splits;
     const int first_slot = shared ? 0 : prefix_splits;   // of the workspace
@@ -172,13 +192,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
     } else {
         // sequence b's tiles start at tile floor(q_start[b] G / 16) + b: room for each one's ragged last tile
-        int lo = 0, c = a.B;
-        while (c > 1) {
-            const int half = c >> 1;
-            const bool before = static_cast<long long>(a.q_start[lo + half]) * G / kRows + lo + half <= tile;
-            lo += before ? half : 0;
-            c = before ? c - half : half;
-        }
+        const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / kRows + i <= tile; });
         b = lo;
         const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
         const long long r = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / kRows + b)) * kRows + n;
@@ -241,9 +255,21 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
             q[j] = f.v;
         }
     }
+    // what the sum over a query starts from (key_operand_small)
+    f4 start;
+    {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += static_cast<float>(q[j][e]);
+        }
+        const float c = sum_over_groups(sum) * (BITS == 4 ? -0x1p-21f : -0x1p-17f);
+        start = f4{c, c, c, c};
+    }
     const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
     const bool capped = FANCY && a.softcap > 0.0f;
-    const float key_factor = capped ? a.scale / a.softcap : a.scale * kLog2e;
+    const float key_factor = (capped ? a.scale / a.softcap : a.scale * kLog2e) * 0x1p24f;
     const float to_log2 = a.softcap * kLog2e;
 
     // Of the wave's next 32 steps, a lane each and half of a step: where the 16 tokens lie, as the number of the first, ~0
@@ -257,37 +283,49 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         place_lo = good ? static_cast<uint32_t>(token) : ~0u;
         place_hi = good ? static_cast<uint32_t>(token >> 32) : ~0u;
     };
-    // A step's codes and scales, loaded a step ahead.  Lane (n, g) takes 32 codes of token n of each 16 and an octet of
-    // tokens 4 g .. 4 g + 3, and the scales of one token: of lanes 0 .. 7 of a row of 16 lanes token 4 g + l of the first
-    // 16 (l < 4) or 4 g + l - 4 of the second, lanes 8 .. 15 again.
-    uint32_t kraw[2][BITS], vraw[2 * BITS];
-    uint32_t ks_raw = 0, vs_raw = 0;
+    // A step's codes and scales.  Lane (n, g) takes 32 codes of token n of each 16 and an octet of tokens 4 g .. 4 g + 3,
+    // and the scales of one token: of lanes 0 .. 7 of a row of 16 lanes token 4 g + l of the first 16 (l < 4) or 4 g + l - 4
+    // of the second, lanes 8 .. 15 again.  The next step's keys are loaded as soon as these are used, the values as soon
+    // as these are: each load has the other half of a step to arrive in, with one set of registers, so that four waves
+    // fit a SIMD (two sets, three waves: 91 instead of 85 us at 64 sequences of up to 8192).
+    uint32_t kraw[2][BITS], vraw[2 * BITS], ks_raw = 0, vs_raw = 0;
     bool there = false;
     const int s_half = (n >> 2) & 1, s_token = 4 * g + (n & 3);
-    auto fetch = [&](int i) __attribute__((always_inline)) {
-        const int j0 = (step0 + wave + kAttnWaves * i) * kStep;
-        unsigned long long token[2];
+    auto place = [&](int i, int half, bool& good) __attribute__((always_inline)) {
+        const uint32_t lo_ = __builtin_amdgcn_readlane(place_lo, 2 * (i & 31) + half);
+        const uint32_t hi_ = __builtin_amdgcn_readlane(place_hi, 2 * (i & 31) + half);
+        good = hi_ != ~0u;
+        return good ? (static_cast<unsigned long long>(hi_) << 32) | lo_ : static_cast<unsigned long long>(h) << a.page_log2;
+    };
+    auto fetch_keys = [&](int i) __attribute__((always_inline)) {
         bool good[2];
+        const unsigned long long token[2] = {place(i, 0, good[0]), place(i, 1, good[1])};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint32_t lo_ = __builtin_amdgcn_readlane(place_lo, 2 * (i & 31) + half);
-            const uint32_t hi_ = __builtin_amdgcn_readlane(place_hi, 2 * (i & 31) + half);
-            good[half] = hi_ != ~0u;
-            token[half] = good[half] ? (static_cast<unsigned long long>(hi_) << 32) | lo_ : static_cast<unsigned long long>(h) << a.page_log2;
             const u4* kp = reinterpret_cast<const u4*>(a.K_codes + token[half] * (16 * BITS));
-            const u4* vp = reinterpret_cast<const u4*>(a.V_codes + token[half] * (16 * BITS));
 #pragma unroll
             for (int x = 0; x < BITS / 4; ++x) {
-                const u4 y = kp[(n * 4 + g) * (BITS / 4) + x], z = vp[(g * 16 + n) * (BITS / 4) + x];
+                const u4 y = kp[(n * 4 + g) * (BITS / 4) + x];
                 kraw[half][4 * x] = y.x; kraw[half][4 * x + 1] = y.y; kraw[half][4 * x + 2] = y.z; kraw[half][4 * x + 3] = y.w;
-                vraw[half * BITS + 4 * x] = z.x; vraw[half * BITS + 4 * x + 1] = z.y;
-                vraw[half * BITS + 4 * x + 2] = z.z; vraw[half * BITS + 4 * x + 3] = z.w;
             }
         }
         const unsigned long long at = (s_half ? token[1] : token[0]) + s_token;
         ks_raw = a.K_scale[at];
         vs_raw = a.V_scale[at];
-        there = (s_half ? good[1] : good[0]) && j0 + 16 * s_half + s_token < span.tokens;
+        there = (s_half ? good[1] : good[0]) && (step0 + wave + kAttnWaves * i) * kStep + 16 * s_half + s_token < span.tokens;
+    };
+    auto fetch_values = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            bool good;
+            const u4* vp = reinterpret_cast<const u4*>(a.V_codes + place(i, half, good) * (16 * BITS));
+#pragma unroll
+            for (int x = 0; x < BITS / 4; ++x) {
+                const u4 z = vp[(g * 16 + n) * (BITS / 4) + x];
+                vraw[half * BITS + 4 * x] = z.x; vraw[half * BITS + 4 * x + 1] = z.y;
+                vraw[half * BITS + 4 * x + 2] = z.z; vraw[half * BITS + 4 * x + 3] = z.w;
+            }
+        }
     };
 
     // M: what a row's exponents are relative to.  It follows the row's maximum by more than kSlack powers of two, up, and
@@ -298,24 +336,13 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     const int turns = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
     if (turns > 0) {
         load_places(0);
-        fetch(0);
+        fetch_keys(0);
+        fetch_values(0);
     }
     for (int i = 0; i < turns; ++i) {
-        uint32_t kc[2][BITS], vc[2 * BITS];
-#pragma unroll
-        for (int x = 0; x < BITS; ++x) {
-            kc[0][x] = kraw[0][x];
-            kc[1][x] = kraw[1][x];
-            vc[x] = vraw[x];
-            vc[BITS + x] = vraw[BITS + x];
-        }
         const float ks = __half2float(__ushort_as_half(static_cast<unsigned short>(ks_raw)));
         const float vs = __half2float(__ushort_as_half(static_cast<unsigned short>(vs_raw)));
         const bool here = there;
-        if (i + 1 < turns) {
-            if (((i + 1) & 31) == 0) load_places(i + 1);
-            fetch(i + 1);
-        }
         // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
         const float vsf = vs == 0.0f ? 0x1p-24f : vs;
         const float kf = here ? __builtin_fmaf(ks, key_factor, ks * 0.0f) : 0.0f;      // NaN where ks is not finite
@@ -327,13 +354,17 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         float x[8];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            f4 s = {};
+            f4 s = start;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS>(kc[half] + j * (BITS / 4)), q[j], s, 0, 0, 0);
+                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand_small<BITS>(kraw[half] + j * (BITS / 4)), q[j], s, 0, 0, 0);
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[4 * half + r] = s[r];
         }
+        // behind the last step it is loaded once more, for nothing
+        const int next = i + 1 < turns ? i + 1 : i;
+        if ((next & 31) == 0 && next > 0) load_places(next);
+        fetch_keys(next);
         auto exponent = [&](int e, float k, float lm) __attribute__((always_inline)) {
             if (FANCY) {
                 float z = x[e] * k;
@@ -394,7 +425,12 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<BITS>(vc, j), w_op, o[j], 0, 0, 0);
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<BITS>(vraw, j), w_op, o[j], 0, 0, 0);
+        fetch_values(next);
+    }
+    if (BITS == 4) {
+#pragma unroll
+        for (int j = 1; j < 8; j += 2) o[j] *= 0.0625f;      // 16 times the code
     }
     if (low > 0.0f) M = -__builtin_inff();     // no token seen
 
@@ -531,13 +567,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         }
     } else {
         // sequence b's tiles start at tile floor(q_start[b] G / rows) + b: room for each one's ragged last tile
-        int lo = 0, c = a.B;
-        while (c > 1) {
-            const int half = c >> 1;
-            const bool before = static_cast<long long>(a.q_start[lo + half]) * G / ROWS + lo + half <= tile;
-            lo += before ? half : 0;
-            c = before ? c - half : half;
-        }
+        const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / ROWS + i <= tile; });
         const int b = lo;
         const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
         const long long first = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / ROWS + b)) * ROWS;
@@ -983,7 +1013,9 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int s
     const long long at = static_cast<long long>(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
     if (at >= rows) return;
     const int lane = threadIdx.x & 63;
-    if (find_sequence(a.q_start, a.B, static_cast<int>(at / a.Hq)) < 0) return;
+    const int t = static_cast<int>(at / a.Hq);
+    const int b = find_last64(a.B, lane, [&](int i) { return a.q_start[i] <= t; });
+    if (t < a.q_start[b] || t >= a.q_start[b + 1]) return;
     const float* row = a.partial + at * kPartial;
     float M = -__builtin_inff(), l = 0.0f;
     f2 o = {};
@@ -1048,7 +1080,8 @@ Part deal(long long rows, long long groups, long long together, bool ragged, int
     p.rows = together >= kWideRows ? 256 : together >= kManyRows ? 128 : kRows;
     p.tiles = ragged ? rows / p.rows + groups : (rows + p.rows - 1) / p.rows;
     const long long busy = (rows / p.rows > groups ? rows / p.rows : groups) * Hkv;     // workgroups with rows
-    const long long wanted = p.rows == kRows ? kRowsWanted : kTilesWanted;
+    const bool uneven = groups * Hkv >= kManyGroups;
+    const long long wanted = p.rows != kRows ? kTilesWanted : uneven ? kRowsWantedUneven : kRowsWanted;
     const int least = p.rows == kRows ? kRowsLeast : kTilesLeast;
     long long splits = (wanted + busy - 1) / busy;
     if (splits * least > tokens) splits = (tokens + least - 1) / least;
@@ -1056,7 +1089,7 @@ Part deal(long long rows, long long groups, long long together, bool ragged, int
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
     // many sequences: shares of one size, so that a long one does not hold up the rest; few: equal shares of each
     const int even = (tokens + p.splits - 1) / p.splits;
-    p.chunk = groups * Hkv >= kRowsWanted / 4 && even > least ? even : least;
+    p.chunk = uneven && even > least ? even : least;
     return p;
 }
 
@@ -1075,7 +1108,7 @@ hipError_t launch_part(const KvAttnArgs& a, const Part& prefix, const Part& own,
     const unsigned items = static_cast<unsigned>(prefix.tiles * prefix.splits + own.tiles * own.splits);
     const int pt = static_cast<int>(prefix.tiles), ot = static_cast<int>(own.tiles);
     if constexpr (ROWS == kRows)
-        hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY>), dim3(items, a.Hkv), dim3(kAttnThreads), 0, s, a, pt, prefix.splits,
+        hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY>), dim3((items + 7) / 8 * 8 * a.Hkv), dim3(kAttnThreads), 0, s, a, pt, prefix.splits,
                            prefix.chunk, ot, own.splits, own.chunk);
     else
         hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, FANCY>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
@@ -1110,7 +1143,7 @@ size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_l
 bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const Plan p = plan(T, Hq, Hkv, B, max_kv, prefix_len);
     constexpr long long kMost = (1LL << 23) - 1;   // workgroups of 512 in a launch dimension
-    return (p.prefix.tiles * p.prefix.splits + p.own.tiles * p.own.splits) * Hkv <= kMost && Hkv <= 65535 &&
+    return (p.prefix.tiles * p.prefix.splits + p.own.tiles * p.own.splits + 8) * Hkv <= kMost &&
            (static_cast<long long>(T) * Hq + kAttnWaves - 1) / kAttnWaves <= kMost;
 }
 

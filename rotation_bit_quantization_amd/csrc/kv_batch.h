@@ -30,7 +30,24 @@ __device__ __forceinline__ int find_sequence16(const int32_t* __restrict__ q_sta
     return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
-// The same by one lane alone: a binary search.
+// The last of 0 .. B - 1 that `before` holds for (it holds up to there, and not behind), or 0: by the 64 lanes of a wave
+// together, one load deep per factor of 64 in B.
+template <typename F>
+__device__ __forceinline__ int find_last64(int B, int lane, F before) {
+    int lo = 0, n = B;
+    while (n > 1) {
+        const int step = (n + 63) >> 6;
+        const int at = lane * step;
+        const bool yes = at < n && before(lo + at);
+        const int seen = __popcll(__ballot(yes));
+        const int skip = max(seen - 1, 0) * step;
+        lo += skip;
+        n = min(step, n - skip);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// The sequence of row t, or -1, by one lane alone: a binary search.
 __device__ __forceinline__ int find_sequence(const int32_t* __restrict__ q_start, int B, int t) {
     int lo = 0, n = B;
     while (n > 1) {
