@@ -1143,7 +1143,7 @@ size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_l
 bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const Plan p = plan(T, Hq, Hkv, B, max_kv, prefix_len);
     constexpr long long kMost = (1LL << 23) - 1;   // workgroups of 512 in a launch dimension
-    return (p.prefix.tiles * p.prefix.splits + p.own.tiles * p.own.splits + 8) * Hkv <= kMost &&
+    return (p.prefix.tiles * p.prefix.splits + p.own.tiles * p.own.splits + 8) * Hkv <= kMost && Hkv <= 65535 &&
            (static_cast<long long>(T) * Hq + kAttnWaves - 1) / kAttnWaves <= kMost;
 }
 

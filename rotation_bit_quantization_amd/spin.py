@@ -10,6 +10,7 @@ Declarations and contracts: include/libspin.h.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -516,17 +517,12 @@ def spin_kv_qkv(K, V, Q=None, bits=4, want_k_rot=False, out=None, stream=None):
 
 # ---------------------------------------------------------------- the paged KV cache
 
-def _launch(fn, tensors, made, stream, args):
-    """Call fn(*args, stream) on the device its tensors live on: on that device's current stream, or on
-    `stream`.  `tensors` have to share one device; `made`, the ones allocated for this call, are kept from
-    reuse until the work on another stream is done."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
-    call = getattr(load(), fn)
-    if _raw_stream is not None and _cur_device is not None and stream is None and _cur_device() == dev.index:
-        st = call(*args, _raw_stream(dev.index))
+def _launch(fn, dev, made, stream, args):
+    """Call fn(*args, stream) on GPU number `dev`: on its current stream, or on `stream`.  The tensors `made` for
+    this call are kept from reuse until the work on another stream is done."""
+    call = _entry(fn)
+    if stream is None and _raw_stream is not None and _cur_device is not None and _cur_device() == dev:
+        st = call(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
             here = torch.cuda.current_stream()
@@ -534,13 +530,36 @@ def _launch(fn, tensors, made, stream, args):
                 stream = here
             elif not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            if stream.device != dev:
-                raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {dev}")
+            if stream.device.index != dev:
+                raise ValueError(f"{fn}: a stream of {stream.device} for tensors on GPU {dev}")
             st = call(*args, stream.cuda_stream)
             if st == SPIN_OK and stream != here:
                 for t in made:
                     t.record_stream(stream)
-    _raise(fn, st)
+    if st != SPIN_OK:
+        raise SpinError(fn, st)
+
+
+@functools.lru_cache(None)
+def _entry(fn):
+    return getattr(load(), fn)
+
+
+def _want(t, name, dtype, shape, dev):
+    """Raise unless t is a contiguous tensor of this type and shape on GPU `dev`; returns its address."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, (dtype,), shape)
+    raise ValueError(f"{name} lives on {t.device}, the others on GPU {dev}")
+
+
+def _gpu(t, name):
+    """The number of the GPU a tensor lives on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU (got {t.device})")
+    return t.get_device()
 
 
 def kv_cache(n_pages, Hkv, page_size, bits=4, device="cuda"):
@@ -557,60 +576,62 @@ def kv_cache(n_pages, Hkv, page_size, bits=4, device="cuda"):
             "V_scale": torch.zeros((n_pages, Hkv, page_size), dtype=torch.float16, device=device)}
 
 
-def _cache(cache):
-    """Check a cache's four tensors; returns them with (n_pages, Hkv, page_size, bits)."""
-    kc, ks, vc, vs = (cache[name] for name in ("K_codes", "K_scale", "V_codes", "V_scale"))
-    _check(kc, "K_codes", (torch.uint8,))
+def _cache(cache, dev):
+    """Check a cache's four tensors; returns their addresses and (n_pages, Hkv, page_size, bits)."""
+    kc = cache["K_codes"]
     if kc.dim() != 4 or kc.shape[3] not in (64, 128):
         raise ValueError(f"K_codes has shape {tuple(kc.shape)}, expected [n_pages, Hkv, page_size, 64 or 128]")
-    n_pages, Hkv, page, width = kc.shape
+    shape = kc.shape
+    n_pages, Hkv, page, width = shape
     bits = width // 16
-    _check(ks, "K_scale", (torch.float16,), (n_pages, Hkv, page))
-    _check(vc, "V_codes", (torch.uint8,), (n_pages, Hkv, page // 4, 16, 4, bits))
-    _check(vs, "V_scale", (torch.float16,), (n_pages, Hkv, page))
-    return (kc, ks, vc, vs), (n_pages, Hkv, page, bits)
+    scale = (n_pages, Hkv, page)
+    return (_want(kc, "K_codes", torch.uint8, shape, dev), _want(cache["K_scale"], "K_scale", torch.float16, scale, dev),
+            _want(cache["V_codes"], "V_codes", torch.uint8, (n_pages, Hkv, page // 4, 16, 4, bits), dev),
+            _want(cache["V_scale"], "V_scale", torch.float16, scale, dev)), n_pages, Hkv, page, bits
 
 
-def _batch(page_table, q_start, kv_len):
-    """Check a batch's three arrays; returns (B, max_pages)."""
-    _check(page_table, "page_table", (torch.int32,))
+def _batch(page_table, q_start, kv_len, dev):
+    """Check a batch's three arrays; returns the addresses of q_start, kv_len and page_table and (B, max_pages)."""
     if page_table.dim() != 2:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [B, max_pages]")
-    B, max_pages = page_table.shape
-    _check(q_start, "q_start", (torch.int32,), (B + 1,))
-    _check(kv_len, "kv_len", (torch.int32,), (B,))
-    return B, max_pages
+    shape = page_table.shape
+    B, max_pages = shape
+    return (_want(q_start, "q_start", torch.int32, (B + 1,), dev), _want(kv_len, "kv_len", torch.int32, (B,), dev),
+            _want(page_table, "page_table", torch.int32, shape, dev)), B, max_pages
 
 
-def _rows(x, name, dtype, T):
-    """Check [T, H, 128] rows whose heads lie beside each other; returns (H, values from a token to the next)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.shape[0] != T or x.shape[2] != 128:
+def _rows(x, name, dtype, T, dev):
+    """Check [T, H, 128] rows whose heads lie beside each other; returns (address, H, values from a token to the
+    next)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{name} must be a [{T}, H, 128] tensor")
-    if x.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got {x.device})")
-    if x.dtype != dtype or dtype not in (torch.float16, torch.float32):
+    rows, H, D = x.shape
+    if rows != T or D != 128:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{T}, H, 128]")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} lives on {x.device}, the others on GPU {dev}")
+    if x.dtype is not dtype or dtype not in (torch.float16, torch.float32):
         raise TypeError(f"{name} has dtype {x.dtype}, expected float16 or float32, the same for all")
-    H = x.shape[1]
-    if x.numel() and (x.stride(2) != 1 or (H > 1 and x.stride(1) != 128)):
+    per_token, per_head, per_value = x.stride()
+    if T and H and (per_value != 1 or (H > 1 and per_head != 128)):
         raise ValueError(f"{name}: the heads of a token must lie beside each other (strides {x.stride()})")
-    return H, x.stride(0) if T > 1 else max(128 * H, 128)
+    return x.data_ptr(), H, per_token if T > 1 else max(128 * H, 128)
 
 
 def spin_rope_table(inv_freq, n_pos, pos0=0, attn_scale=1.0, table=None, stream=None):
     """inv_freq [n] float64 -> table [n_pos, 2 n] fp32: n cosines, then n sines of (pos0 + p) * inv_freq."""
-    _check(inv_freq, "inv_freq", (torch.float64,))
+    dev = _gpu(inv_freq, "inv_freq")
     if inv_freq.dim() != 1:
         raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [n]")
     n = inv_freq.shape[0]
-    made = []
+    freq = _want(inv_freq, "inv_freq", torch.float64, (n,), dev)
+    made = ()
     if table is None:
         table = torch.empty((n_pos, 2 * n), dtype=torch.float32, device=inv_freq.device)
-        made.append(table)
-    _check(table, "table", (torch.float32,), (n_pos, 2 * n))
-    if n_pos == 0:                  # an empty tensor has no address to pass
-        return table
-    _launch("spin_rope_table", (inv_freq, table), made, stream,
-            (_ptr(inv_freq), n, int(pos0), n_pos, float(attn_scale), _ptr(table)))
+        made = (table,)
+    out = _want(table, "table", torch.float32, (n_pos, 2 * n), dev)
+    if n_pos != 0:                  # an empty tensor has no address to pass
+        _launch("spin_rope_table", dev, made, stream, (freq, n, int(pos0), n_pos, float(attn_scale), out))
     return table
 
 
@@ -620,42 +641,41 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     fine) -> Q_out [T, Hq, 128] fp16 (or None); the codes of K and V go into the pages of ``cache``.
 
     ``rope`` is a spin_rope_table of the rotated part of a head; ``q_norm`` and ``k_norm`` are [128] fp32 weights."""
-    tensors, (n_pages, Hkv, page, bits) = _cache(cache)
-    B, max_pages = _batch(page_table, q_start, kv_len)
-    if not isinstance(K, torch.Tensor):
-        raise TypeError("K must be a torch.Tensor")
-    T = K.shape[0]
-    hk, k_stride = _rows(K, "K", K.dtype, T)
-    hv, v_stride = _rows(V, "V", K.dtype, T)
+    dev = _gpu(K, "K")
+    (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
+    (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
+    T, dtype = K.shape[0], K.dtype
+    k, hk, k_stride = _rows(K, "K", dtype, T, dev)
+    v, hv, v_stride = _rows(V, "V", dtype, T, dev)
     if hk != Hkv or hv != Hkv:
         raise ValueError(f"K has {hk} and V {hv} heads, the cache {Hkv}")
-    Hq, q_stride, made = 0, 0, []
+    q = out = None
+    Hq, q_stride, made = 0, 0, ()
     if Q is not None:
-        Hq, q_stride = _rows(Q, "Q", K.dtype, T)
+        q, Hq, q_stride = _rows(Q, "Q", dtype, T, dev)
         if Q_out is None:
             Q_out = torch.empty((T, Hq, 128), dtype=torch.float16, device=Q.device)
-            made.append(Q_out)
-        _check(Q_out, "Q_out", (torch.float16,), (T, Hq, 128))
+            made = (Q_out,)
+        out = _want(Q_out, "Q_out", torch.float16, (T, Hq, 128), dev)
     elif Q_out is not None:
         raise ValueError("Q_out without Q")
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _check(w, name, (torch.float32,), (128,))
-    rope_len = rot_dim = 0
+    qn = None if q_norm is None else _want(q_norm, "q_norm", torch.float32, (128,), dev)
+    kn = None if k_norm is None else _want(k_norm, "k_norm", torch.float32, (128,), dev)
+    rows, rope_len, rot_dim = None, 0, 0
     if rope is not None:
-        _check(rope, "rope", (torch.float32,))
+        if rope.dim() != 2:
+            raise ValueError(f"rope has shape {tuple(rope.shape)}, expected [positions, rotated values]")
         rope_len, rot_dim = rope.shape
-    if T == 0 or B == 0:            # an empty tensor has no address to pass
-        return Q_out
-    kc, ks, vc, vs = tensors
-    _launch("spin_kv_append", (K, V, Q, Q_out, q_norm, k_norm, rope, page_table, q_start, kv_len, *tensors), made, stream,
-            (_ptr(Q), _ptr(K), _ptr(V), _dtype_code(K), T, Hq, Hkv, 128, q_stride, k_stride, v_stride, _ptr(q_norm),
-             _ptr(k_norm), float(eps), _ptr(rope), rope_len, rot_dim, int(interleaved), int(pos0), bits, _ptr(kc), _ptr(ks),
-             _ptr(vc), _ptr(vs), n_pages, page, B, _ptr(q_start), _ptr(kv_len), _ptr(page_table), max_pages,
-             _ptr(Q_out)))
+        rows = _want(rope, "rope", torch.float32, rope.shape, dev)
+    if T != 0 and B != 0:           # an empty tensor has no address to pass
+        _launch("spin_kv_append", dev, made, stream,
+                (q, k, v, SPIN_F16 if dtype is torch.float16 else SPIN_F32, T, Hq, Hkv, 128, q_stride, k_stride, v_stride, qn,
+                 kn, eps, rows, rope_len, rot_dim, int(interleaved), int(pos0), bits, kc, ks, vc, vs, n_pages, page, B, starts,
+                 lens, table, max_pages, out))
     return Q_out
 
 
+@functools.lru_cache(4096)
 def spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len=0):
     """Bytes of workspace that spin_kv_attn (spin_kv_attn_shared with a prefix) takes at these sizes."""
     n = ctypes.c_size_t(0)
@@ -666,38 +686,39 @@ def spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len=0):
 
 def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O,
           workspace, stream):
-    tensors, (n_pages, Hkv, page, bits) = _cache(cache)
-    B, max_pages = _batch(page_table, q_start, kv_len)
-    _check(Q, "Q", (torch.float16,))
-    if Q.dim() != 3 or Q.shape[2] != 128:
-        raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, 128]")
-    T, Hq = Q.shape[0], Q.shape[1]
-    prefix_table, prefix_len = prefix if prefix is not None else (None, 0)
-    if slopes is not None:
-        _check(slopes, "slopes", (torch.float32,), (Hq,))
-    if bidir_len is not None:
-        _check(bidir_len, "bidir_len", (torch.int32,), (B,))
-    made = []
+    dev = _gpu(Q, "Q")
+    (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
+    (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
+    shape = Q.shape
+    if len(shape) != 3 or shape[2] != 128:
+        raise ValueError(f"Q has shape {tuple(shape)}, expected [T, Hq, 128]")
+    T, Hq, _ = shape
+    q = _want(Q, "Q", torch.float16, shape, dev)
+    slope = None if slopes is None else _want(slopes, "slopes", torch.float32, (Hq,), dev)
+    both = None if bidir_len is None else _want(bidir_len, "bidir_len", torch.int32, (B,), dev)
+    prefix_len, front = 0, ()
+    if prefix is not None:
+        prefix_len = prefix[1]
+        front = (_want(prefix[0], "prefix_table", torch.int32, prefix[0].shape, dev) or None, prefix_len)
+    made = ()
     if O is None:
-        O = torch.empty((T, Hq, 128), dtype=torch.float16, device=Q.device)
-        made.append(O)
-    _check(O, "O", (torch.float16,), (T, Hq, 128))
+        O = torch.empty_like(Q)
+        made = (O,)
+    out = _want(O, "O", torch.float16, shape, dev)
     if T == 0 or B == 0:            # an empty tensor has no address to pass
         return O
     need = spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page, prefix_len)
-    if workspace is None:
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=Q.device)
-            made.append(workspace)
-    else:
-        _check(workspace, "workspace", (torch.uint8,))
-    kc, ks, vc, vs = tensors
-    _launch(fn, (Q, O, workspace, slopes, bidir_len, prefix_table, page_table, q_start, kv_len, *tensors), made, stream,
-            (_ptr(Q), T, Hq, Hkv, 128, bits, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages, page,
-             *(() if prefix is None else (_ptr(prefix_table), prefix_len)), B, _ptr(q_start), _ptr(kv_len),
-             _ptr(page_table), max_pages, 128 ** -0.5 if scale is None else float(scale), float(softcap), _ptr(slopes),
-             int(window), int(causal), _ptr(bidir_len), _ptr(O), _ptr(workspace),
-             0 if workspace is None else workspace.numel()))
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+        ws = _want(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
+    elif need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=Q.device)
+        ws, ws_bytes = workspace.data_ptr(), need
+        made = (*made, workspace)
+    _launch(fn, dev, made, stream,
+            (q, T, Hq, Hkv, 128, bits, kc, ks, vc, vs, n_pages, page, *front, B, starts, lens, table, max_pages,
+             0.08838834764831845 if scale is None else scale, softcap, slope, int(window), int(causal), both, out, ws, ws_bytes))
     return O
 
 
@@ -715,9 +736,8 @@ def spin_kv_attn_shared(Q, cache, prefix_table, prefix_len, page_table, q_start,
                         slopes=None, window=0, causal=True, bidir_len=None, O=None, workspace=None, stream=None):
     """spin_kv_attn where the first ``prefix_len`` tokens of every sequence lie in the pages ``prefix_table``
     names ([ceil(prefix_len / page_size)] int32) and ``page_table`` and ``kv_len`` count what follows."""
-    _check(prefix_table, "prefix_table", (torch.int32,))
-    page = cache["K_codes"].shape[2]
-    if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-int(prefix_len) // page):
+    prefix_len = int(prefix_len)
+    if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-prefix_len // cache["K_codes"].shape[2]):
         raise ValueError(f"prefix_table has shape {tuple(prefix_table.shape)}, too few pages for {prefix_len} tokens")
-    return _attn("spin_kv_attn_shared", Q, cache, (prefix_table, int(prefix_len)), page_table, q_start, kv_len, scale,
+    return _attn("spin_kv_attn_shared", Q, cache, (prefix_table, prefix_len), page_table, q_start, kv_len, scale,
                  softcap, slopes, window, causal, bidir_len, O, workspace, stream)

@@ -117,8 +117,10 @@ def test_the_binding_checks_before_the_library(lib):
         spin.kv_cache(4, 2, 24, 4, device="cpu")
     c = spin.kv_cache(4, 2, 16, 8, device="cpu")
     assert c["K_codes"].shape == (4, 2, 16, 128) and c["V_codes"].shape == (4, 2, 4, 16, 4, 8)
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         spin.spin_kv_attn(None, c, None, None, None)
+    with pytest.raises(ValueError):
+        spin.spin_kv_attn(c["K_scale"], c, None, None, None)
 
 
 def test_validation_under_host_sanitizers():
