@@ -546,8 +546,8 @@ spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dty
  * one that does not is not touched by it.
  * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (bits, causal, a scale that is
  * not finite, a softcap that is negative or not finite), SPIN_ERR_BAD_SHAPE
- * (also a workspace that is too small, Hkv above 65535, and more than 2^23 - 1
- * workgroups),
+ * (also a workspace that is too small, Hkv above 65535, more than 2^22 - 1
+ * workgroups or 2^26 rows of Q),
  * SPIN_ERR_MISALIGNED (every pointer 16 bytes).
  */
 spin_status spin_kv_attn(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,

@@ -39,7 +39,8 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
 // Workgroups that fill the card, and the fewest tokens worth one, of the two kernels; the most shares of a row's tokens.
-constexpr int kRowsWanted = 1024, kRowsWantedUneven = 2304, kRowsLeast = 128;
+constexpr int kRowsWanted = 1024, kRowsLeast = 128;
+constexpr int kRowsWantedUneven = 2304, kRowsLeastUneven = 512;
 constexpr int kManyGroups = 384;          // (sequence, head) pairs from which shares have one size for all sequences
 constexpr int kTilesWanted = 256, kTilesLeast = 256;
 constexpr int kMostSplits = 256;
@@ -195,12 +196,11 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / kRows + i <= tile; });
         b = lo;
         const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
-        const long long r = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / kRows + b)) * kRows + n;
-        const long long rows = static_cast<long long>(q1 - q0) * G;
-        valid = r >= 0 && r < rows;
-        const int i = valid ? static_cast<int>(r / G) : 0;
+        const int r = (tile - static_cast<int>(static_cast<long long>(q0) * G / kRows + b)) * kRows + n;
+        valid = r >= 0 && r < (q1 - q0) * G;
+        const int i = valid ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(G)) : 0;
         t = q0 + i;
-        head = h * G + (valid ? static_cast<int>(r - static_cast<long long>(i) * G) : 0);
+        head = h * G + (valid ? r - i * G : 0);
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
     }
     if (__ballot(valid) == 0) return;      // the same 16 rows in every wave: the workgroup leaves together
@@ -555,11 +555,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     bool valid;
     if (shared) {
         span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
-        const long long r = static_cast<long long>(tile) * ROWS + row_wave * 32 + n;
-        const long long tt = r / G;
-        t = static_cast<int>(tt);
-        head = h * G + static_cast<int>(r - tt * G);
-        const int b = tt < a.T ? find_sequence(a.q_start, a.B, t) : -1;
+        const unsigned r = static_cast<unsigned>(tile) * ROWS + row_wave * 32 + n;
+        t = static_cast<int>(r / G);
+        head = h * G + static_cast<int>(r - static_cast<unsigned>(t) * G);
+        // every row's own sequence: a search in LDS, where the borders fit it
+        constexpr int kFit = sizeof(sh) / sizeof(int32_t);
+        int32_t* const borders = reinterpret_cast<int32_t*>(sh);
+        const bool fits = a.B < kFit;
+        if (fits) {
+            for (int i = threadIdx.x; i <= a.B; i += kTileThreads) borders[i] = a.q_start[i];
+            __syncthreads();
+        }
+        const int b = t < a.T ? find_sequence(fits ? borders : a.q_start, a.B, t) : -1;
+        if (fits) __syncthreads();
         valid = b >= 0;
         if (valid) {
             pos = a.prefix_len + context(a, b) - a.q_start[b + 1] + t;
@@ -570,14 +578,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / ROWS + i <= tile; });
         const int b = lo;
         const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
-        const long long first = (static_cast<long long>(tile) - (static_cast<long long>(q0) * G / ROWS + b)) * ROWS;
-        const long long rows = static_cast<long long>(q1 - q0) * G;
+        const int first = (tile - static_cast<int>(static_cast<long long>(q0) * G / ROWS + b)) * ROWS;
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
-        const long long r = first + row_wave * 32 + n;
-        valid = r >= 0 && r < rows;
-        const int i = valid ? static_cast<int>(r / G) : 0;
+        const int r = first + row_wave * 32 + n;
+        valid = r >= 0 && r < (q1 - q0) * G;
+        const int i = valid ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(G)) : 0;
         t = q0 + i;
-        head = h * G + (valid ? static_cast<int>(r - static_cast<long long>(i) * G) : 0);
+        head = h * G + (valid ? r - i * G : 0);
         if (valid) {
             pos = a.prefix_len + span.tokens - a.q_start[b + 1] + t;
             if (a.bidir_len) both = a.bidir_len[b];
@@ -1082,7 +1089,7 @@ Part deal(long long rows, long long groups, long long together, bool ragged, int
     const long long busy = (rows / p.rows > groups ? rows / p.rows : groups) * Hkv;     // workgroups with rows
     const bool uneven = groups * Hkv >= kManyGroups;
     const long long wanted = p.rows != kRows ? kTilesWanted : uneven ? kRowsWantedUneven : kRowsWanted;
-    const int least = p.rows == kRows ? kRowsLeast : kTilesLeast;
+    const int least = p.rows != kRows ? kTilesLeast : uneven ? kRowsLeastUneven : kRowsLeast;
     long long splits = (wanted + busy - 1) / busy;
     if (splits * least > tokens) splits = (tokens + least - 1) / least;
     if (splits > kMostSplits) splits = kMostSplits;
@@ -1142,9 +1149,10 @@ size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_l
 
 bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const Plan p = plan(T, Hq, Hkv, B, max_kv, prefix_len);
-    constexpr long long kMost = (1LL << 23) - 1;   // workgroups of 512 in a launch dimension
+    // workgroups of 512 a launch dimension holds, halved: the rows of a key head stay below 2^30
+    constexpr long long kMost = (1LL << 22) - 1;
     return (p.prefix.tiles * p.prefix.splits + p.own.tiles * p.own.splits + 8) * Hkv <= kMost && Hkv <= 65535 &&
-           (static_cast<long long>(T) * Hq + kAttnWaves - 1) / kAttnWaves <= kMost;
+           static_cast<long long>(T) * Hq <= (1LL << 26);
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s) {
