@@ -528,7 +528,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     // Rows of one chunk more than they hold, so that eight rows' same chunk lies in different banks and every address
     // is a base and a constant.  Value d is row 16 (d % 8) + d / 8.
     struct Step {
-        u4 k[kTileTokens * 17];                    // 16 chunks of 8 values a token
+        u4 k[kTileTokens * 17];                    // 16 chunks of 8 values a token, the even ones first
         u4 v[128 * 9];                             // 8 chunks of 8 tokens a value
         f4 f[3][kTileTokens / 4];                  // per token: key factor, log2 of the value scale, its reciprocal
     };
@@ -635,6 +635,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const int steps = __builtin_amdgcn_readfirstlane(max(0, min(share, steps_all - split * share)));
     step0 = __builtin_amdgcn_readfirstlane(step0 + split * share);
 
+    const int group = 16 * (wave >> 1);            // of a step's tokens, those that the wave stages
+    // Of steps st .. st + 63, a lane each: where the wave's 16 tokens lie, as the number of the first, ~0 if nowhere.
+    uint32_t place_lo = 0, place_hi = 0;
+    auto load_places = [&](int st) __attribute__((always_inline)) {
+        const long long j = static_cast<long long>(step0 + st + lane) * kTileTokens + group;
+        const int page = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
+        const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+        const bool good = page >= 0 && page < a.n_pages;
+        place_lo = good ? static_cast<uint32_t>(token) : ~0u;
+        place_hi = good ? static_cast<uint32_t>(token >> 32) : ~0u;
+    };
+    load_places(0);
+
     // queries: lane (n, hf) holds values 16 k + 8 hf .. + 7 of its row, k = 0 .. 7, in the order of the keys' codes
     h8 q[8];
     {
@@ -658,29 +671,21 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     // What a wave stages of a step: eight tokens' keys, eight tokens' values and eight tokens' scales of both, all of the
     // same 16 tokens, which lie in one page.  The keys are tokens 8 w .. 8 w + 7 of the step, the values those of two
     // quads that share a chunk.  Codes are loaded a step ahead, the numbers of 64 steps' pages at once, a lane each.
-    // Lanes are dealt out so that those that write at one time write to different banks.
-    const int group = 16 * (wave >> 1);
-    const int k_token = 8 * wave + (lane & 7), k_part = lane >> 3;
-    const int v_octet = (lane & 7) + 8 * (lane >> 5), v_pair = (lane >> 3) & 1, v_half = (lane >> 4) & 1;
+    // Lanes are dealt out so that 16 of them load consecutive bytes, and those that write at one time write to different
+    // banks.
+    const int k_token = 8 * wave + (lane >> 3), k_part = lane & 7;
+    const int v_octet = ((lane >> 1) & 7) + 8 * (lane >> 5), v_pair = lane & 1, v_half = (lane >> 4) & 1;
     const int k_at = ((k_token & 15) * 8 + k_part) * 2 * BITS;                                 // bytes within the 16 tokens
     const int v_at = ((((wave & 1) + 2 * v_half) * 16 + v_octet) * 2 + v_pair) * 2 * BITS;
     const bool s_values = (lane & 8) != 0;                  // of 16 lanes 0 .. 7 stage key, 8 .. 15 value scales, four times over
     const uint16_t* const scales = s_values ? a.V_scale : a.K_scale;
     const int s_token = 8 * wave + (lane & 7);
-    uint32_t kraw[BITS / 2], vraw[BITS / 2];
-    uint32_t sraw = 0;
-    bool there = false;
-    // Of steps st .. st + 63, a lane each: where the wave's 16 tokens lie, as the number of the first, ~0 if nowhere.
-    uint32_t place_lo = 0, place_hi = 0;
-    auto load_places = [&](int st) __attribute__((always_inline)) {
-        const long long j = static_cast<long long>(step0 + st + lane) * kTileTokens + group;
-        const int page = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
-        const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
-        const bool good = page >= 0 && page < a.n_pages;
-        place_lo = good ? static_cast<uint32_t>(token) : ~0u;
-        place_hi = good ? static_cast<uint32_t>(token >> 32) : ~0u;
+    struct Raw {
+        uint32_t k[BITS / 2], v[BITS / 2], scale;
+        bool there;
     };
     auto fetch = [&](int st) __attribute__((always_inline)) {
+        Raw raw;
         const uint32_t lo = __builtin_amdgcn_readlane(place_lo, st & 63), hi = __builtin_amdgcn_readlane(place_hi, st & 63);
         const bool good = hi != ~0u;
         const unsigned long long token = good ? (static_cast<unsigned long long>(hi) << 32) | lo : static_cast<unsigned long long>(h) << a.page_log2;
@@ -688,31 +693,32 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         const uint8_t* vp = a.V_codes + token * (16 * BITS);
         if (BITS == 4) {
             const u2 x = *reinterpret_cast<const u2*>(kp + k_at), y = *reinterpret_cast<const u2*>(vp + v_at);
-            kraw[0] = x.x; kraw[1] = x.y;
-            vraw[0] = y.x; vraw[1] = y.y;
+            raw.k[0] = x.x; raw.k[1] = x.y;
+            raw.v[0] = y.x; raw.v[1] = y.y;
         } else {
             const u4 x = *reinterpret_cast<const u4*>(kp + k_at), y = *reinterpret_cast<const u4*>(vp + v_at);
-            kraw[0] = x.x; kraw[1] = x.y; kraw[BITS / 2 - 2] = x.z; kraw[BITS / 2 - 1] = x.w;
-            vraw[0] = y.x; vraw[1] = y.y; vraw[BITS / 2 - 2] = y.z; vraw[BITS / 2 - 1] = y.w;
+            raw.k[0] = x.x; raw.k[1] = x.y; raw.k[BITS / 2 - 2] = x.z; raw.k[BITS / 2 - 1] = x.w;
+            raw.v[0] = y.x; raw.v[1] = y.y; raw.v[BITS / 2 - 2] = y.z; raw.v[BITS / 2 - 1] = y.w;
         }
-        sraw = scales[token + (s_token & 15)];
-        there = good && (step0 + st) * kTileTokens + s_token < span.tokens;
+        raw.scale = scales[token + (s_token & 15)];
+        raw.there = good && (step0 + st) * kTileTokens + s_token < span.tokens;
+        return raw;
     };
-    auto stage_keys = [&](int buf, int part) __attribute__((always_inline)) {          // part 0, 1: eight codes each
-        sh[buf].k[k_token * 17 + 2 * k_part + part] = __builtin_bit_cast(u4, key_operand<BITS>(kraw + part * (BITS / 4)));
+    auto stage_keys = [&](const Raw& raw, int buf, int part) __attribute__((always_inline)) {          // part 0, 1: eight codes each
+        sh[buf].k[k_token * 17 + k_part + 8 * part] = __builtin_bit_cast(u4, key_operand<BITS>(raw.k + part * (BITS / 4)));
     };
-    auto stage_values = [&](int buf, int part) __attribute__((always_inline)) {        // part 0 .. 3: two values of two tokens
+    auto stage_values = [&](const Raw& raw, int buf, int part) __attribute__((always_inline)) {        // part 0 .. 3: two values of two tokens
         uint32_t* p = reinterpret_cast<uint32_t*>(&sh[buf].v[v_octet * 9 + wave]) + 2 * v_half + v_pair;
 #pragma unroll
-        for (int j = 2 * part; j < 2 * part + 2; ++j) p[j * 576] = value_pair<BITS>(vraw, j);
+        for (int j = 2 * part; j < 2 * part + 2; ++j) p[j * 576] = value_pair<BITS>(raw.v, j);
     };
-    auto stage_scales = [&](int buf) __attribute__((always_inline)) {
-        const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sraw)));
+    auto stage_scales = [&](const Raw& raw, int buf) __attribute__((always_inline)) {
+        const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(raw.scale)));
         // a scale of 0 has codes of 0: its weight stays in the sum of weights through any other scale
         const float vs = s == 0.0f ? 0x1p-24f : s;
-        const float key = there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;      // NaN where s is not finite
-        const float log_v = there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
-        const float rcp_v = there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
+        const float key = raw.there ? __builtin_fmaf(s, key_factor, s * 0.0f) : 0.0f;      // NaN where s is not finite
+        const float log_v = raw.there ? __builtin_amdgcn_logf(vs) : -__builtin_inff();
+        const float rcp_v = raw.there && vs <= 65504.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
         float* f = reinterpret_cast<float*>(sh[buf].f) + s_token;
         f[s_values ? kTileTokens : 0] = s_values ? log_v : key;
         f[s_values ? 2 * kTileTokens : 0] = s_values ? rcp_v : key;
@@ -728,6 +734,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     f16v s;            // products of 32 tokens with their codes, then their exponents
     h8 w[2];           // their weights
     u4 vc[8];          // the tokens' values
+    Raw raw;           // what the next step to be staged was loaded as
     f4 kf[4], rv[4];   // factors of the tokens: key, reciprocal value scale,
     float lv;          // log2 of the value scale, lane c of 16 for the lane's token c
 
@@ -750,7 +757,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     };
     auto key_chunk = [&](int buf, int sub, int k) __attribute__((always_inline)) {
         const int token = 32 * sub + n;
-        return sh[buf].k[token * 17 + 2 * k + hf];
+        return sh[buf].k[token * 17 + k + 8 * hf];
     };
     auto value_chunk = [&](int buf, int sub, int i) __attribute__((always_inline)) {      // i = 4 kk + m
         return sh[buf].v[(32 * (i & 3) + n) * 9 + 4 * sub + 2 * (i >> 2) + hf];
@@ -858,14 +865,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             weighted(c);
-            if (STAGE) stage_values(to, c);
+            if (STAGE) stage_values(raw, to, c);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             product(c);
-            if (STAGE && c < 2) stage_keys(to, c);
-            if (STAGE && c == 2) stage_scales(to);
+            if (STAGE && c < 2) stage_keys(raw, to, c);
+            if (STAGE && c == 2) stage_scales(raw, to);
             __builtin_amdgcn_sched_barrier(0);
             weighted(4 + c);
             __builtin_amdgcn_sched_barrier(0);
@@ -876,16 +883,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         __builtin_amdgcn_s_setprio(0);
     };
 
-    auto stage_all = [&](int buf) __attribute__((always_inline)) {
-        stage_keys(buf, 0);
-        stage_keys(buf, 1);
+    auto stage_all = [&](const Raw& of, int buf) __attribute__((always_inline)) {
+        stage_keys(of, buf, 0);
+        stage_keys(of, buf, 1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) stage_values(buf, c);
-        stage_scales(buf);
+        for (int c = 0; c < 4; ++c) stage_values(of, buf, c);
+        stage_scales(of, buf);
     };
     auto fetch_later = [&](int st) __attribute__((always_inline)) {       // nothing, past the last step
         if ((st & 63) == 0) load_places(st);
-        fetch(st);
+        raw = fetch(st);
     };
     // Two waves share a SIMD, one of each half of the workgroup.  The upper half runs a part behind the lower one, so
     // that of the two waves one has matrix and one has vector work, always:
@@ -904,13 +911,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const int own_sub = kPair && upper ? 1 : 0;
     const int base = step0 * kTileTokens + span.base;
     if (steps > 0) {
-        load_places(0);
-        fetch(0);
-        stage_all(0);
-        fetch(1);
+        const Raw first = fetch(0), second = fetch(1);
+        stage_all(first, 0);
         if (kPair) {
-            stage_all(1);
-            fetch(2);
+            raw = fetch(2);
+            stage_all(second, 1);
+        } else {
+            raw = second;
         }
     }
     __syncthreads();
@@ -1080,17 +1087,18 @@ struct Plan {
     size_t workspace;
 };
 
-// `together`: rows on the same tokens; `ragged`: every group's rows begin a tile; `groups`: stretches of tokens (sequences, or one prefix); `tokens`: the most of one
-Part deal(long long rows, long long groups, long long together, bool ragged, int Hkv, int tokens) {
+// `groups`: stretches of tokens (sequences, or one prefix); `ragged`: every group's rows begin a tile; `tokens`: the most
+// of a group; `taken`: workgroups of the same launch on the other part.
+Part deal(int tile, long long rows, long long groups, bool ragged, int Hkv, int tokens, long long taken) {
     Part p = {};
     if (tokens <= 0) return p;
-    p.rows = together >= kWideRows ? 256 : together >= kManyRows ? 128 : kRows;
+    p.rows = tile;
     p.tiles = ragged ? rows / p.rows + groups : (rows + p.rows - 1) / p.rows;
     const long long busy = (rows / p.rows > groups ? rows / p.rows : groups) * Hkv;     // workgroups with rows
     const bool uneven = groups * Hkv >= kManyGroups;
-    const long long wanted = p.rows != kRows ? kTilesWanted : uneven ? kRowsWantedUneven : kRowsWanted;
+    const long long wanted = p.rows != kRows ? kTilesWanted - taken : uneven ? kRowsWantedUneven : kRowsWanted;
     const int least = p.rows != kRows ? kTilesLeast : uneven ? kRowsLeastUneven : kRowsLeast;
-    long long splits = (wanted + busy - 1) / busy;
+    long long splits = taken > 0 ? wanted / busy : (wanted + busy - 1) / busy;
     if (splits * least > tokens) splits = (tokens + least - 1) / least;
     if (splits > kMostSplits) splits = kMostSplits;
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
@@ -1103,8 +1111,13 @@ Part deal(long long rows, long long groups, long long together, bool ragged, int
 Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const long long rows = static_cast<long long>(T) * (Hq / Hkv);
     Plan p = {};
-    p.prefix = deal(rows, 1, rows, false, Hkv, prefix_len);
-    p.own = deal(rows, B, rows / B, true, Hkv, max_kv);
+    // rows on the same tokens: of a sequence on average, of all sequences in a prefix
+    const long long each = rows / B;
+    const int prefix_tile = rows >= kWideRows / 2 ? 256 : rows >= kManyRows ? 128 : kRows;
+    const int own_tile = each < kManyRows ? kRows : prefix_len > 0 ? prefix_tile : each >= kWideRows ? 256 : 128;
+    p.own = deal(own_tile, rows, B, true, Hkv, max_kv, 0);
+    const long long taken = own_tile == prefix_tile && own_tile != kRows ? (rows / own_tile > B ? rows / own_tile : B) * p.own.splits * Hkv : 0;
+    p.prefix = deal(prefix_tile, rows, 1, false, Hkv, prefix_len, taken);
     p.splits = p.prefix.splits + p.own.splits;
     p.workspace = p.splits > 1 ? static_cast<size_t>(p.splits) * T * Hq * kPartial * sizeof(float) : 0;
     return p;
