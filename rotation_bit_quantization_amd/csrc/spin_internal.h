@@ -61,7 +61,8 @@ struct KvAppendArgs {
     uint8_t* V_codes;
     uint16_t* V_scale;
     uint16_t* Q_out;
-    long long kv_blocks;           // set by the launcher
+    unsigned kv_blocks;            // set by the launcher
+    int heads;
     float norm;
 };
 hipError_t launch_kv_append(KvAppendArgs a, bool x_f16, int bits, hipStream_t s);
