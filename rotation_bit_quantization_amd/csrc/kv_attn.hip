@@ -133,9 +133,10 @@ __device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
 }
 
-// tanh from one exponential: 1 - 2 / (e^(2 x) + 1), right at both infinities.
-__device__ __forceinline__ float tanh_fast(float x) {
-    return 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * kLog2e * x) + 1.0f);
+// A capped score in the exponent: cap log2(e) tanh(z) = top - 2 top / (2^y + 1), y = 2 log2(e) z, right at both
+// infinities.  `lm` is what is added to it, `top` = cap log2(e) already among it.
+__device__ __forceinline__ float capped_plus(float y, float top, float lm) {
+    return __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y) + 1.0f), -2.0f * top, lm);
 }
 
 // Tokens of sequence b in its own pages.
@@ -269,8 +270,8 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     }
     const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
     const bool capped = FANCY && a.softcap > 0.0f;
-    const float key_factor = (capped ? a.scale / a.softcap : a.scale * kLog2e) * 0x1p24f;
-    const float to_log2 = a.softcap * kLog2e;
+    const float key_factor = (capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e) * 0x1p24f;
+    const float cap_top = capped ? a.softcap * kLog2e : 0.0f;
 
     // Of the wave's next 32 steps, a lane each and half of a step: where the 16 tokens lie, as the number of the first, ~0
     // if nowhere.
@@ -365,24 +366,23 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         const int next = i + 1 < turns ? i + 1 : i;
         if ((next & 31) == 0 && next > 0) load_places(next);
         fetch_keys(next);
-        auto exponent = [&](int e, float k, float lm) __attribute__((always_inline)) {
-            if (FANCY) {
-                float z = x[e] * k;
-                if (capped) z = tanh_fast(z) * to_log2;
-                z = __builtin_fmaf(-slope, __builtin_fabsf(static_cast<float>(pos - (j0 + 16 * (e >> 2) + 4 * g + (e & 3)))), z);
-                x[e] = z + lm;
-            } else {
-                x[e] = __builtin_fmaf(x[e], k, lm);
-            }
+        const float from = M - cap_top;
+        const float rel = static_cast<float>(pos - j0 - 4 * g);
+        auto exponent = [&](int e, float k, float lm, bool cap) __attribute__((always_inline)) {
+            if (FANCY) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
+            x[e] = cap ? capped_plus(x[e] * k, cap_top, lm) : __builtin_fmaf(x[e], k, lm);
         };
-        exponent(0, row_lane<0>(kf), row_lane<0>(lv) - M);
-        exponent(1, row_lane<1>(kf), row_lane<1>(lv) - M);
-        exponent(2, row_lane<2>(kf), row_lane<2>(lv) - M);
-        exponent(3, row_lane<3>(kf), row_lane<3>(lv) - M);
-        exponent(4, row_lane<4>(kf), row_lane<4>(lv) - M);
-        exponent(5, row_lane<5>(kf), row_lane<5>(lv) - M);
-        exponent(6, row_lane<6>(kf), row_lane<6>(lv) - M);
-        exponent(7, row_lane<7>(kf), row_lane<7>(lv) - M);
+#define SPIN_ONE(N, CAP) exponent(N, row_lane<N>(kf), row_lane<N>(lv) - from, CAP);
+#define SPIN_ALL(CAP)                                                                     \
+    SPIN_ONE(0, CAP) SPIN_ONE(1, CAP) SPIN_ONE(2, CAP) SPIN_ONE(3, CAP) SPIN_ONE(4, CAP) \
+    SPIN_ONE(5, CAP) SPIN_ONE(6, CAP) SPIN_ONE(7, CAP)
+        if (capped) {
+            SPIN_ALL(true)
+        } else {
+            SPIN_ALL(false)
+        }
+#undef SPIN_ALL
+#undef SPIN_ONE
         if (st < whole0 || st >= whole1) {
             asm volatile("" ::: "memory");     // keeps this a branch
             const int rel = pos - j0 - 4 * g;
@@ -665,8 +665,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const int at_row = valid ? t * a.Hq + head : -1;       // T * Hq is below 2^26
     const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
     const bool capped = FANCY && a.softcap > 0.0f;
-    const float key_factor = capped ? a.scale / a.softcap : a.scale * kLog2e;
-    const float to_log2 = a.softcap * kLog2e;
+    const float key_factor = capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e;
+    const float cap_top = capped ? a.softcap * kLog2e : 0.0f;
 
     // What a wave stages of a step: eight tokens' keys, eight tokens' values and eight tokens' scales of both, all of the
     // same 16 tokens, which lie in one page.  The keys are tokens 8 w .. 8 w + 7 of the step, the values those of two
@@ -772,19 +772,24 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     };
     // products to exponents of the tokens at positions j0 .. j0 + 31, relative to M
     auto exponents = [&](int j0) __attribute__((always_inline)) {
-        auto one = [&](int e, float lm) __attribute__((always_inline)) {
-            if (FANCY) {
-                float z = s[e] * kf[e >> 2][e & 3];
-                if (capped) z = tanh_fast(z) * to_log2;
-                z = __builtin_fmaf(-slope, __builtin_fabsf(static_cast<float>(pos - (j0 + 8 * (e >> 2) + 4 * hf + (e & 3)))), z);
-                s[e] = z + lm;
-            } else {
-                s[e] = __builtin_fmaf(s[e], kf[e >> 2][e & 3], lm);
-            }
+        const float from = M - cap_top;
+        const float rel = static_cast<float>(pos - j0 - 4 * hf);
+        auto one = [&](int e, float lm, bool cap) __attribute__((always_inline)) {
+            const float k = kf[e >> 2][e & 3];
+            if (FANCY) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
+            s[e] = cap ? capped_plus(s[e] * k, cap_top, lm) : __builtin_fmaf(s[e], k, lm);
         };
-#define SPIN_ONE(N) one(N, row_lane<N>(lv) - M);
-        SPIN_ONE(0) SPIN_ONE(1) SPIN_ONE(2) SPIN_ONE(3) SPIN_ONE(4) SPIN_ONE(5) SPIN_ONE(6) SPIN_ONE(7)
-        SPIN_ONE(8) SPIN_ONE(9) SPIN_ONE(10) SPIN_ONE(11) SPIN_ONE(12) SPIN_ONE(13) SPIN_ONE(14) SPIN_ONE(15)
+#define SPIN_ONE(N, CAP) one(N, row_lane<N>(lv) - from, CAP);
+#define SPIN_ALL(CAP)                                                                     \
+    SPIN_ONE(0, CAP) SPIN_ONE(1, CAP) SPIN_ONE(2, CAP) SPIN_ONE(3, CAP) SPIN_ONE(4, CAP) \
+    SPIN_ONE(5, CAP) SPIN_ONE(6, CAP) SPIN_ONE(7, CAP) SPIN_ONE(8, CAP) SPIN_ONE(9, CAP) \
+    SPIN_ONE(10, CAP) SPIN_ONE(11, CAP) SPIN_ONE(12, CAP) SPIN_ONE(13, CAP) SPIN_ONE(14, CAP) SPIN_ONE(15, CAP)
+        if (capped) {
+            SPIN_ALL(true)
+        } else {
+            SPIN_ALL(false)
+        }
+#undef SPIN_ALL
 #undef SPIN_ONE
     };
     auto mask = [&](int j0) __attribute__((always_inline)) {
