@@ -46,8 +46,9 @@ constexpr int kTilesWanted = 256, kTilesLeast = 256;
 constexpr int kMostSplits = 256;
 constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kManyRows = 32;             // rows on the same tokens from which tiles of 128, 256 rows are taken
-constexpr int kWideRows = 1024;
+constexpr int kManyRows = 64;             // rows on the same tokens, and rows times tokens of all heads, from which ..
+constexpr double kTileWork = 1 << 25;     // .. tiles of 128 rows are taken, ..
+constexpr double kWideWork = 1 << 27;     // .. and of 256 (twice that of a sequence's own tokens: masks leave half of them)
 constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
 
 union Frag {
@@ -144,6 +145,9 @@ __device__ __forceinline__ int context(const KvAttnArgs& a, int b) {
     return min(max(a.kv_len[b], 0), a.max_pages << a.page_log2);
 }
 
+// A border of the batch, held to its T rows.
+__device__ __forceinline__ int within(int row, int T) { return min(max(row, 0), T); }
+
 // Which tokens a workgroup has.
 struct Span {
     const int32_t* table;
@@ -151,6 +155,41 @@ struct Span {
     int tokens;         // tokens the table's pages hold
     int base;           // position of the first of them
 };
+
+// Tiles are numbered through the sequences without gaps.  floor(q_start[b] G / ROWS) + b would number them, with gaps, in
+// one step, but workgroups go to the XCDs and to the shader engines of each in a fixed turn, and gaps at every second
+// number leave half of those without work: 16 sequences of 128 rows on 4096 tokens took 113 us so, 70 without gaps (of 64
+// rows, 176 and 96).
+
+// Tiles of sequence b0 + lane.
+template <int ROWS>
+__device__ __forceinline__ int count_tiles(const KvAttnArgs& a, int G, int b0, int lane) {
+    const int i = b0 + lane;
+    const int rows = i < a.B ? (within(a.q_start[i + 1], a.T) - within(a.q_start[i], a.T)) * G : 0;
+    return rows > 0 ? (rows + ROWS - 1) / ROWS : 0;
+}
+
+// The sum of lanes 0 .. l, in lane l.
+__device__ __forceinline__ int sums_up_to(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // rows of 16: shifts by 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // lane 15 of rows 0, 2 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // lane 31 to rows 2, 3
+    return v;
+}
+
+// Where `tile` is among the lanes' tiles, b is set and the tile's number in its sequence returned, otherwise its number
+// behind them.
+__device__ __forceinline__ int find_tile(int tiles, int b0, int tile, int& b) {
+    const int upto = sums_up_to(tiles);
+    const unsigned long long hit = __ballot(upto > tile);
+    if (hit == 0) return tile - __builtin_amdgcn_readlane(upto, 63);
+    const int l = __builtin_ctzll(hit);
+    b = b0 + l;
+    return tile - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l));
+}
 
 // One tile of 16 query rows of one key head, over a share of the tokens: each
 // wave takes every fourth step of 32 tokens, the waves' results are joined in
@@ -196,7 +235,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         // sequence b's tiles start at tile floor(q_start[b] G / 16) + b: room for each one's ragged last tile
         const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / kRows + i <= tile; });
         b = lo;
-        const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
+        const int q0 = within(a.q_start[b], a.T), q1 = within(a.q_start[b + 1], a.T);
         const int r = (tile - static_cast<int>(static_cast<long long>(q0) * G / kRows + b)) * kRows + n;
         valid = r >= 0 && r < (q1 - q0) * G;
         const int i = valid ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(G)) : 0;
@@ -539,14 +578,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const int n = lane & 31, hf = lane >> 5;
     const int row_wave = kPair ? wave & 3 : wave;
     const int G = a.Hq / a.Hkv;
-    // key heads alternate fastest: with 8 of them a head stays on one XCD; late tiles, the long ones, come first
+    // key heads alternate fastest: with 8 of them a head stays on one XCD
     const int h = blockIdx.x % a.Hkv;
     const int prefix_items = prefix_tiles * prefix_splits;
     const int index = blockIdx.x / a.Hkv;
     const bool shared = index < prefix_items;
-    const int item = shared ? index : prefix_items + own_tiles * own_splits - 1 - index;
     const int splits = shared ? prefix_splits : own_splits;
-    const int tile = item / splits, split = item - tile * splits;
+    const int item = shared ? index : index - prefix_items;
+    int tile = item / splits;                      // own: counted from the last one
+    const int split = item - tile * splits;
     const int first_slot = shared ? 0 : prefix_splits;
     const int total_splits = prefix_splits + own_splits;
 
@@ -574,11 +614,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
             if (a.bidir_len) both = a.bidir_len[b];
         }
     } else {
-        // sequence b's tiles start at tile floor(q_start[b] G / rows) + b: room for each one's ragged last tile
-        const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / ROWS + i <= tile; });
-        const int b = lo;
-        const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.T);
-        const int first = (tile - static_cast<int>(static_cast<long long>(q0) * G / ROWS + b)) * ROWS;
+        // the last tiles, the long ones, come first; the grid has room for a ragged tile of every sequence
+        int all = count_tiles<ROWS>(a, G, 0, lane);
+        const int mine = all;
+        for (int b0 = 64; b0 < a.B; b0 += 64) all += count_tiles<ROWS>(a, G, b0, lane);
+        all = __builtin_amdgcn_readlane(sums_up_to(all), 63);
+        if (tile >= all) return;
+        int b = -1;
+        tile = all - 1 - tile;
+        for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) tile = find_tile(b0 == 0 ? mine : count_tiles<ROWS>(a, G, b0, lane), b0, tile, b);
+        if (b < 0) return;                         // borders that do not ascend
+        const int first = tile * ROWS;
+        const int q0 = within(a.q_start[b], a.T), q1 = within(a.q_start[b + 1], a.T);
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
         const int r = first + row_wave * 32 + n;
         valid = r >= 0 && r < (q1 - q0) * G;
@@ -1093,17 +1140,18 @@ struct Plan {
 };
 
 // `groups`: stretches of tokens (sequences, or one prefix); `ragged`: every group's rows begin a tile; `tokens`: the most
-// of a group; `taken`: workgroups of the same launch on the other part.
-Part deal(int tile, long long rows, long long groups, bool ragged, int Hkv, int tokens, long long taken) {
+// of a group.
+Part deal(int tile, long long rows, long long groups, bool ragged, int Hkv, int tokens) {
     Part p = {};
     if (tokens <= 0) return p;
     p.rows = tile;
     p.tiles = ragged ? rows / p.rows + groups : (rows + p.rows - 1) / p.rows;
     const long long busy = (rows / p.rows > groups ? rows / p.rows : groups) * Hkv;     // workgroups with rows
     const bool uneven = groups * Hkv >= kManyGroups;
-    const long long wanted = p.rows != kRows ? kTilesWanted - taken : uneven ? kRowsWantedUneven : kRowsWanted;
+    const long long wanted = p.rows != kRows ? kTilesWanted : uneven ? kRowsWantedUneven : kRowsWanted;
     const int least = p.rows != kRows ? kTilesLeast : uneven ? kRowsLeastUneven : kRowsLeast;
-    long long splits = taken > 0 ? wanted / busy : (wanted + busy - 1) / busy;
+    // one tile a CU: no more than there are; of 16 rows several share one
+    long long splits = p.rows != kRows ? wanted / busy : (wanted + busy - 1) / busy;
     if (splits * least > tokens) splits = (tokens + least - 1) / least;
     if (splits > kMostSplits) splits = kMostSplits;
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
@@ -1116,13 +1164,13 @@ Part deal(int tile, long long rows, long long groups, bool ragged, int Hkv, int 
 Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const long long rows = static_cast<long long>(T) * (Hq / Hkv);
     Plan p = {};
-    // rows on the same tokens: of a sequence on average, of all sequences in a prefix
-    const long long each = rows / B;
-    const int prefix_tile = rows >= kWideRows / 2 ? 256 : rows >= kManyRows ? 128 : kRows;
-    const int own_tile = each < kManyRows ? kRows : prefix_len > 0 ? prefix_tile : each >= kWideRows ? 256 : 128;
-    p.own = deal(own_tile, rows, B, true, Hkv, max_kv, 0);
-    const long long taken = own_tile == prefix_tile && own_tile != kRows ? (rows / own_tile > B ? rows / own_tile : B) * p.own.splits * Hkv : 0;
-    p.prefix = deal(prefix_tile, rows, 1, false, Hkv, prefix_len, taken);
+    // rows times tokens, of all key heads: what there is to do
+    const double prefix_work = static_cast<double>(rows) * prefix_len * Hkv, own_work = static_cast<double>(rows) * max_kv * Hkv;
+    const int prefix_tile = rows < kManyRows || prefix_work < kTileWork ? kRows : prefix_work < kWideWork ? 128 : 256;
+    int own_tile = rows / B < kManyRows || own_work < kTileWork ? kRows : own_work < 2 * kWideWork ? 128 : 256;
+    if (own_tile != kRows && prefix_len > 0 && prefix_tile != kRows) own_tile = prefix_tile;     // one launch
+    p.prefix = deal(prefix_tile, rows, 1, false, Hkv, prefix_len);
+    p.own = deal(own_tile, rows, B, true, Hkv, max_kv);
     p.splits = p.prefix.splits + p.own.splits;
     p.workspace = p.splits > 1 ? static_cast<size_t>(p.splits) * T * Hq * kPartial * sizeof(float) : 0;
     return p;
