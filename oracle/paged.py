@@ -103,8 +103,9 @@ def cache_tokens(cache, pages, h, n):
 
 
 def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None, window=0, causal=True, bidir_len=None,
-              prefix_table=None, prefix_len=0):
-    """(O [T, Hq, 128] float64, NaN rows where nothing is written, bound [T, Hq, 128]).
+              prefix_table=None, prefix_len=0, rows=None):
+    """(O [T, Hq, 128] float64, NaN rows where nothing is written, bound [T, Hq, 128]).  ``rows``: those of T to
+    compute, all by default; what is returned for others means nothing.
 
     ``bound`` is how far a result may be that holds scores in float32, rounds softmax weights (times the value's
     scale, relative to the row's largest) to fp16 and the result to fp16:
@@ -129,6 +130,8 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
             kc, ks, vc, vs, there = parts
             j = np.arange(prefix_len + kv)
             for t in range(q_start[b], min(q_start[b + 1], T)):
+                if rows is not None and t not in rows:
+                    continue
                 p = prefix_len + kv - int(q_start[b + 1]) + t
                 seen = there.copy()
                 if causal:
