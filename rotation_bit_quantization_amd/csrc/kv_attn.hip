@@ -44,6 +44,7 @@ constexpr int kRowsWantedUneven = 2304, kRowsLeastUneven = 512;
 constexpr int kManyGroups = 384;          // (sequence, head) pairs from which shares have one size for all sequences
 constexpr int kTilesWanted = 256, kTilesLeast = 256;
 constexpr int kMostSplits = 256;
+constexpr int kCounted = 256;              // sequences up to which tiles of 16 rows are found by counting
 constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kManyRows = 64;             // rows on the same tokens, and rows times tokens of all heads, from which ..
@@ -156,10 +157,13 @@ struct Span {
     int base;           // position of the first of them
 };
 
-// Tiles are numbered through the sequences without gaps.  floor(q_start[b] G / ROWS) + b would number them, with gaps, in
-// one step, but workgroups go to the XCDs and to the shader engines of each in a fixed turn, and gaps at every second
-// number leave half of those without work: 16 sequences of 128 rows on 4096 tokens took 113 us so, 70 without gaps (of 64
-// rows, 176 and 96).
+// Tiles are numbered through the sequences without gaps, by counting them, 64 sequences at a time.  floor(q_start[b] G /
+// ROWS) + b would number them, with gaps, in one step, but workgroups go to the XCDs and to the shader engines of each in
+// a fixed turn, and gaps at every second number leave half of those without work: 16 sequences of 128 rows on 4096
+// tokens took 113 us so, 70 without gaps (of 64 rows, 176 and 96); 32 single tokens with 16 heads a key head on 8192, 105
+// and 62.  From some hundred sequences on counting takes longer than a tile of 16 rows has (256 single
+// tokens of 16 heads on 500 tokens: 36 us counted, 39 with gaps; 512: 83 and 78; 4096 of 4 heads on 64: 609 and 224); there
+// numbers with gaps visit the XCDs in a turn that shifts.
 
 // Tiles of sequence b0 + lane.
 template <int ROWS>
@@ -209,7 +213,8 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     // Workgroup L runs on XCD L % 8: the heads of an item follow each other on one, so that the lines that hold several
     // heads' scales come into one L2.
     const int h = (blockIdx.x >> 3) % a.Hkv;
-    const int index = (blockIdx.x >> 3) / a.Hkv * 8 + (blockIdx.x & 7);
+    const int eight = (blockIdx.x >> 3) / a.Hkv;
+    const int index = eight * 8 + ((blockIdx.x + eight + (eight >> 3)) & 7);   // gaps in the numbers visit every XCD
     const int prefix_items = prefix_tiles * prefix_splits;
     if (index >= prefix_items + own_tiles * own_splits) return;
     const bool shared = index < prefix_items;
@@ -232,11 +237,19 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         valid = b >= 0;
         span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
     } else {
-        // sequence b's tiles start at tile floor(q_start[b] G / 16) + b: room for each one's ragged last tile
-        const int lo = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / kRows + i <= tile; });
-        b = lo;
+        int own = tile;
+        if (a.B == 1) {
+            b = 0;
+        } else if (a.B <= kCounted) {
+            b = -1;
+            for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) own = find_tile(count_tiles<kRows>(a, G, b0, lane), b0, own, b);
+            if (b < 0) return;             // the grid has room for a ragged tile of every sequence
+        } else {
+            b = find_last64(a.B, lane, [&](int i) { return static_cast<long long>(a.q_start[i]) * G / kRows + i <= tile; });
+            own -= static_cast<int>(static_cast<long long>(within(a.q_start[b], a.T)) * G / kRows + b);
+        }
         const int q0 = within(a.q_start[b], a.T), q1 = within(a.q_start[b + 1], a.T);
-        const int r = (tile - static_cast<int>(static_cast<long long>(q0) * G / kRows + b)) * kRows + n;
+        const int r = own * kRows + n;
         valid = r >= 0 && r < (q1 - q0) * G;
         const int i = valid ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(G)) : 0;
         t = q0 + i;
