@@ -39,9 +39,8 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
 // Workgroups that fill the card, and the fewest tokens worth one, of the two kernels; the most shares of a row's tokens.
-constexpr int kRowsWanted = 1024, kRowsLeast = 128;
-constexpr int kRowsWantedUneven = 2304, kRowsLeastUneven = 512;
-constexpr int kManyGroups = 384;          // (sequence, head) pairs from which shares have one size for all sequences
+constexpr int kRowsWaves = 4096, kLeastShare = 32, kLongShare = 1024;
+constexpr int kShort = 2048, kShortest = 512;
 constexpr int kTilesWanted = 256, kTilesLeast = 256;
 constexpr int kMostSplits = 256;
 constexpr int kCounted = 256;              // sequences up to which tiles of 16 rows are found by counting
@@ -201,11 +200,11 @@ __device__ __forceinline__ int find_tile(int tiles, int b0, int tile, int& b) {
 // workspace, [share][T * Hq] rows.
 //
 // Bound at few rows: reading the cache, 2 (16 BITS + 2) bytes a token and head.
-template <int BITS, bool FANCY>
-__global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
+template <int BITS, bool FANCY, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                   int own_tiles, int own_splits, int own_chunk) {
-    __shared__ float o_sh[kAttnWaves][kRows][129];
-    __shared__ float m_sh[kAttnWaves][kRows], l_sh[kAttnWaves][kRows];
+    __shared__ float o_sh[WAVES][kRows][129];
+    __shared__ float m_sh[WAVES][kRows], l_sh[WAVES][kRows];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -329,7 +328,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     // if nowhere.
     uint32_t place_lo = 0, place_hi = 0;
     auto load_places = [&](int i) __attribute__((always_inline)) {      // the wave's steps i .. i + 31
-        const long long j = static_cast<long long>(step0 + wave + kAttnWaves * (i + (lane >> 1))) * kStep + 16 * (lane & 1);
+        const long long j = static_cast<long long>(step0 + wave + WAVES * (i + (lane >> 1))) * kStep + 16 * (lane & 1);
         const int page = j < span.tokens ? span.table[min(static_cast<int>(j >> a.page_log2), span.n_table - 1)] : -1;
         const long long token = ((static_cast<long long>(page) * a.Hkv + h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
         const bool good = page >= 0 && page < a.n_pages;
@@ -365,7 +364,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         const unsigned long long at = (s_half ? token[1] : token[0]) + s_token;
         ks_raw = a.K_scale[at];
         vs_raw = a.V_scale[at];
-        there = (s_half ? good[1] : good[0]) && (step0 + wave + kAttnWaves * i) * kStep + 16 * s_half + s_token < span.tokens;
+        there = (s_half ? good[1] : good[0]) && (step0 + wave + WAVES * i) * kStep + 16 * s_half + s_token < span.tokens;
     };
     auto fetch_values = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
@@ -386,7 +385,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     float M = 0.0f, low = __builtin_inff(), l_sum = 0.0f;
     f4 o[8] = {};
 
-    const int turns = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
+    const int turns = steps > wave ? (steps - wave + WAVES - 1) / WAVES : 0;
     if (turns > 0) {
         load_places(0);
         fetch_keys(0);
@@ -401,7 +400,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         const float kf = here ? __builtin_fmaf(ks, key_factor, ks * 0.0f) : 0.0f;      // NaN where ks is not finite
         const float lv = here ? __builtin_amdgcn_logf(vsf) : -__builtin_inff();
         const float rv = here && vsf <= 65504.0f ? __builtin_amdgcn_rcpf(vsf) : 0.0f;
-        const int st = step0 + wave + kAttnWaves * i;
+        const int st = step0 + wave + WAVES * i;
         const int j0 = st * kStep + span.base;
 
         float x[8];
@@ -492,7 +491,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     __syncthreads();
     float M_all = m_sh[0][n];
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) M_all = __builtin_fmaxf(M_all, m_sh[w][n]);
+    for (int w = 1; w < WAVES; ++w) M_all = __builtin_fmaxf(M_all, m_sh[w][n]);
     const float f = M == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(M - M_all);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -502,13 +501,14 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
     if (g == 0) l_sh[wave][n] = l_sum * f;
     __syncthreads();
     // 16 threads a row, 8 values each
+    if (WAVES > 4 && threadIdx.x >= 256) return;
     const int row = threadIdx.x >> 4, c = threadIdx.x & 15;
     const int t_row = __shfl(t, row, 64), head_row = __shfl(head, row, 64);   // lane `row` of every wave has row `row`
     const bool valid_row = __shfl(static_cast<int>(valid), row, 64) != 0;
     if (!valid_row) return;
     float l_all = 0.0f, out[8] = {};
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         l_all += l_sh[w][row];
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] += o_sh[w][row][8 * c + i];
@@ -524,7 +524,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void kv_attn_rows16(KvAttnArgs a, 
         float* p = a.partial + ((first_slot + split) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
         float M_row = m_sh[0][row];
 #pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w) M_row = __builtin_fmaxf(M_row, m_sh[w][row]);
+        for (int w = 1; w < WAVES; ++w) M_row = __builtin_fmaxf(M_row, m_sh[w][row]);
         if (l_all != 0.0f) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) reinterpret_cast<f2*>(p + 8 * c)[i] = f2{out[2 * i], out[2 * i + 1]};
@@ -1144,6 +1144,7 @@ struct Part {
     int rows;                      // 16: kv_attn_rows16; 128, 256: kv_attn_tile; 0: no tokens
     long long tiles;
     int splits, chunk;
+    int waves;                     // of a workgroup with 16 rows
 };
 
 struct Plan {
@@ -1154,23 +1155,29 @@ struct Plan {
 
 // `groups`: stretches of tokens (sequences, or one prefix); `ragged`: every group's rows begin a tile; `tokens`: the most
 // of a group.
-Part deal(int tile, long long rows, long long groups, bool ragged, int Hkv, int tokens) {
+Part deal(int tile, int waves, long long rows, long long groups, bool ragged, int Hkv, int tokens) {
     Part p = {};
     if (tokens <= 0) return p;
     p.rows = tile;
+    p.waves = waves;
     p.tiles = ragged ? rows / p.rows + groups : (rows + p.rows - 1) / p.rows;
     const long long busy = (rows / p.rows > groups ? rows / p.rows : groups) * Hkv;     // workgroups with rows
-    const bool uneven = groups * Hkv >= kManyGroups;
-    const long long wanted = p.rows != kRows ? kTilesWanted : uneven ? kRowsWantedUneven : kRowsWanted;
-    const int least = p.rows != kRows ? kTilesLeast : uneven ? kRowsLeastUneven : kRowsLeast;
-    // one tile a CU: no more than there are; of 16 rows several share one
-    long long splits = p.rows != kRows ? wanted / busy : (wanted + busy - 1) / busy;
-    if (splits * least > tokens) splits = (tokens + least - 1) / least;
+    long long splits;
+    if (tile != kRows) {
+        // one workgroup a CU: no more than there are
+        splits = kTilesWanted / busy;
+        p.chunk = kTilesLeast;
+    } else if (busy * waves >= kRowsWaves / 2) {
+        // shares of one size for all sequences, so that a long one does not hold up the rest
+        p.chunk = kLongShare * waves;
+        splits = (tokens + p.chunk - 1) / p.chunk;
+    } else {
+        splits = (kRowsWaves + busy * waves - 1) / (busy * waves);
+        p.chunk = kLeastShare * waves;
+    }
+    if (splits * p.chunk > tokens) splits = (tokens + p.chunk - 1) / p.chunk;
     if (splits > kMostSplits) splits = kMostSplits;
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
-    // many sequences: shares of one size, so that a long one does not hold up the rest; few: equal shares of each
-    const int even = (tokens + p.splits - 1) / p.splits;
-    p.chunk = uneven && even > least ? even : least;
     return p;
 }
 
@@ -1182,8 +1189,11 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     const int prefix_tile = rows < kManyRows || prefix_work < kTileWork ? kRows : prefix_work < kWideWork ? 128 : 256;
     int own_tile = rows / B < kManyRows || own_work < kTileWork ? kRows : own_work < 2 * kWideWork ? 128 : 256;
     if (own_tile != kRows && prefix_len > 0 && prefix_tile != kRows) own_tile = prefix_tile;     // one launch
-    p.prefix = deal(prefix_tile, rows, 1, false, Hkv, prefix_len);
-    p.own = deal(own_tile, rows, B, true, Hkv, max_kv);
+    const long long busy = (rows / kRows > B ? rows / kRows : B) * Hkv;
+    const int waves = prefix_len > 0 || (max_kv <= kShortest && busy * 8 >= kRowsWaves / 2) ? 4 : 8;
+    p.prefix = deal(prefix_tile, waves, rows, 1, false, Hkv, prefix_len);
+    p.own = deal(own_tile, waves, rows, B, true, Hkv, max_kv);
+    if (own_tile == kRows && prefix_len == 0 && max_kv <= kShort) p.own.splits = 1;     // the kernel's share is all
     p.splits = p.prefix.splits + p.own.splits;
     p.workspace = p.splits > 1 ? static_cast<size_t>(p.splits) * T * Hq * kPartial * sizeof(float) : 0;
     return p;
@@ -1193,12 +1203,18 @@ template <int BITS, int ROWS, bool FANCY>
 hipError_t launch_part(const KvAttnArgs& a, const Part& prefix, const Part& own, hipStream_t s) {
     const unsigned items = static_cast<unsigned>(prefix.tiles * prefix.splits + own.tiles * own.splits);
     const int pt = static_cast<int>(prefix.tiles), ot = static_cast<int>(own.tiles);
-    if constexpr (ROWS == kRows)
-        hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY>), dim3((items + 7) / 8 * 8 * a.Hkv), dim3(kAttnThreads), 0, s, a, pt, prefix.splits,
-                           prefix.chunk, ot, own.splits, own.chunk);
-    else
+    if constexpr (ROWS == kRows) {
+        const dim3 grid((items + 7) / 8 * 8 * a.Hkv);
+        if (own.waves == 8 || prefix.waves == 8)
+            hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY, 8>), grid, dim3(512), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
+                               own.chunk);
+        else
+            hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY, 4>), grid, dim3(256), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
+                               own.chunk);
+    } else {
         hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, FANCY>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
                            prefix.splits, prefix.chunk, ot, own.splits, own.chunk);
+    }
     return hipGetLastError();
 }
 

@@ -584,20 +584,33 @@ def _cache(cache, dev):
     shape = kc.shape
     n_pages, Hkv, page, width = shape
     bits = width // 16
-    scale = (n_pages, Hkv, page)
-    return (_want(kc, "K_codes", torch.uint8, shape, dev), _want(cache["K_scale"], "K_scale", torch.float16, scale, dev),
-            _want(cache["V_codes"], "V_codes", torch.uint8, (n_pages, Hkv, page // 4, 16, 4, bits), dev),
-            _want(cache["V_scale"], "V_scale", torch.float16, scale, dev)), n_pages, Hkv, page, bits
+    ks, vc, vs = cache["K_scale"], cache["V_codes"], cache["V_scale"]
+    scale, values, f16, u8 = (n_pages, Hkv, page), (n_pages, Hkv, page // 4, 16, 4, bits), torch.float16, torch.uint8
+    # the checks of _want, in one expression: this runs in every call
+    if not (kc.dtype is u8 and vc.dtype is u8 and ks.dtype is f16 and vs.dtype is f16 and ks.shape == scale and
+            vs.shape == scale and vc.shape == values and kc.get_device() == dev and ks.get_device() == dev and
+            vc.get_device() == dev and vs.get_device() == dev and kc.is_contiguous() and ks.is_contiguous() and
+            vc.is_contiguous() and vs.is_contiguous()):
+        _want(kc, "K_codes", u8, shape, dev)
+        _want(ks, "K_scale", f16, scale, dev)
+        _want(vc, "V_codes", u8, values, dev)
+        _want(vs, "V_scale", f16, scale, dev)
+    return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()), n_pages, Hkv, page, bits
 
 
 def _batch(page_table, q_start, kv_len, dev):
     """Check a batch's three arrays; returns the addresses of q_start, kv_len and page_table and (B, max_pages)."""
     if page_table.dim() != 2:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [B, max_pages]")
-    shape = page_table.shape
-    B, max_pages = shape
-    return (_want(q_start, "q_start", torch.int32, (B + 1,), dev), _want(kv_len, "kv_len", torch.int32, (B,), dev),
-            _want(page_table, "page_table", torch.int32, shape, dev)), B, max_pages
+    B, max_pages = page_table.shape
+    i32 = torch.int32
+    if not (q_start.dtype is i32 and kv_len.dtype is i32 and page_table.dtype is i32 and q_start.shape == (B + 1,) and
+            kv_len.shape == (B,) and q_start.get_device() == dev and kv_len.get_device() == dev and
+            page_table.get_device() == dev and q_start.is_contiguous() and kv_len.is_contiguous() and page_table.is_contiguous()):
+        _want(q_start, "q_start", i32, (B + 1,), dev)
+        _want(kv_len, "kv_len", i32, (B,), dev)
+        _want(page_table, "page_table", i32, (B, max_pages), dev)
+    return (q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr()), B, max_pages
 
 
 def _rows(x, name, dtype, T, dev):
@@ -656,7 +669,9 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
         if Q_out is None:
             Q_out = torch.empty((T, Hq, 128), dtype=torch.float16, device=Q.device)
             made = (Q_out,)
-        out = _want(Q_out, "Q_out", torch.float16, (T, Hq, 128), dev)
+            out = Q_out.data_ptr()
+        else:
+            out = _want(Q_out, "Q_out", torch.float16, (T, Hq, 128), dev)
     elif Q_out is not None:
         raise ValueError("Q_out without Q")
     qn = None if q_norm is None else _want(q_norm, "q_norm", torch.float32, (128,), dev)
@@ -704,7 +719,9 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
     if O is None:
         O = torch.empty_like(Q)
         made = (O,)
-    out = _want(O, "O", torch.float16, shape, dev)
+        out = O.data_ptr()
+    else:
+        out = _want(O, "O", torch.float16, shape, dev)
     if T == 0 or B == 0:            # an empty tensor has no address to pass
         return O
     need = spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page, prefix_len)
@@ -713,7 +730,7 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
         ws_bytes = workspace.numel()
         ws = _want(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
     elif need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=Q.device)
+        workspace = Q.new_empty((need + 1) // 2)
         ws, ws_bytes = workspace.data_ptr(), need
         made = (*made, workspace)
     _launch(fn, dev, made, stream,

@@ -254,9 +254,9 @@ def test_captured_calls_replay(q_len, prefix):
 
 def test_on_another_stream_and_with_a_workspace():
     rng = np.random.default_rng(14)
-    cache, kv = dev(pool(rng, 40, 1, 16, 4)), [600]
+    cache, kv = dev(pool(rng, 200, 1, 16, 4)), [3000]
     q = dev(rng.standard_normal((1, 8, 128)).astype(np.float16))
-    args = (q, cache, dev(tables(rng, kv, 16, 40)), dev(starts([1])), dev(np.array(kv, np.int32)))
+    args = (q, cache, dev(tables(rng, kv, 16, 200)), dev(starts([1])), dev(np.array(kv, np.int32)))
     want = host(spin.spin_kv_attn(*args))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())

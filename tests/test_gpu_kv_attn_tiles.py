@@ -129,6 +129,23 @@ def test_many_single_tokens(B):
     check(rng, [1] * B, rng.integers(0, 60, B).tolist(), 6, 2, 4, 16)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("more", [{}, dict(softcap=20.0), dict(alibi=True, window=2000), dict(bidir=True), dict(causal=False, window=40)])
+def test_long_contexts_in_shares(bits, more):
+    rng = np.random.default_rng(bits)
+    check(rng, [1, 2, 0, 1, 5], [2500, 6000, 3000, 1, 300], 6, 2, bits, 32, **more)
+    check(rng, [1, 1], [2048, 513], 20, 1, bits, 16, **more)                  # one share
+
+
+def test_one_long_sequence_among_many():
+    """Shares of one size for all, of which the others have one."""
+    rng = np.random.default_rng(2)
+    kv_len = rng.integers(0, 40, 260)
+    kv_len[[3, 200]] = 17000, 8200
+    check(rng, [1] * 260, kv_len.tolist(), 2, 1, 4, 64)
+    check(rng, [1] * 260, kv_len.tolist(), 16, 1, 8, 64, most=60)
+
+
 @pytest.mark.parametrize("work", WORK)
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
