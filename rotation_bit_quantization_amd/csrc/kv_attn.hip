@@ -38,17 +38,25 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kRows = 16;                 // query rows of a tile
 constexpr int kStep = 32;                 // tokens a wave takes at a time
-// Workgroups that fill the card, and the fewest tokens worth one, of the two kernels; the most shares of a row's tokens.
+// Shares of a sequence's tokens, tiles of 16 rows: waves that fill the card, and per wave of a workgroup the fewest tokens
+// worth a share and those of a share where there are workgroups enough without.  Up to kShort tokens there is one share and
+// no join (one token on 1000 tokens 11.9 us a call against 16.7 with shares of 128 and a join, 16 on 1500 15.4 and 17.7; 1 on
+// 3000 21.9 and 16.3); up to kShortest and in many workgroups four waves do (256 on 300: 28 us, with eight 39).
 constexpr int kRowsWaves = 4096, kLeastShare = 32, kLongShare = 1024;
 constexpr int kShort = 2048, kShortest = 512;
-constexpr int kTilesWanted = 256, kTilesLeast = 256;
+constexpr int kTilesWanted = 256, kTilesLeast = 256;      // tiles of 128 and 256: one a CU
 constexpr int kMostSplits = 256;
-constexpr int kCounted = 256;              // sequences up to which tiles of 16 rows are found by counting
+constexpr int kCounted = 256;             // sequences up to which tiles of 16 rows are found by counting
 constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kManyRows = 64;             // rows on the same tokens, and rows times tokens of all heads, from which ..
-constexpr double kTileWork = 1 << 25;     // .. tiles of 128 rows are taken, ..
-constexpr double kWideWork = 1 << 27;     // .. and of 256 (twice that of a sequence's own tokens: masks leave half of them)
+// Rows on the same tokens, and rows times tokens of all heads, from which tiles of 128 rows are taken, and of 256 (twice
+// that for a sequence's own tokens: masks leave half of them).  Measured in us on tiles of 16, 128, 256 rows with 32 + 8
+// heads: 16 sequences on 4096 tokens with 64 rows a key head each 56, 58, 77; 128 89, 67, 84; 256 153, 94, 106; 512 278,
+// 183, 151; 2048 1005, 661, 559.  One sequence on 4096: 256 rows 27, 29, 32; 512 36, 34, 40; 8192 219, 147, 143.  A prefix of
+// 2048: 1024 rows 48, 54, 62; of 8192: 512 55, 55, 60, 2048 172, 137, 132; of 32768: 128 53, 54, 62, 256 89, 72, 74, 2048 604,
+// 369, 335.
+constexpr int kManyRows = 64;
+constexpr double kTileWork = 1 << 25, kWideWork = 1 << 27;
 constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
 
 union Frag {
@@ -194,12 +202,18 @@ __device__ __forceinline__ int find_tile(int tiles, int b0, int tile, int& b) {
     return tile - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l));
 }
 
-// One tile of 16 query rows of one key head, over a share of the tokens: each
-// wave takes every fourth step of 32 tokens, the waves' results are joined in
-// LDS.  With one share the rows are finished here, otherwise they go to the
+// One tile of 16 query rows of one key head, over a share of the tokens: the
+// WAVES (4 or 8) waves take steps of 32 tokens in turn and are joined in LDS.
+// With one share the rows are finished here, otherwise they go to the
 // workspace, [share][T * Hq] rows.
 //
 // Bound at few rows: reading the cache, 2 (16 BITS + 2) bytes a token and head.
+// Codes go from memory to the lane that multiplies them, without LDS: 16 rows
+// leave nothing to share between waves.  Measured: 8 tokens of 32 + 8 heads on
+// 32768 each, INT8, capped, 102 us + 5 us for the join (550 MB, 5.4 TB/s); 64
+// on 0.25 .. 1 times 8192, INT4, 84 us (340 MB, 4.0 TB/s: the conversion of INT4
+// codes to fp16 takes as long as their reading); 1 on 1000 10 us, of which four
+// loads that wait for each other (sequence, length, page, codes) and four steps.
 template <int BITS, bool FANCY, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                   int own_tiles, int own_splits, int own_chunk) {
@@ -338,8 +352,8 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     // A step's codes and scales.  Lane (n, g) takes 32 codes of token n of each 16 and an octet of tokens 4 g .. 4 g + 3,
     // and the scales of one token: of lanes 0 .. 7 of a row of 16 lanes token 4 g + l of the first 16 (l < 4) or 4 g + l - 4
     // of the second, lanes 8 .. 15 again.  The next step's keys are loaded as soon as these are used, the values as soon
-    // as these are: each load has the other half of a step to arrive in, with one set of registers, so that four waves
-    // fit a SIMD (two sets, three waves: 91 instead of 85 us at 64 sequences of up to 8192).
+    // as these are: each load has the other half of a step to arrive in, with one set of registers, so that at 4 bits four
+    // waves fit a SIMD.
     uint32_t kraw[2][BITS], vraw[2 * BITS], ks_raw = 0, vs_raw = 0;
     bool there = false;
     const int s_half = (n >> 2) & 1, s_token = 4 * g + (n & 3);
@@ -572,6 +586,15 @@ __device__ __forceinline__ void part_barrier() {
 // that take half of the tokens each.  The waves share 64 tokens at a time,
 // which the workgroup turns into fp16 codes in LDS once, keys as [token][d] and
 // values as [d][token].
+//
+// Bound: the vector work of the softmax and of staging beside the matrix work.
+// Two waves share a SIMD; a step of 64 tokens and 256 rows holds 2 x 1024
+// cycles of MFMA, and 2 x (2 x 850) of exponents and weights, which overlap across
+// the waves but for the loads and the staging: 4150 cycles without fetching the
+// next step's codes, 4700 with.  Measured: a prompt of 8192 tokens, 32 + 8 heads,
+// INT4, 620 - 730 us (0.55 TFLOP, 0.75 - 0.89 PFLOP/s); uneven chunks of 1723
+// tokens, 32 + 32 heads, INT8, capped and with a distance bias, on up to 2900,
+// 160 - 172 us (32 exponentials and reciprocals a lane and 32 tokens more).
 template <int BITS, int ROWS, bool FANCY>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                 int own_tiles, int own_splits, int own_chunk) {
@@ -1086,7 +1109,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
 
 // Joins the shares of a row: one wave a row, two values a lane, eight shares'
 // sums in flight.  Shares without a visible token have not written their sums,
-// and are not read.
+// and are not read.  Bound by the launch and by loads in turn: 4 - 6 us at up to
+// 8192 rows.
 __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int splits) {
     const long long rows = static_cast<long long>(a.T) * a.Hq;
     const long long at = static_cast<long long>(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
@@ -1190,6 +1214,7 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     int own_tile = rows / B < kManyRows || own_work < kTileWork ? kRows : own_work < 2 * kWideWork ? 128 : 256;
     if (own_tile != kRows && prefix_len > 0 && prefix_tile != kRows) own_tile = prefix_tile;     // one launch
     const long long busy = (rows / kRows > B ? rows / kRows : B) * Hkv;
+    // a prefix's rows are many, and their tiles' waves work on shares: four suffice (64 tokens behind 8192: 38 us, eight 43)
     const int waves = prefix_len > 0 || (max_kv <= kShortest && busy * 8 >= kRowsWaves / 2) ? 4 : 8;
     p.prefix = deal(prefix_tile, waves, rows, 1, false, Hkv, prefix_len);
     p.own = deal(own_tile, waves, rows, B, true, Hkv, max_kv);
@@ -1205,7 +1230,7 @@ hipError_t launch_part(const KvAttnArgs& a, const Part& prefix, const Part& own,
     const int pt = static_cast<int>(prefix.tiles), ot = static_cast<int>(own.tiles);
     if constexpr (ROWS == kRows) {
         const dim3 grid((items + 7) / 8 * 8 * a.Hkv);
-        if (own.waves == 8 || prefix.waves == 8)
+        if (own.waves == 8)
             hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY, 8>), grid, dim3(512), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
                                own.chunk);
         else

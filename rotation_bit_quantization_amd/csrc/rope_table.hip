@@ -16,6 +16,11 @@
 // the angle, turns the pair by the first order, (c - s e, s + c e).  Below 2^25
 // radians e^2 / 2 is below 2^-55; angles above take the functions every time.
 // Eight steps add less than 27 * 2^-53 (a step 2.4 * 2^-53 in each of the pair).
+//
+// Bound: writing the table.  Measured: 40960 positions of 64 pairs 7.4 us (21 MB,
+// 2.8 TB/s; a launch's 3 us among them), 262144 of 32 12.9 us (67 MB, 5.2 TB/s);
+// with the functions for every pair 12 and 29 us.  Runs of 8 and 32: 7.5 and 14.4,
+// 7.2 and 14.6.
 #include "spin_internal.h"
 
 namespace spin {
