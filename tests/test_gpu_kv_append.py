@@ -243,3 +243,26 @@ def test_a_layer_serves_a_prompt_and_then_tokens(bits, graph):
         close(host(O).astype(np.float64), ref, bound)
         want, _ = oracle.quantize_rows(host(O).reshape(sum(n), Hq * 128).astype(np.float32))
         assert np.array_equal(host(codes), oracle.pack_int4(want))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(336, 31, 17), (1030, 30, 18), (1400, 1, 23)])     # two, four and four heads a lane group
+@pytest.mark.parametrize("bits,dtype,rot,interleaved,norm", [(4, np.float32, 128, False, True), (8, np.float16, 64, True, False),
+                                                             (8, np.float32, 48, False, True), (4, np.float16, 0, False, False)])
+def test_several_heads_of_a_token_at_once(T, Hq, Hkv, bits, dtype, rot, interleaved, norm):
+    rng = np.random.default_rng(T + bits)
+    q_len = [T - 120, 0, 1, 90, 20]
+    kv_len = [T - 120 + 7, 30, 9, 60, 25]          # the fourth has more new tokens than tokens
+    check(rng, q_len, kv_len, Hq, Hkv, bits, 64, dtype=dtype, rot=rot, interleaved=interleaved, norm=norm, before=3, behind=6,
+          rope_len=T - 130 if rot else None)
+
+
+def test_rope_table_of_any_frequency():
+    """Turned a step at a time below 2^25 radians, by the functions above; the formula's value on both sides of it."""
+    inv = np.array([300.0, -0.7, 0.0, 1e5, 2.0 ** 25 / 4100, -2.0 ** 25 / 4100, 1e-300, 1e20, 2.0 ** 60, np.inf, np.nan])
+    for pos0 in (0, 4000, (1 << 25) - 20, (1 << 29) - 333):
+        with np.errstate(invalid="ignore"):
+            ref = oracle.rope_table(inv, 333, pos0)
+        got = host(spin.spin_rope_table(dev(inv), 333, pos0=pos0))
+        bad = np.isnan(ref)
+        assert np.isnan(got[bad]).all()
+        assert (np.abs(got - ref)[~bad] <= 2.0 ** -24 * np.abs(ref[~bad]) + 2.0 ** -48).all()
