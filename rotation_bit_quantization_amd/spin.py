@@ -619,15 +619,16 @@ def _rows(x, name, dtype, T, dev):
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{name} must be a [{T}, H, 128] tensor")
     rows, H, D = x.shape
-    if rows != T or D != 128:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{T}, H, 128]")
-    if x.get_device() != dev:
-        raise ValueError(f"{name} lives on {x.device}, the others on GPU {dev}")
-    if x.dtype is not dtype or dtype not in (torch.float16, torch.float32):
-        raise TypeError(f"{name} has dtype {x.dtype}, expected float16 or float32, the same for all")
     per_token, per_head, per_value = x.stride()
-    if T and H and (per_value != 1 or (H > 1 and per_head != 128)):
-        raise ValueError(f"{name}: the heads of a token must lie beside each other (strides {x.stride()})")
+    if not (rows == T and D == 128 and x.get_device() == dev and x.dtype is dtype and per_head == 128 and per_value == 1):
+        if rows != T or D != 128:
+            raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{T}, H, 128]")
+        if x.get_device() != dev:
+            raise ValueError(f"{name} lives on {x.device}, the others on GPU {dev}")
+        if x.dtype is not dtype:
+            raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}, the same for all")
+        if T and H and (per_value != 1 or (H > 1 and per_head != 128)):
+            raise ValueError(f"{name}: the heads of a token must lie beside each other (strides {x.stride()})")
     return x.data_ptr(), H, per_token if T > 1 else max(128 * H, 128)
 
 
@@ -658,6 +659,8 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
     T, dtype = K.shape[0], K.dtype
+    if dtype is not torch.float16 and dtype is not torch.float32:
+        raise TypeError(f"K has dtype {dtype}, expected float16 or float32")
     k, hk, k_stride = _rows(K, "K", dtype, T, dev)
     v, hv, v_stride = _rows(V, "V", dtype, T, dev)
     if hk != Hkv or hv != Hkv:
@@ -667,7 +670,7 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     if Q is not None:
         q, Hq, q_stride = _rows(Q, "Q", dtype, T, dev)
         if Q_out is None:
-            Q_out = torch.empty((T, Hq, 128), dtype=torch.float16, device=Q.device)
+            Q_out = Q.new_empty((T, Hq, 128), dtype=torch.float16)
             made = (Q_out,)
             out = Q_out.data_ptr()
         else:
