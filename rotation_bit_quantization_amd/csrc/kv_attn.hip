@@ -590,8 +590,7 @@ __device__ __forceinline__ void part_barrier() {
 // Bound: the vector work of the softmax and of staging beside the matrix work.
 // Two waves share a SIMD; a step of 64 tokens and 256 rows holds 2 x 1024
 // cycles of MFMA, and 2 x (2 x 850) of exponents and weights, which overlap across
-// the waves but for the loads and the staging: 4150 cycles without fetching the
-// next step's codes, 4700 with.  Measured: a prompt of 8192 tokens, 32 + 8 heads,
+// the waves but for the loads and the staging, 400 - 550 cycles.  Measured: a prompt of 8192 tokens, 32 + 8 heads,
 // INT4, 620 - 730 us (0.55 TFLOP, 0.75 - 0.89 PFLOP/s); uneven chunks of 1723
 // tokens, 32 + 32 heads, INT8, capped and with a distance bias, on up to 2900,
 // 160 - 172 us (32 exponentials and reciprocals a lane and 32 tokens more).
@@ -1036,12 +1035,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
             fetch_later(st + 3);
         } else {
             matrix_part(buf, 1, true, next);
-            fetch_later(st + 2);
             __syncthreads();
             load_values(buf, 1);
             if (some) vector_part(j0 + 32, whole);
             part_barrier();
             matrix_part(next, 0, false, 0);
+            fetch_later(st + 2);           // here, not behind M0, which staging makes the longer part: 735 against 752 us
         }
         if (kPair)
             __syncthreads();
