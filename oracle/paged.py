@@ -123,6 +123,8 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
         if prefix_len:
             front = cache_tokens(cache, prefix_table, h, prefix_len)
         for b in range(len(kv_len)):
+            if rows is not None and not any(t in rows for t in range(q_start[b], q_start[b + 1])):
+                continue
             kv = min(max(int(kv_len[b]), 0), table.shape[1] * page)
             parts = cache_tokens(cache, table[b], h, kv)
             if prefix_len:

@@ -553,6 +553,14 @@ def _want(t, name, dtype, shape, dev):
     raise ValueError(f"{name} lives on {t.device}, the others on GPU {dev}")
 
 
+def _int(x, name):
+    """x as a C int takes it; ctypes would drop the bits above."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} is {x}, beyond 32 bits")
+    return x
+
+
 def _gpu(t, name):
     """The number of the GPU a tensor lives on."""
     if not isinstance(t, torch.Tensor):
@@ -645,7 +653,7 @@ def spin_rope_table(inv_freq, n_pos, pos0=0, attn_scale=1.0, table=None, stream=
         made = (table,)
     out = _want(table, "table", torch.float32, (n_pos, 2 * n), dev)
     if n_pos != 0:                  # an empty tensor has no address to pass
-        _launch("spin_rope_table", dev, made, stream, (freq, n, int(pos0), n_pos, float(attn_scale), out))
+        _launch("spin_rope_table", dev, made, stream, (freq, n, _int(pos0, "pos0"), n_pos, float(attn_scale), out))
     return table
 
 
@@ -688,7 +696,7 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     if T != 0 and B != 0:           # an empty tensor has no address to pass
         _launch("spin_kv_append", dev, made, stream,
                 (q, k, v, SPIN_F16 if dtype is torch.float16 else SPIN_F32, T, Hq, Hkv, 128, q_stride, k_stride, v_stride, qn,
-                 kn, eps, rows, rope_len, rot_dim, int(interleaved), int(pos0), bits, kc, ks, vc, vs, n_pages, page, B, starts,
+                 kn, eps, rows, rope_len, rot_dim, _int(interleaved, "interleaved"), _int(pos0, "pos0"), bits, kc, ks, vc, vs, n_pages, page, B, starts,
                  lens, table, max_pages, out))
     return Q_out
 
@@ -738,7 +746,7 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
         made = (*made, workspace)
     _launch(fn, dev, made, stream,
             (q, T, Hq, Hkv, 128, bits, kc, ks, vc, vs, n_pages, page, *front, B, starts, lens, table, max_pages,
-             0.08838834764831845 if scale is None else scale, softcap, slope, int(window), int(causal), both, out, ws, ws_bytes))
+             0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both, out, ws, ws_bytes))
     return O
 
 

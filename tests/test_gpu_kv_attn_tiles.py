@@ -129,6 +129,23 @@ def test_many_single_tokens(B):
     check(rng, [1] * B, rng.integers(0, 60, B).tolist(), 6, 2, 4, 16)
 
 
+def test_more_sequences_behind_a_prefix_than_a_workgroup_can_list():
+    B = 28000
+    rng = np.random.default_rng(B)
+    check(rng, [1] * B, rng.integers(0, 4, B).tolist(), 1, 1, 4, 16, prefix_len=1300, most=60, before=1, behind=1)
+
+
+@pytest.mark.parametrize("work", [0] + WORK)
+def test_the_widest_window_is_none(work):
+    rng = np.random.default_rng(4)
+    cache, table = pool(rng, 40, 1, 16, 4), tables(rng, [90, 300], 16, 40)
+    q, q_start = rng.standard_normal((160, 2, 128)).astype(np.float16), starts([80, 80])
+    table = widened(table, 320, 1, 16, work)
+    for causal in (True, False):
+        a, b = (attend(q, cache, table, q_start, [90, 300], window=w, causal=causal) for w in (0, 2 ** 31 - 1))
+        assert np.array_equal(a, b)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("more", [{}, dict(softcap=20.0), dict(alibi=True, window=2000), dict(bidir=True), dict(causal=False, window=40)])
 def test_long_contexts_in_shares(bits, more):
@@ -255,3 +272,16 @@ def test_captured_calls_replay(work):
             O.fill_(5.0)
             g.replay()
             assert np.array_equal(host(O), want), rep
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    rng = np.random.default_rng(15)
+    cache, q = dev(pool(rng, 4, 2, 16, 4)), dev(rng.standard_normal((2, 4, 128)).astype(np.float16))
+    batch = dev(np.zeros((1, 2), np.int32)), dev(np.array([0, 2], np.int32)), dev(np.array([20], np.int32))
+    for bad in (dict(window=2 ** 32 + 5), dict(window=-2 ** 32 + 5), dict(causal=2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            spin.spin_kv_attn(q, cache, *batch, **bad)
+    with pytest.raises(ValueError):
+        spin.spin_kv_append(q, q[:, :2].contiguous(), q[:, :2].contiguous(), cache, *batch, pos0=2 ** 32)
+    with pytest.raises(ValueError):
+        spin.spin_rope_table(torch.ones(4, dtype=torch.float64, device=DEV), 8, pos0=2 ** 32)
