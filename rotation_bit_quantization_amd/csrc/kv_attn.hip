@@ -202,6 +202,28 @@ __device__ __forceinline__ int find_tile(int tiles, int b0, int tile, int& b) {
     return tile - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l));
 }
 
+// Up to 64 sequences, a lane each: their tiles' counts and their numbers in the order of their lengths, the longest first,
+// in steps of a sixteenth of the longest.  Workgroups take sequences in this order, which costs equal lengths 0.5 us and
+// brings 64 of 0.25 .. 1 times 8192 tokens from 85 to 73 us, 48 of u^4 times 16384 (u even in 0 .. 1) from 92 to 59.
+__device__ __forceinline__ void longest_first(const KvAttnArgs& a, int lane, int& tiles, int& id) {
+    const bool there = lane < a.B;
+    const float length = there ? static_cast<float>(context(a, lane)) : 0.0f;
+    float top = max_over_groups(length);
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m, 64));
+    const int step = there ? 15 - min(static_cast<int>(length * 15.999f * __builtin_amdgcn_rcpf(__builtin_fmaxf(top, 1.0f))), 15) : 16;
+    int rank = lane, before = 0;       // lanes without a sequence stay behind the others
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const unsigned long long same = __ballot(step == k);
+        const int at = before + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(same >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(same), 0));
+        rank = step == k ? at : rank;
+        before += __popcll(same);
+    }
+    tiles = __builtin_amdgcn_ds_permute(rank << 2, tiles);
+    id = __builtin_amdgcn_ds_permute(rank << 2, id);
+}
+
 // One tile of 16 query rows of one key head, over a share of the tokens: the
 // WAVES (4 or 8) waves take steps of 32 tokens in turn and are joined in LDS.
 // With one share the rows are finished here, otherwise they go to the
@@ -211,9 +233,10 @@ __device__ __forceinline__ int find_tile(int tiles, int b0, int tile, int& b) {
 // Codes go from memory to the lane that multiplies them, without LDS: 16 rows
 // leave nothing to share between waves.  Measured: 8 tokens of 32 + 8 heads on
 // 32768 each, INT8, capped, 102 us + 5 us for the join (550 MB, 5.4 TB/s); 64
-// on 0.25 .. 1 times 8192, INT4, 84 us (340 MB, 4.0 TB/s: the conversion of INT4
-// codes to fp16 takes as long as their reading); 1 on 1000 10 us, of which four
-// loads that wait for each other (sequence, length, page, codes) and four steps.
+// on 0.25 .. 1 times 8192, INT4, 73 us (340 MB, 4.7 TB/s; the vector pipes are
+// busy half of it with turning INT4 codes to fp16, and the last sequences run
+// alone), on 8192 each 5.4 TB/s; 1 on 1000 10 us, of which four loads that wait
+// for each other (sequence, length, page, codes) and four steps.
 template <int BITS, bool FANCY, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                   int own_tiles, int own_splits, int own_chunk) {
@@ -253,6 +276,19 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         int own = tile;
         if (a.B == 1) {
             b = 0;
+        } else if (a.B <= 64) {
+            int tiles = count_tiles<kRows>(a, G, 0, lane), id = lane;
+            if (a.B > 8 && a.max_pages << a.page_log2 > kShort) {
+                // Two workgroups of eight waves a CU: the longest first, and where they all run at once those that come
+                // second to a CU the shortest first.
+                longest_first(a, lane, tiles, id);
+                const int all = __builtin_amdgcn_readlane(sums_up_to(tiles), 63), half = 256 / a.Hkv;
+                if (all <= 2 * half && own >= half && own < all) own = half + all - 1 - own;
+            }
+            b = -1;
+            own = find_tile(tiles, 0, own, b);
+            if (b < 0) return;
+            b = __builtin_amdgcn_readlane(id, b);
         } else if (a.B <= kCounted) {
             b = -1;
             for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) own = find_tile(count_tiles<kRows>(a, G, b0, lane), b0, own, b);

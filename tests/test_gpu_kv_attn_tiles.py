@@ -154,6 +154,19 @@ def test_long_contexts_in_shares(bits, more):
     check(rng, [1, 1], [2048, 513], 20, 1, bits, 16, **more)                  # one share
 
 
+@pytest.mark.parametrize("B", [8, 9, 33, 64])
+@pytest.mark.parametrize("G,Hkv", [(4, 8), (16, 2), (3, 1)])
+def test_sequences_taken_in_the_order_of_their_lengths(B, G, Hkv):
+    """Equal lengths, lengths of zero, one far longer than the rest; one token each, then some with several tiles."""
+    rng = np.random.default_rng(B + G)
+    for q_len in (np.ones(B, int), rng.integers(0, 9, B)):
+        for kv_len in (np.full(B, 70), q_len + rng.integers(0, 200, B), np.where(np.arange(B) == B // 2, 2600, q_len)):
+            kv_len = kv_len * (rng.random(B) > 0.1)
+            table = tables(rng, kv_len, 64, int((-(-kv_len // 64)).sum()) + 2)
+            table = np.pad(table, ((0, 0), (0, max(0, 40 - table.shape[1]))), constant_values=-1)      # room for 2560 tokens
+            check(rng, q_len.tolist(), kv_len.tolist(), G * Hkv, Hkv, 4, 64, table=table, before=1, behind=1, most=40)
+
+
 def test_one_long_sequence_among_many():
     """Shares of one size for all, of which the others have one."""
     rng = np.random.default_rng(2)
