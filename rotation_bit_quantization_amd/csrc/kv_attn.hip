@@ -627,9 +627,9 @@ __device__ __forceinline__ void part_barrier() {
 // Two waves share a SIMD; a step of 64 tokens and 256 rows holds 2 x 1024
 // cycles of MFMA, and 2 x (2 x 850) of exponents and weights, which overlap across
 // the waves but for the loads and the staging, 400 - 550 cycles.  Measured: a prompt of 8192 tokens, 32 + 8 heads,
-// INT4, 620 - 730 us (0.55 TFLOP, 0.75 - 0.89 PFLOP/s); uneven chunks of 1723
+// INT4, 605 - 735 us (0.55 TFLOP, 0.75 - 0.91 PFLOP/s); uneven chunks of 1723
 // tokens, 32 + 32 heads, INT8, capped and with a distance bias, on up to 2900,
-// 160 - 172 us (32 exponentials and reciprocals a lane and 32 tokens more).
+// 154 - 173 us (32 exponentials and reciprocals a lane and 32 tokens more).
 template <int BITS, int ROWS, bool FANCY>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                 int own_tiles, int own_splits, int own_chunk) {
@@ -656,7 +656,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const bool shared = index < prefix_items;
     const int splits = shared ? prefix_splits : own_splits;
     const int item = shared ? index : index - prefix_items;
-    int tile = item / splits;                      // own: counted from the last one
+    int tile = item / splits;
     const int split = item - tile * splits;
     const int first_slot = shared ? 0 : prefix_splits;
     const int total_splits = prefix_splits + own_splits;
@@ -685,16 +685,25 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
             if (a.bidir_len) both = a.bidir_len[b];
         }
     } else {
-        // the last tiles, the long ones, come first; the grid has room for a ragged tile of every sequence
-        int all = count_tiles<ROWS>(a, G, 0, lane);
-        const int mine = all;
-        for (int b0 = 64; b0 < a.B; b0 += 64) all += count_tiles<ROWS>(a, G, b0, lane);
-        all = __builtin_amdgcn_readlane(sums_up_to(all), 63);
-        if (tile >= all) return;
+        // The longest sequences come first (12 chunks of 7566 tokens on up to 5000: 383 -> 341 us), and of each its last tiles;
+        // the grid has room for a ragged tile of every sequence.
         int b = -1;
-        tile = all - 1 - tile;
-        for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) tile = find_tile(b0 == 0 ? mine : count_tiles<ROWS>(a, G, b0, lane), b0, tile, b);
-        if (b < 0) return;                         // borders that do not ascend
+        if (a.B <= 64) {
+            int tiles = count_tiles<ROWS>(a, G, 0, lane), id = lane;
+            if (a.B > 1) longest_first(a, lane, tiles, id);
+            tile = find_tile(tiles, 0, tile, b);
+            if (b < 0) return;
+            tile = __builtin_amdgcn_readlane(tiles, b) - 1 - tile;
+            b = __builtin_amdgcn_readlane(id, b);
+        } else {
+            int all = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 64) all += count_tiles<ROWS>(a, G, b0, lane);
+            all = __builtin_amdgcn_readlane(sums_up_to(all), 63);
+            if (tile >= all) return;
+            tile = all - 1 - tile;
+            for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) tile = find_tile(count_tiles<ROWS>(a, G, b0, lane), b0, tile, b);
+            if (b < 0) return;                     // borders that do not ascend
+        }
         const int first = tile * ROWS;
         const int q0 = within(a.q_start[b], a.T), q1 = within(a.q_start[b + 1], a.T);
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
