@@ -226,8 +226,9 @@ __device__ __forceinline__ void longest_first(const KvAttnArgs& a, int lane, int
 
 // One tile of 16 query rows of one key head, over a share of the tokens: the
 // WAVES (4 or 8) waves take steps of 32 tokens in turn and are joined in LDS.
-// With one share the rows are finished here, otherwise they go to the
-// workspace, [share][T * Hq] rows.
+// With one share the rows are finished here, with what a prefix has left in the
+// workspace in an earlier launch, otherwise they go to the workspace, [share][T *
+// Hq] rows.
 //
 // Bound at few rows: reading the cache, 2 (16 BITS + 2) bytes a token and head.
 // Codes go from memory to the lane that multiplies them, without LDS: 16 rows
@@ -258,7 +259,6 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     const int splits = shared ? prefix_splits : own_splits;
     const int tile = item / splits, split = item - tile * splits;
     const int first_slot = shared ? 0 : prefix_splits;   // of the workspace
-    const int total_splits = prefix_splits + own_splits;
 
     // the rows: (token, head of the group) pairs, of one sequence or (prefix) of all
     Span span;
@@ -564,17 +564,12 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         for (int i = 0; i < 8; ++i) out[i] += o_sh[w][row][8 * c + i];
     }
     const long long at = static_cast<long long>(t_row) * a.Hq + head_row;
-    if (total_splits == 1) {
-        const float rl = l_all == 0.0f ? 0.0f : 1.0f / l_all;
-        Frag res;
+    float M_row = m_sh[0][row];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) res.v[i] = static_cast<_Float16>(out[i] * rl);
-        *reinterpret_cast<u4*>(a.O + at * 128 + 8 * c) = u4{res.w[0], res.w[1], res.w[2], res.w[3]};
-    } else {
+    for (int w = 1; w < WAVES; ++w) M_row = __builtin_fmaxf(M_row, m_sh[w][row]);
+    const bool last = prefix_tiles == 0 && own_splits == 1;        // what the prefix gave is there: an earlier launch's
+    if (!last) {
         float* p = a.partial + ((first_slot + split) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
-        float M_row = m_sh[0][row];
-#pragma unroll
-        for (int w = 1; w < WAVES; ++w) M_row = __builtin_fmaxf(M_row, m_sh[w][row]);
         if (l_all != 0.0f) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) reinterpret_cast<f2*>(p + 8 * c)[i] = f2{out[2 * i], out[2 * i + 1]};
@@ -583,7 +578,47 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
             p[128] = M_row;
             p[129] = l_all;
         }
+        return;
     }
+    // joins them, as kv_attn_join does, four shares at a time
+    float M_run = l_all == 0.0f ? -__builtin_inff() : M_row;
+    for (int s0 = 0; s0 < prefix_splits; s0 += 4) {
+        f2 ml[4], y[4][4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const float* p = a.partial + (min(s0 + s, prefix_splits - 1) * static_cast<long long>(a.T) * a.Hq + at) * kPartial;
+            ml[s] = *reinterpret_cast<const f2*>(p + 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[s][i] = reinterpret_cast<const f2*>(p + 8 * c)[i];
+        }
+        float M_new = M_run;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            ml[s].y = s0 + s < prefix_splits ? ml[s].y : 0.0f;
+            M_new = ml[s].y == 0.0f ? M_new : __builtin_fmaxf(M_new, ml[s].x);
+        }
+        const float keep = M_run == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(M_run - M_new);
+        l_all = l_all == 0.0f ? 0.0f : l_all * keep;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = l_all == 0.0f ? 0.0f : out[i] * keep;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (ml[s].y == 0.0f) continue;         // no token seen: its sums are not written
+            const float f = __builtin_amdgcn_exp2f(ml[s].x - M_new);
+            l_all = __builtin_fmaf(ml[s].y, f, l_all);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                out[2 * i] = __builtin_fmaf(y[s][i].x, f, out[2 * i]);
+                out[2 * i + 1] = __builtin_fmaf(y[s][i].y, f, out[2 * i + 1]);
+            }
+        }
+        M_run = M_new;
+    }
+    const float rl = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+    Frag res;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) res.v[i] = static_cast<_Float16>(out[i] * rl);
+    *reinterpret_cast<u4*>(a.O + at * 128 + 8 * c) = u4{res.w[0], res.w[1], res.w[2], res.w[3]};
 }
 
 // ---------------------------------------------------------------------------------------------- many rows
@@ -1322,7 +1357,8 @@ bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
 hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s) {
     const Plan p = plan(a.T, a.Hq, a.Hkv, a.B, a.max_pages << a.page_log2, a.prefix_len);
     const hipError_t e = bits == 8 ? launch_bits<8>(a, p, s) : launch_bits<4>(a, p, s);
-    if (e != hipSuccess || p.splits == 1) return e;
+    // where a prefix has an earlier launch and the sequences' own tokens one share of 16 rows, that joins what both give
+    if (e != hipSuccess || p.splits == 1 || (p.own.rows == kRows && p.own.splits == 1 && p.prefix.rows > kRows)) return e;
     const long long rows = static_cast<long long>(a.T) * a.Hq;
     hipLaunchKernelGGL(kv_attn_join, dim3(static_cast<unsigned>((rows + kAttnWaves - 1) / kAttnWaves)), dim3(kAttnThreads), 0,
                        s, a, p.splits);
