@@ -49,6 +49,9 @@ constexpr int kMostSplits = 256;
 constexpr int kCounted = 256;             // sequences up to which tiles of 16 rows are found by counting
 constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
 constexpr float kLog2e = 1.4426950408889634f;
+// Caps up to this one go by capped_plus, whose error is that of a number of the cap's size, above by capped_wide, which is
+// ten operations longer (8 tokens on 32768, INT8, cap 50: 108 and 111 us; 1723 in chunks, cap 30 and a bias: 160 and 191).
+constexpr float kNearCap = 64.0f;
 // Rows on the same tokens, and rows times tokens of all heads, from which tiles of 128 rows are taken, and of 256 (twice
 // that for a sequence's own tokens: masks leave half of them).  Measured in us on tiles of 16, 128, 256 rows with 32 + 8
 // heads: 16 sequences on 4096 tokens with 64 rows a key head each 56, 58, 77; 128 89, 67, 84; 256 153, 94, 106; 512 278,
@@ -142,10 +145,44 @@ __device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
 }
 
-// A capped score in the exponent: cap log2(e) tanh(z) = top - 2 top / (2^y + 1), y = 2 log2(e) z, right at both
-// infinities.  `lm` is what is added to it, `top` = cap log2(e) already among it.
+// A capped score in the exponent: cap log2(e) tanh(z / cap) = top - 2 top / (2^y + 1), y = 2 log2(e) z / cap, right at
+// both infinities.  `lm` is what is added to it, `top` = cap log2(e) already among it.  The two terms are of the size of
+// the cap whatever the score is, so that their roundings are: ten of 2^-24 cap (2^-21.7 cap measured).  At caps up to
+// kNearCap that is below a twelfth of the rounding of the weight to fp16.
 __device__ __forceinline__ float capped_plus(float y, float top, float lm) {
     return __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y) + 1.0f), -2.0f * top, lm);
+}
+
+// The same for any cap, off by at most 2^-18 of the score: z tanh(u) / u by its series (the next term is 2^-26 at 1/4)
+// where |u| = |z| / cap is small, the form above where the score is a quarter of the cap or more.  z in units of
+// 1 / log2(e), `rtop` = 1 / top.
+__device__ __forceinline__ float capped_wide(float z, float top, float rtop) {
+    const float u = z * rtop, u2 = u * u;
+    float p = __builtin_fmaf(u2, 62.0f / 2835.0f, -17.0f / 315.0f);
+    p = __builtin_fmaf(p, u2, 2.0f / 15.0f);
+    p = __builtin_fmaf(p, u2, -1.0f / 3.0f);
+    p = __builtin_fmaf(p, u2, 1.0f);
+    const float far = __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(u * (2.0f * kLog2e)) + 1.0f), -2.0f * top, top);
+    return __builtin_fabsf(u) < 0.25f ? z * p : far;
+}
+
+// What a kernel does to the scores: nothing; a distance bias, a cap up to kNearCap, or both; a cap above, with or without
+// a bias.
+enum Scores { kPlain, kFancy, kWideCap };
+
+// How a score is capped: the factor of a product and its key's scale, the cap in units of 1 / log2(e) (0: none) and its
+// reciprocal.
+struct Cap {
+    float factor, top, rtop;
+};
+template <int SCORES>
+__device__ __forceinline__ Cap cap_of(const KvAttnArgs& a) {
+    if (SCORES == kWideCap) {
+        const float top = __builtin_fminf(a.softcap * kLog2e, 0x1p126f);       // its double has to be finite
+        return {a.scale * kLog2e, top, 1.0f / top};
+    }
+    const bool capped = SCORES == kFancy && a.softcap > 0.0f;
+    return {capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e, capped ? a.softcap * kLog2e : 0.0f, 0.0f};
 }
 
 // Tokens of sequence b in its own pages.
@@ -238,7 +275,7 @@ __device__ __forceinline__ void longest_first(const KvAttnArgs& a, int lane, int
 // busy half of it with turning INT4 codes to fp16, and the last sequences run
 // alone), on 8192 each 5.4 TB/s; 1 on 1000 10 us, of which four loads that wait
 // for each other (sequence, length, page, codes) and four steps.
-template <int BITS, bool FANCY, int WAVES>
+template <int BITS, int SCORES, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                   int own_tiles, int own_splits, int own_chunk) {
     __shared__ float o_sh[WAVES][kRows][129];
@@ -369,10 +406,10 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         const float c = sum_over_groups(sum) * (BITS == 4 ? -0x1p-21f : -0x1p-17f);
         start = f4{c, c, c, c};
     }
-    const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
-    const bool capped = FANCY && a.softcap > 0.0f;
-    const float key_factor = (capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e) * 0x1p24f;
-    const float cap_top = capped ? a.softcap * kLog2e : 0.0f;
+    const float slope = SCORES != kPlain && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+    const bool near_cap = SCORES == kFancy && a.softcap > 0.0f;
+    const Cap cap = cap_of<SCORES>(a);
+    const float key_factor = cap.factor * 0x1p24f;
 
     // Of the wave's next 32 steps, a lane each and half of a step: where the 16 tokens lie, as the number of the first, ~0
     // if nowhere.
@@ -467,17 +504,18 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         const int next = i + 1 < turns ? i + 1 : i;
         if ((next & 31) == 0 && next > 0) load_places(next);
         fetch_keys(next);
-        const float from = M - cap_top;
+        const float from = SCORES == kFancy ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * g);
-        auto exponent = [&](int e, float k, float lm, bool cap) __attribute__((always_inline)) {
-            if (FANCY) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
-            x[e] = cap ? capped_plus(x[e] * k, cap_top, lm) : __builtin_fmaf(x[e], k, lm);
+        auto exponent = [&](int e, float k, float lm, bool capped) __attribute__((always_inline)) {
+            if (SCORES != kPlain) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
+            x[e] = SCORES == kWideCap ? capped_wide(x[e] * k, cap.top, cap.rtop) + lm
+                                      : capped ? capped_plus(x[e] * k, cap.top, lm) : __builtin_fmaf(x[e], k, lm);
         };
 #define SPIN_ONE(N, CAP) exponent(N, row_lane<N>(kf), row_lane<N>(lv) - from, CAP);
 #define SPIN_ALL(CAP)                                                                     \
     SPIN_ONE(0, CAP) SPIN_ONE(1, CAP) SPIN_ONE(2, CAP) SPIN_ONE(3, CAP) SPIN_ONE(4, CAP) \
     SPIN_ONE(5, CAP) SPIN_ONE(6, CAP) SPIN_ONE(7, CAP)
-        if (capped) {
+        if (near_cap) {
             SPIN_ALL(true)
         } else {
             SPIN_ALL(false)
@@ -665,7 +703,7 @@ __device__ __forceinline__ void part_barrier() {
 // INT4, 605 - 735 us (0.55 TFLOP, 0.75 - 0.91 PFLOP/s); uneven chunks of 1723
 // tokens, 32 + 32 heads, INT8, capped and with a distance bias, on up to 2900,
 // 154 - 173 us (32 exponentials and reciprocals a lane and 32 tokens more).
-template <int BITS, int ROWS, bool FANCY>
+template <int BITS, int ROWS, int SCORES>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                 int own_tiles, int own_splits, int own_chunk) {
     constexpr bool kPair = ROWS == 128;            // two waves a row
@@ -825,10 +863,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         }
     }
     const int at_row = valid ? t * a.Hq + head : -1;       // T * Hq is below 2^26
-    const float slope = FANCY && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
-    const bool capped = FANCY && a.softcap > 0.0f;
-    const float key_factor = capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e;
-    const float cap_top = capped ? a.softcap * kLog2e : 0.0f;
+    const float slope = SCORES != kPlain && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+    const bool near_cap = SCORES == kFancy && a.softcap > 0.0f;
+    const Cap cap = cap_of<SCORES>(a);
+    const float key_factor = cap.factor;
 
     // What a wave stages of a step: eight tokens' keys, eight tokens' values and eight tokens' scales of both, all of the
     // same 16 tokens, which lie in one page.  The keys are tokens 8 w .. 8 w + 7 of the step, the values those of two
@@ -934,19 +972,20 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     };
     // products to exponents of the tokens at positions j0 .. j0 + 31, relative to M
     auto exponents = [&](int j0) __attribute__((always_inline)) {
-        const float from = M - cap_top;
+        const float from = SCORES == kFancy ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * hf);
-        auto one = [&](int e, float lm, bool cap) __attribute__((always_inline)) {
+        auto one = [&](int e, float lm, bool capped) __attribute__((always_inline)) {
             const float k = kf[e >> 2][e & 3];
-            if (FANCY) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
-            s[e] = cap ? capped_plus(s[e] * k, cap_top, lm) : __builtin_fmaf(s[e], k, lm);
+            if (SCORES != kPlain) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
+            s[e] = SCORES == kWideCap ? capped_wide(s[e] * k, cap.top, cap.rtop) + lm
+                                      : capped ? capped_plus(s[e] * k, cap.top, lm) : __builtin_fmaf(s[e], k, lm);
         };
 #define SPIN_ONE(N, CAP) one(N, row_lane<N>(lv) - from, CAP);
 #define SPIN_ALL(CAP)                                                                     \
     SPIN_ONE(0, CAP) SPIN_ONE(1, CAP) SPIN_ONE(2, CAP) SPIN_ONE(3, CAP) SPIN_ONE(4, CAP) \
     SPIN_ONE(5, CAP) SPIN_ONE(6, CAP) SPIN_ONE(7, CAP) SPIN_ONE(8, CAP) SPIN_ONE(9, CAP) \
     SPIN_ONE(10, CAP) SPIN_ONE(11, CAP) SPIN_ONE(12, CAP) SPIN_ONE(13, CAP) SPIN_ONE(14, CAP) SPIN_ONE(15, CAP)
-        if (capped) {
+        if (near_cap) {
             SPIN_ALL(true)
         } else {
             SPIN_ALL(false)
@@ -1303,20 +1342,20 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     return p;
 }
 
-template <int BITS, int ROWS, bool FANCY>
+template <int BITS, int ROWS, int SCORES>
 hipError_t launch_part(const KvAttnArgs& a, const Part& prefix, const Part& own, hipStream_t s) {
     const unsigned items = static_cast<unsigned>(prefix.tiles * prefix.splits + own.tiles * own.splits);
     const int pt = static_cast<int>(prefix.tiles), ot = static_cast<int>(own.tiles);
     if constexpr (ROWS == kRows) {
         const dim3 grid((items + 7) / 8 * 8 * a.Hkv);
         if (own.waves == 8)
-            hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY, 8>), grid, dim3(512), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
+            hipLaunchKernelGGL((kv_attn_rows16<BITS, SCORES, 8>), grid, dim3(512), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
                                own.chunk);
         else
-            hipLaunchKernelGGL((kv_attn_rows16<BITS, FANCY, 4>), grid, dim3(256), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
+            hipLaunchKernelGGL((kv_attn_rows16<BITS, SCORES, 4>), grid, dim3(256), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
                                own.chunk);
     } else {
-        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, FANCY>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
+        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, SCORES>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
                            prefix.splits, prefix.chunk, ot, own.splits, own.chunk);
     }
     return hipGetLastError();
@@ -1328,8 +1367,9 @@ hipError_t launch_rows(const KvAttnArgs& a, Part prefix, Part own, hipStream_t s
     if (prefix.rows != ROWS) prefix.tiles = 0;
     if (own.rows != ROWS) own.tiles = 0;
     if (prefix.tiles == 0 && own.tiles == 0) return hipSuccess;
-    return a.softcap > 0.0f || a.slopes ? launch_part<BITS, ROWS, true>(a, prefix, own, s)
-                                        : launch_part<BITS, ROWS, false>(a, prefix, own, s);
+    if (a.softcap > kNearCap) return launch_part<BITS, ROWS, kWideCap>(a, prefix, own, s);
+    return a.softcap > 0.0f || a.slopes ? launch_part<BITS, ROWS, kFancy>(a, prefix, own, s)
+                                        : launch_part<BITS, ROWS, kPlain>(a, prefix, own, s);
 }
 
 template <int BITS>
