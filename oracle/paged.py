@@ -113,7 +113,7 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
       z      128 products and their sum, the key's scale, the softmax scale, bias and cap: 132 roundings of at most
              2^-24 of sum |terms|, and the exponentials' own errors, 2^-16 in all at the sizes here
       cap    2^-18 of the capped score (the tanh's argument, exponential, reciprocal and sums, 36 roundings of 2^-24
-             where the score is a quarter of the cap, fewer below); caps up to 64 also 2^-22 of the cap
+             where the score is a quarter of the cap, fewer below); at caps up to 64 2^-22 of the cap instead
       w      half a step, 2^-11 relative; below 2^-14 of the largest half a subnormal step, 2^-25
       O      half a step, 2^-11 relative; below 2^-14 half a subnormal step, 2^-25
     """
@@ -155,7 +155,7 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
                     ez = 132 * 2.0 ** -24 * abs(scale) * (np.abs(kd) @ np.abs(x)) * sc + 2.0 ** -16
                     if softcap:
                         z = softcap * np.tanh(z / softcap)
-                        ez += np.abs(z) * 2.0 ** -18 + (softcap * 2.0 ** -22 if softcap <= 64 else 0.0)
+                        ez += softcap * 2.0 ** -22 if softcap <= 64 else np.abs(z) * 2.0 ** -18
                     if slopes is not None:
                         bias = float(slopes[g]) * np.abs(p - j[seen])
                         z = z - bias
