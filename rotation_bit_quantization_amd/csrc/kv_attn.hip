@@ -170,6 +170,12 @@ __device__ __forceinline__ float capped_wide(float z, float top, float rtop) {
 // a bias.
 enum Scores { kPlain, kFancy, kWideCap };
 
+// A factor of scores within the numbers that keep them finite.  Products are multiples of 2^-48, or zero: ones that this
+// brings down stay past any cap, and further apart than any weight bears.
+__device__ __forceinline__ float held(float factor) {
+    return __builtin_fminf(__builtin_fmaxf(factor, -0x1p100f), 0x1p100f);
+}
+
 // How a score is capped: the factor of a product and its key's scale, the cap in units of 1 / log2(e) (0: none) and its
 // reciprocal.
 struct Cap {
@@ -409,7 +415,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     const float slope = SCORES != kPlain && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
     const bool near_cap = SCORES == kFancy && a.softcap > 0.0f;
     const Cap cap = cap_of<SCORES>(a);
-    const float key_factor = cap.factor * 0x1p24f;
+    const float key_factor = held(cap.factor * 0x1p24f);
 
     // Of the wave's next 32 steps, a lane each and half of a step: where the 16 tokens lie, as the number of the first, ~0
     // if nowhere.
@@ -866,7 +872,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     const float slope = SCORES != kPlain && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
     const bool near_cap = SCORES == kFancy && a.softcap > 0.0f;
     const Cap cap = cap_of<SCORES>(a);
-    const float key_factor = cap.factor;
+    const float key_factor = held(cap.factor);
 
     // What a wave stages of a step: eight tokens' keys, eight tokens' values and eight tokens' scales of both, all of the
     // same 16 tokens, which lie in one page.  The keys are tokens 8 w .. 8 w + 7 of the step, the values those of two

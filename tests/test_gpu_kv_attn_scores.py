@@ -37,3 +37,14 @@ def test_caps_of_every_size(cap, bits, work):
 def test_scores_up_to_and_past_the_cap(cap, times, work):
     rng = np.random.default_rng(int(cap))
     check(rng, [2] if work == 0 else [140], [300], 4, 2, 8, 32, work, softcap=cap, scale=times * cap / 8 * 128 ** -0.5)
+
+
+@pytest.mark.parametrize("work", [0] + WORK)
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("cap,scale", [(1e-20, 0.1), (1e-30, 0.1), (1e-38, -0.1), (1e-45, 0.1), (1e-45, 3e38), (5.0, 3e38),
+                                       (100.0, -3e38), (3e38, 3e38), (0.0, 1e32), (0.0, 3e38), (0.0, -3e38)])
+def test_caps_near_zero_and_scales_near_infinity(cap, scale, bits, work):
+    """Scores of any size: queries of zeros weigh all tokens alike, others are finite."""
+    rng = np.random.default_rng(bits)
+    for loud in (0.0, 1.5):
+        check(rng, [2, 1] if work == 0 else [140, 1], [300, 0], 4, 2, bits, 16, work, softcap=cap, scale=scale, loud=loud)
