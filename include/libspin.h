@@ -449,12 +449,13 @@ spin_status spin_kv_qkv(const void* Q, const void* K, const void* V, spin_dtype 
  *               sequence's pages are not used.
  * These arrays lie on the device; what they hold cannot be checked by the
  * host, and is checked by the kernels: an entry that is no page of the pool
- * (-1, say) has no tokens (nothing is stored there, nothing is seen there), a
- * kv_len above max_pages * page_size counts as that much, below 0 as 0.  With
- * q_start not rising as it should, the rows concerned get wrong values, and
- * nothing is read or written outside the arrays.  A page may stand in several
- * tables (a shared prefix), as long as no two rows of one spin_kv_append call
- * are stored in the same slot.
+ * (-1, say) has no tokens (nothing is stored there, nothing is seen there), and
+ * so have places from max_pages * page_size on: with a kv_len above that, the
+ * sequence's other tokens keep their places.  A kv_len below 0 counts as 0,
+ * above 2^30 as 2^30.  With q_start not rising as it should, the rows concerned
+ * get wrong values, and nothing is read or written outside the arrays.  A page
+ * may stand in several tables (a shared prefix), as long as no two rows of one
+ * spin_kv_append call are stored in the same slot.
  */
 #define SPIN_KV_MIN_PAGE 16
 #define SPIN_KV_MAX_PAGE 1024

@@ -10,7 +10,7 @@ everywhere.  Layouts (this library's reading; the pages fix none):
 
 Sequence b owns query rows q_start[b] .. q_start[b + 1] - 1, its i-th row stands
 at place kv_len[b] - q_len + i of its table, whose place p lies in slot p % page
-of page table[b][p // page].
+of page table[b][p // page]; places past the table have no page.
 """
 
 import numpy as np
@@ -44,11 +44,16 @@ def turn_heads(x, rows=None, interleaved=False, weight=None, eps=0.0):
     return rotate_rows(y, D)
 
 
+def _length(n):
+    """A sequence's length as its tokens' places go by it, past its table or not."""
+    return min(max(int(n), 0), 1 << 30)
+
+
 def _places(q_start, kv_len, T):
     """[(row, sequence, place)] of the rows that belong to a sequence."""
     for b in range(len(kv_len)):
         for t in range(q_start[b], min(q_start[b + 1], T)):
-            yield t, b, int(kv_len[b]) - int(q_start[b + 1]) + t
+            yield t, b, _length(kv_len[b]) - int(q_start[b + 1]) + t
 
 
 def kv_append(q, k, v, cache, table, q_start, kv_len, rope=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
@@ -127,7 +132,7 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
         for b in range(len(kv_len)):
             if rows is not None and not any(t in rows for t in range(q_start[b], q_start[b + 1])):
                 continue
-            kv = min(max(int(kv_len[b]), 0), table.shape[1] * page)
+            kv = min(_length(kv_len[b]), table.shape[1] * page)
             parts = cache_tokens(cache, table[b], h, kv)
             if prefix_len:
                 parts = tuple(np.concatenate([f, p]) for f, p in zip(front, parts))
@@ -136,7 +141,7 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
             for t in range(q_start[b], min(q_start[b + 1], T)):
                 if rows is not None and t not in rows:
                     continue
-                p = prefix_len + kv - int(q_start[b + 1]) + t
+                p = prefix_len + _length(kv_len[b]) - int(q_start[b + 1]) + t
                 seen = there.copy()
                 if causal:
                     seen &= (j <= p) | (j < (bidir_len[b] if bidir_len is not None else 0))

@@ -227,7 +227,7 @@ __device__ __forceinline__ Place find_place(const KvAppendArgs& a, int t, int l)
     const int b = find_sequence16(a.q_start, a.B, t, l);
     if (b < 0) return p;
     p.in_batch = true;
-    const long long pos = static_cast<long long>(a.kv_len[b]) - a.q_start[b + 1] + t;
+    const long long pos = static_cast<long long>(placed(a.kv_len[b])) - a.q_start[b + 1] + t;
     if (pos < 0 || pos >= static_cast<long long>(a.max_pages) << a.page_log2) return p;
     if (a.rope && pos + a.pos0 >= a.rope_len) return p;
     p.pos = pos;

@@ -191,7 +191,7 @@ __device__ __forceinline__ Cap cap_of(const KvAttnArgs& a) {
     return {capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e, capped ? a.softcap * kLog2e : 0.0f, 0.0f};
 }
 
-// Tokens of sequence b in its own pages.
+// Tokens of sequence b that its table has room for.
 __device__ __forceinline__ int context(const KvAttnArgs& a, int b) {
     return min(max(a.kv_len[b], 0), a.max_pages << a.page_log2);
 }
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
 
     int pos = 0, both = 0;                 // the row's position, and the tokens that it sees whatever their order
     if (valid) {
-        pos = a.prefix_len + context(a, b) - a.q_start[b + 1] + t;
+        pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
         if (a.bidir_len) both = a.bidir_len[b];
     }
     // the tokens that any of the rows sees
@@ -532,12 +532,12 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
             asm volatile("" ::: "memory");     // keeps this a branch
             const int rel = pos - j0 - 4 * g;
             const int end = a.causal ? max(rel, both - j0 - 4 * g - 1) : 32;
-            const int off = a.window > 0 ? rel + a.window - 1 : 32;
+            const uint32_t off = a.window > 0 ? static_cast<uint32_t>(rel) + static_cast<uint32_t>(a.window) - 1u : 32u;
             const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = 16 * (e >> 2) + (e & 3);
-                const bool seen = (end >= c) & (static_cast<uint32_t>(off - c) < wide);
+                const bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
                 x[e] = seen ? x[e] : -__builtin_inff();
             }
         }
@@ -760,7 +760,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         if (fits) __syncthreads();
         valid = b >= 0;
         if (valid) {
-            pos = a.prefix_len + context(a, b) - a.q_start[b + 1] + t;
+            pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
             if (a.bidir_len) both = a.bidir_len[b];
         }
     } else {
@@ -792,7 +792,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         t = q0 + i;
         head = h * G + (valid ? r - i * G : 0);
         if (valid) {
-            pos = a.prefix_len + span.tokens - a.q_start[b + 1] + t;
+            pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
             if (a.bidir_len) both = a.bidir_len[b];
         }
     }
@@ -1003,12 +1003,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         // token c of the lane's half (c = 8 i + r): the row's last token in order, and its window, counted from there
         const int rel = pos - j0 - 4 * hf;
         const int end = a.causal ? max(rel, both - j0 - 4 * hf - 1) : 32;
-        const int off = a.window > 0 ? rel + a.window - 1 : 32;
+        const uint32_t off = a.window > 0 ? static_cast<uint32_t>(rel) + static_cast<uint32_t>(a.window) - 1u : 32u;
         const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int c = 8 * (e >> 2) + (e & 3);
-            const bool seen = (end >= c) & (static_cast<uint32_t>(off - c) < wide);
+            const bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
             s[e] = seen ? s[e] : -__builtin_inff();
         }
     };

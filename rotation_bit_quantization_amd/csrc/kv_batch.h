@@ -13,6 +13,10 @@
 
 namespace spin {
 
+// What a sequence's new tokens count their places back from: its length, which may pass its table (tokens there have no
+// page, and the others keep their places), held to numbers that positions behind a prefix fit 32 bits with.
+__device__ __forceinline__ int placed(int kv_len) { return min(max(kv_len, 0), 1 << 30); }
+
 // The sequence of row t, or -1, found by the 16 lanes of a DPP row together (l
 // = 0 .. 15 its lane, all 16 with the same t): a 16-way search, one load deep
 // per factor of 16 in B.

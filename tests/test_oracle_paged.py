@@ -63,3 +63,26 @@ def test_attention_is_softmax(causal):
         z = z.masked_fill(torch.ones(n, n).triu(1).bool(), -np.inf)
     assert np.allclose(got, (z.softmax(-1) @ v).transpose(0, 1).numpy(), atol=1e-12)
     assert (bound > 0).all() and bound.max() < 0.01
+
+
+def test_lengths_past_the_table():
+    """Appended and attended tokens stand at the same places: a table with room for 32 of 34 tokens is one whose third
+    page is none of the pool, and the new tokens that have a page see themselves."""
+    n, H = 4, 1
+    x, q = rng.standard_normal((n, H, 128)).astype(np.float32), rng.standard_normal((n, H, 128))
+    empty = {"K_codes": np.zeros((2, H, 16, 128), np.uint8), "K_scale": np.zeros((2, H, 16), np.float16),
+             "V_codes": np.zeros((2, H, 4, 16, 4, 8), np.uint8), "V_scale": np.zeros((2, H, 16), np.float16)}
+    short, wide = np.array([[0, 1]]), np.array([[0, 1, -1]])
+    a, qa = oracle.kv_append(q, x, x, empty, short, [0, n], [34])
+    b, qb = oracle.kv_append(q, x, x, empty, wide, [0, n], [34])
+    assert all(np.array_equal(a[k], b[k]) for k in a)
+    assert np.array_equal(qa[:2], qb[:2]) and (qa[2:] == 0).all()
+    assert (a["K_scale"][1, 0, 14:] > 0).all() and (a["K_scale"][0] == 0).all() and (a["K_scale"][1, 0, :14] == 0).all()
+    for more in (dict(), dict(window=3), dict(slopes=np.array([0.3], np.float32)), dict(bidir_len=[5])):
+        u, _ = oracle.kv_attend(q, a, short, [0, n], [34], 0.1, **more)
+        v, _ = oracle.kv_attend(q, a, wide, [0, n], [34], 0.1, **more)
+        assert np.array_equal(u, v)
+    # of a window of one token each row sees the value that it appended itself, the last two nothing
+    u, _ = oracle.kv_attend(q, a, short, [0, n], [34], 0.1, window=1)
+    codes, scale, _ = oracle.kv_quant8(x, False)
+    assert np.allclose(u[:2], (codes * scale[..., None].astype(np.float64))[:2]) and (u[2:] == 0).all()
