@@ -2,9 +2,11 @@
 
 Every function here checks tensor dtype / device / contiguity, allocates the
 outputs it was not given (torch device memory), and calls the C entry point
-of the same name on torch's current HIP stream.  All arithmetic happens in the
-HIP kernels of libspin.so; if the library is missing this module raises
-instead of computing anything itself.
+of the same name on torch's current HIP stream, or on ``stream`` (a torch
+stream, or a handle): what the call makes then belongs to that stream, and the
+caller orders the stream behind the work on the arguments, and its own work
+behind the stream.  All arithmetic happens in the HIP kernels of libspin.so; if
+the library is missing this module raises instead of computing anything itself.
 
 Declarations and contracts: include/libspin.h.
 """
@@ -111,7 +113,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _cur_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _stream(stream):
+def _stream(stream=None):
     """The hipStream_t to launch on, as an integer: torch's current stream on the
     current device unless one is given."""
     if stream is None:
@@ -121,6 +123,28 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on_stream(stream, of, call, *args, **kw):
+    """call(*args, **kw) with ``stream`` (a torch stream, or a handle) as torch's current one, on the GPU that ``of`` lives
+    on.  Tensors made for the call then come from memory of that stream: memory of the stream that was current may
+    still be in use by work queued there, which nothing orders ``stream`` behind.  Those that the call returns are kept
+    from reuse until what the caller's stream has queued on them is done."""
+    if not (isinstance(of, torch.Tensor) and of.is_cuda):
+        return call(*args, **kw)              # raises, and names what is wrong
+    dev = of.get_device()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device.index != dev:
+        raise ValueError(f"{call.__name__}: a stream of {stream.device} for tensors on GPU {dev}")
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        res = call(*args, **kw)
+    given = {id(t) for a in (*args, *kw.values()) for t in (a.values() if isinstance(a, dict) else (a,))}
+    for t in res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else (res,):
+        if isinstance(t, torch.Tensor) and id(t) not in given:
+            t.record_stream(here)
+    return res
 
 
 def _ptr(t):
@@ -156,6 +180,8 @@ def _dtype_code(t):
 
 def spin_fold_rotation(W, R, r_block, W_rot=None, Wq=None, w_scale=None, stream=None):
     """W [K, N] fp32, R [r, r] fp32 or None -> (W_rot [K, N] fp32, Wq [N, K/2] u8, w_scale [N] fp32)."""
+    if stream is not None:
+        return _on_stream(stream, W, spin_fold_rotation, W, R, r_block, W_rot, Wq, w_scale)
     _check(W, "W", (torch.float32,))
     K, N = W.shape
     if R is not None:
@@ -168,13 +194,15 @@ def spin_fold_rotation(W, R, r_block, W_rot=None, Wq=None, w_scale=None, stream=
     _check(Wq, "Wq", (torch.uint8,), (N, K // 2))
     _check(w_scale, "w_scale", (torch.float32,), (N,))
     st = load().spin_fold_rotation(_ptr(W), K, N, _ptr(R), int(r_block), _ptr(W_rot), _ptr(Wq),
-                                   _ptr(w_scale), _stream(stream))
+                                   _ptr(w_scale), _stream())
     _raise("spin_fold_rotation", st)
     return W_rot, Wq, w_scale
 
 
 def spin_fwht_quant(X, had_n, Xq=None, x_scale=None, X_rot=None, want_rot=False, stream=None):
     """X [M, K] fp16/fp32 -> (Xq [M, K/2] u8, x_scale [M] fp32, X_rot [M, K] fp32 or None)."""
+    if stream is not None:
+        return _on_stream(stream, X, spin_fwht_quant, X, had_n, Xq, x_scale, X_rot, want_rot)
     _check(X, "X", (torch.float16, torch.float32))
     M, K = X.shape
     dev = X.device
@@ -187,7 +215,7 @@ def spin_fwht_quant(X, had_n, Xq=None, x_scale=None, X_rot=None, want_rot=False,
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (M, K))
     st = load().spin_fwht_quant(_ptr(X), _dtype_code(X), M, K, int(had_n), _ptr(Xq), _ptr(x_scale),
-                                _ptr(X_rot), _stream(stream))
+                                _ptr(X_rot), _stream())
     _raise("spin_fwht_quant", st)
     return Xq, x_scale, X_rot
 
@@ -198,6 +226,8 @@ def spin_w4a4_gemm(Xq, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=Fals
 
     ``kernel`` (SPIN_GEMM_INT8 / SPIN_GEMM_FP6 / SPIN_GEMM_FP6_SPLITK) names the kernel family through
     spin_w4a4_gemm_ex; None leaves the choice to the library."""
+    if stream is not None:
+        return _on_stream(stream, Xq, spin_w4a4_gemm, Xq, x_scale, Wq, w_scale, Y, acc_out, want_acc, kernel)
     _check(Xq, "Xq", (torch.uint8,))
     _check(Wq, "Wq", (torch.uint8,))
     M, Kh = Xq.shape
@@ -215,11 +245,11 @@ def spin_w4a4_gemm(Xq, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=Fals
         _check(acc_out, "acc_out", (torch.int32,), (M, N))
     if kernel is None:
         st = load().spin_w4a4_gemm(_ptr(Xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, 2 * Kh,
-                                   _ptr(Y), _ptr(acc_out), _stream(stream))
+                                   _ptr(Y), _ptr(acc_out), _stream())
         _raise("spin_w4a4_gemm", st)
     else:
         st = load().spin_w4a4_gemm_ex(_ptr(Xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, 2 * Kh,
-                                      _ptr(Y), _ptr(acc_out), int(kernel), _stream(stream))
+                                      _ptr(Y), _ptr(acc_out), int(kernel), _stream())
         _raise("spin_w4a4_gemm_ex", st)
     return Y, acc_out
 
@@ -233,6 +263,8 @@ def spin_fwht_quant_f6(X, Xf6=None, x_sum=None, x_scale=None, stream=None, had_n
     """X [M, K] -> (Xf6 uint8 [f6_bytes(M, K)], x_sum [M] int32, x_scale [M] fp32).
 
     had_n = 12288: X fp16 [M, 12288], the R4 Hadamard first; had_n = 1: X fp16 / fp32, quantized as given."""
+    if stream is not None:
+        return _on_stream(stream, X, spin_fwht_quant_f6, X, Xf6, x_sum, x_scale, had_n=had_n)
     _check(X, "X", (torch.float16,) if had_n == 12288 else (torch.float16, torch.float32))
     M, K = X.shape
     dev = X.device
@@ -243,7 +275,7 @@ def spin_fwht_quant_f6(X, Xf6=None, x_sum=None, x_scale=None, stream=None, had_n
     _check(x_sum, "x_sum", (torch.int32,), (M,))
     _check(x_scale, "x_scale", (torch.float32,), (M,))
     st = load().spin_fwht_quant_f6(_ptr(X), _dtype_code(X), M, K, int(had_n), _ptr(Xf6), _ptr(x_sum),
-                                   _ptr(x_scale), _stream(stream))
+                                   _ptr(x_scale), _stream())
     _raise("spin_fwht_quant_f6", st)
     return Xf6, x_sum, x_scale
 
@@ -251,6 +283,9 @@ def spin_fwht_quant_f6(X, Xf6=None, x_sum=None, x_scale=None, stream=None, had_n
 def spin_w4a4_gemm_f6(Xf6, x_sum, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=False, stream=None):
     """Activation codes in the FP6 operand layout (+ row sums, scales) x packed Wq [N, K/2]
     -> (Y [M, N] fp32, acc [M, N] int32 or None)."""
+    if stream is not None:
+        return _on_stream(stream, x_sum, spin_w4a4_gemm_f6, Xf6, x_sum, x_scale, Wq, w_scale, Y, acc_out,
+                          want_acc)
     _check(x_sum, "x_sum", (torch.int32,))
     M = x_sum.shape[0]
     _check(Wq, "Wq", (torch.uint8,))
@@ -267,7 +302,7 @@ def spin_w4a4_gemm_f6(Xf6, x_sum, x_scale, Wq, w_scale, Y=None, acc_out=None, wa
     if acc_out is not None:
         _check(acc_out, "acc_out", (torch.int32,), (M, N))
     st = load().spin_w4a4_gemm_f6(_ptr(Xf6), _ptr(x_sum), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, K,
-                                  _ptr(Y), _ptr(acc_out), _stream(stream))
+                                  _ptr(Y), _ptr(acc_out), _stream())
     _raise("spin_w4a4_gemm_f6", st)
     return Y, acc_out
 
@@ -275,6 +310,8 @@ def spin_w4a4_gemm_f6(Xf6, x_sum, x_scale, Wq, w_scale, Y=None, acc_out=None, wa
 def spin_codes_f6(Wq, Wf6=None, w_sum=None, stream=None):
     """Packed codes [N, K/2] (weights, or activations) -> (uint8 [f6_bytes(N, K)], row sums [N] int32):
     the codes in the FP6 operand layout, for spin_w4a4_gemm_f6f6."""
+    if stream is not None:
+        return _on_stream(stream, Wq, spin_codes_f6, Wq, Wf6, w_sum)
     _check(Wq, "Wq", (torch.uint8,))
     N, Kh = Wq.shape
     K = 2 * Kh
@@ -283,7 +320,7 @@ def spin_codes_f6(Wq, Wf6=None, w_sum=None, stream=None):
     w_sum = torch.empty((N,), dtype=torch.int32, device=dev) if w_sum is None else w_sum
     _check(Wf6, "Wf6", (torch.uint8,), (f6_bytes(N, K),))
     _check(w_sum, "w_sum", (torch.int32,), (N,))
-    st = load().spin_codes_f6(_ptr(Wq), N, K, _ptr(Wf6), _ptr(w_sum), _stream(stream))
+    st = load().spin_codes_f6(_ptr(Wq), N, K, _ptr(Wf6), _ptr(w_sum), _stream())
     _raise("spin_codes_f6", st)
     return Wf6, w_sum
 
@@ -292,6 +329,9 @@ def spin_w4a4_gemm_f6f6(Xf6, x_sum, x_scale, Wf6, w_sum, w_scale, K, Y=None, acc
                         stream=None):
     """Both operands in the FP6 operand layout (+ code sums, scales) -> (Y [M, N] fp32, acc [M, N] int32
     or None).  K is the reduction length (the layouts do not carry it)."""
+    if stream is not None:
+        return _on_stream(stream, x_sum, spin_w4a4_gemm_f6f6, Xf6, x_sum, x_scale, Wf6, w_sum, w_scale, K, Y,
+                          acc_out, want_acc)
     _check(x_sum, "x_sum", (torch.int32,))
     _check(w_sum, "w_sum", (torch.int32,))
     M, N = x_sum.shape[0], w_sum.shape[0]
@@ -307,7 +347,7 @@ def spin_w4a4_gemm_f6f6(Xf6, x_sum, x_scale, Wf6, w_sum, w_scale, K, Y=None, acc
     if acc_out is not None:
         _check(acc_out, "acc_out", (torch.int32,), (M, N))
     st = load().spin_w4a4_gemm_f6f6(_ptr(Xf6), _ptr(x_sum), _ptr(x_scale), _ptr(Wf6), _ptr(w_sum), _ptr(w_scale),
-                                    M, N, K, _ptr(Y), _ptr(acc_out), _stream(stream))
+                                    M, N, K, _ptr(Y), _ptr(acc_out), _stream())
     _raise("spin_w4a4_gemm_f6f6", st)
     return Y, acc_out
 
@@ -331,6 +371,9 @@ def spin_fwht_quant_gemm(X, Wq, w_scale, Xq=None, x_scale=None, Y=None, acc_out=
                          workspace=None, stream=None):
     """X [M, 12288] fp16 (R4 = H_12288 applied online) and the folded Wq [N, 6144], w_scale [N]
     -> (Y [M, N] fp32, Xq [M, 6144] u8, x_scale [M] fp32, acc [M, N] int32 or None), one launch."""
+    if stream is not None:
+        return _on_stream(stream, X, spin_fwht_quant_gemm, X, Wq, w_scale, Xq, x_scale, Y, acc_out, want_acc,
+                          workspace)
     _check(X, "X", (torch.float16,))
     _check(Wq, "Wq", (torch.uint8,))
     M, K = X.shape
@@ -351,7 +394,7 @@ def spin_fwht_quant_gemm(X, Wq, w_scale, Xq=None, x_scale=None, Y=None, acc_out=
     ws = fused_workspace(dev) if workspace is None else workspace
     _check(ws, "workspace", (torch.int32,), (SPIN_FWHT_QUANT_GEMM_WORKSPACE_WORDS,))
     st = load().spin_fwht_quant_gemm(_ptr(X), SPIN_F16, M, K, K, _ptr(Wq), _ptr(w_scale), N, _ptr(Xq),
-                                     _ptr(x_scale), _ptr(Y), _ptr(acc_out), _ptr(ws), _stream(stream))
+                                     _ptr(x_scale), _ptr(Y), _ptr(acc_out), _ptr(ws), _stream())
     _raise("spin_fwht_quant_gemm", st)
     return Y, Xq, x_scale, acc_out
 
@@ -382,6 +425,8 @@ def spin_kv_quant(X, rotate, quantize=True, codes=None, scale=None, X_rot=None, 
     ``scale`` is returned as a float16 tensor holding the fp16 bit patterns the
     library writes.
     """
+    if stream is not None:
+        return _on_stream(stream, X, spin_kv_quant, X, rotate, quantize, codes, scale, X_rot, want_rot)
     _check(X, "X", (torch.float16, torch.float32))
     T, H, D = X.shape
     dev = X.device
@@ -395,7 +440,7 @@ def spin_kv_quant(X, rotate, quantize=True, codes=None, scale=None, X_rot=None, 
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (T, H, D))
     st = load().spin_kv_quant(_ptr(X), _dtype_code(X), T, H, D, int(rotate), _ptr(codes),
-                              _ptr(scale), _ptr(X_rot), _stream(stream))
+                              _ptr(scale), _ptr(X_rot), _stream())
     _raise("spin_kv_quant", st)
     return codes, scale, X_rot
 
@@ -404,6 +449,8 @@ def spin_kv_quant(X, rotate, quantize=True, codes=None, scale=None, X_rot=None, 
 
 def spin_fwht_quant8(X, had_n, Xq8=None, x_scale=None, X_rot=None, want_rot=False, stream=None):
     """X [M, K] fp16/fp32 -> (Xq8 [M, K] int8, x_scale [M] fp32, X_rot [M, K] fp32 or None)."""
+    if stream is not None:
+        return _on_stream(stream, X, spin_fwht_quant8, X, had_n, Xq8, x_scale, X_rot, want_rot)
     _check(X, "X", (torch.float16, torch.float32))
     M, K = X.shape
     dev = X.device
@@ -416,13 +463,15 @@ def spin_fwht_quant8(X, had_n, Xq8=None, x_scale=None, X_rot=None, want_rot=Fals
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (M, K))
     st = load().spin_fwht_quant8(_ptr(X), _dtype_code(X), M, K, int(had_n), _ptr(Xq8), _ptr(x_scale),
-                                 _ptr(X_rot), _stream(stream))
+                                 _ptr(X_rot), _stream())
     _raise("spin_fwht_quant8", st)
     return Xq8, x_scale, X_rot
 
 
 def spin_w4a8_gemm(Xq8, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=False, stream=None):
     """Int8 Xq8 [M, K], packed Wq [N, K/2] + scales -> (Y [M, N] fp32, acc [M, N] int32 or None)."""
+    if stream is not None:
+        return _on_stream(stream, Xq8, spin_w4a8_gemm, Xq8, x_scale, Wq, w_scale, Y, acc_out, want_acc)
     _check(Xq8, "Xq8", (torch.int8,))
     _check(Wq, "Wq", (torch.uint8,))
     M, K = Xq8.shape
@@ -439,7 +488,7 @@ def spin_w4a8_gemm(Xq8, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=Fal
     if acc_out is not None:
         _check(acc_out, "acc_out", (torch.int32,), (M, N))
     st = load().spin_w4a8_gemm(_ptr(Xq8), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, K,
-                               _ptr(Y), _ptr(acc_out), _stream(stream))
+                               _ptr(Y), _ptr(acc_out), _stream())
     _raise("spin_w4a8_gemm", st)
     return Y, acc_out
 
@@ -447,6 +496,8 @@ def spin_w4a8_gemm(Xq8, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=Fal
 def spin_kv_quant8(X, rotate, quantize=True, codes=None, scale=None, X_rot=None, want_rot=False,
                    stream=None):
     """X [T, H, 128] fp16/fp32 -> (codes [T, H, 128] int8 | None, scale [T, H] fp16 | None, X_rot | None)."""
+    if stream is not None:
+        return _on_stream(stream, X, spin_kv_quant8, X, rotate, quantize, codes, scale, X_rot, want_rot)
     _check(X, "X", (torch.float16, torch.float32))
     T, H, D = X.shape
     dev = X.device
@@ -460,7 +511,7 @@ def spin_kv_quant8(X, rotate, quantize=True, codes=None, scale=None, X_rot=None,
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (T, H, D))
     st = load().spin_kv_quant8(_ptr(X), _dtype_code(X), T, H, D, int(rotate), _ptr(codes),
-                               _ptr(scale), _ptr(X_rot), _stream(stream))
+                               _ptr(scale), _ptr(X_rot), _stream())
     _raise("spin_kv_quant8", st)
     return codes, scale, X_rot
 
@@ -474,6 +525,8 @@ def spin_kv_qkv(K, V, Q=None, bits=4, want_k_rot=False, out=None, stream=None):
     Codes are [T, Hkv, 64] uint8 at bits=4 and [T, Hkv, 128] int8 at bits=8.  ``out`` may
     hold preallocated tensors under the same names; missing ones are allocated.
     """
+    if stream is not None:
+        return _on_stream(stream, K, spin_kv_qkv, K, V, Q, bits, want_k_rot, out)
     _check(K, "K", (torch.float16, torch.float32))
     T, Hkv, D = K.shape
     _check(V, "V", (K.dtype,), (T, Hkv, D))
@@ -510,32 +563,21 @@ def spin_kv_qkv(K, V, Q=None, bits=4, want_k_rot=False, out=None, stream=None):
         res[name] = t
     st = load().spin_kv_qkv(_ptr(Q), _ptr(K), _ptr(V), _dtype_code(K), T, Hq, Hkv, D, int(bits),
                             _ptr(res["Q_rot"]), _ptr(res["K_codes"]), _ptr(res["K_scale"]),
-                            _ptr(res["K_rot"]), _ptr(res["V_codes"]), _ptr(res["V_scale"]), _stream(stream))
+                            _ptr(res["K_rot"]), _ptr(res["V_codes"]), _ptr(res["V_scale"]), _stream())
     _raise("spin_kv_qkv", st)
     return res
 
 
 # ---------------------------------------------------------------- the paged KV cache
 
-def _launch(fn, dev, made, stream, args):
-    """Call fn(*args, stream) on GPU number `dev`: on its current stream, or on `stream`.  The tensors `made` for
-    this call are kept from reuse until the work on another stream is done."""
+def _launch(fn, dev, args):
+    """Call fn(*args, stream) on GPU number `dev`, on its current stream."""
     call = _entry(fn)
-    if stream is None and _raw_stream is not None and _cur_device is not None and _cur_device() == dev:
+    if _raw_stream is not None and _cur_device is not None and _cur_device() == dev:
         st = call(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            here = torch.cuda.current_stream()
-            if stream is None:
-                stream = here
-            elif not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            if stream.device.index != dev:
-                raise ValueError(f"{fn}: a stream of {stream.device} for tensors on GPU {dev}")
-            st = call(*args, stream.cuda_stream)
-            if st == SPIN_OK and stream != here:
-                for t in made:
-                    t.record_stream(stream)
+            st = call(*args, torch.cuda.current_stream().cuda_stream)
     if st != SPIN_OK:
         raise SpinError(fn, st)
 
@@ -642,18 +684,18 @@ def _rows(x, name, dtype, T, dev):
 
 def spin_rope_table(inv_freq, n_pos, pos0=0, attn_scale=1.0, table=None, stream=None):
     """inv_freq [n] float64 -> table [n_pos, 2 n] fp32: n cosines, then n sines of (pos0 + p) * inv_freq."""
+    if stream is not None:
+        return _on_stream(stream, inv_freq, spin_rope_table, inv_freq, n_pos, pos0, attn_scale, table)
     dev = _gpu(inv_freq, "inv_freq")
     if inv_freq.dim() != 1:
         raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [n]")
     n = inv_freq.shape[0]
     freq = _want(inv_freq, "inv_freq", torch.float64, (n,), dev)
-    made = ()
     if table is None:
         table = torch.empty((n_pos, 2 * n), dtype=torch.float32, device=inv_freq.device)
-        made = (table,)
     out = _want(table, "table", torch.float32, (n_pos, 2 * n), dev)
     if n_pos != 0:                  # an empty tensor has no address to pass
-        _launch("spin_rope_table", dev, made, stream, (freq, n, _int(pos0, "pos0"), n_pos, float(attn_scale), out))
+        _launch("spin_rope_table", dev, (freq, n, _int(pos0, "pos0"), n_pos, float(attn_scale), out))
     return table
 
 
@@ -663,6 +705,9 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     fine) -> Q_out [T, Hq, 128] fp16 (or None); the codes of K and V go into the pages of ``cache``.
 
     ``rope`` is a spin_rope_table of the rotated part of a head; ``q_norm`` and ``k_norm`` are [128] fp32 weights."""
+    if stream is not None:
+        return _on_stream(stream, K, spin_kv_append, Q, K, V, cache, page_table, q_start, kv_len, rope,
+                          interleaved, q_norm, k_norm, eps, pos0, Q_out)
     dev = _gpu(K, "K")
     (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
@@ -674,12 +719,11 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     if hk != Hkv or hv != Hkv:
         raise ValueError(f"K has {hk} and V {hv} heads, the cache {Hkv}")
     q = out = None
-    Hq, q_stride, made = 0, 0, ()
+    Hq, q_stride = 0, 0
     if Q is not None:
         q, Hq, q_stride = _rows(Q, "Q", dtype, T, dev)
         if Q_out is None:
             Q_out = Q.new_empty((T, Hq, 128), dtype=torch.float16)
-            made = (Q_out,)
             out = Q_out.data_ptr()
         else:
             out = _want(Q_out, "Q_out", torch.float16, (T, Hq, 128), dev)
@@ -694,7 +738,7 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
         rope_len, rot_dim = rope.shape
         rows = _want(rope, "rope", torch.float32, rope.shape, dev)
     if T != 0 and B != 0:           # an empty tensor has no address to pass
-        _launch("spin_kv_append", dev, made, stream,
+        _launch("spin_kv_append", dev,
                 (q, k, v, SPIN_F16 if dtype is torch.float16 else SPIN_F32, T, Hq, Hkv, 128, q_stride, k_stride, v_stride, qn,
                  kn, eps, rows, rope_len, rot_dim, _int(interleaved, "interleaved"), _int(pos0, "pos0"), bits, kc, ks, vc, vs, n_pages, page, B, starts,
                  lens, table, max_pages, out))
@@ -711,7 +755,7 @@ def spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len=0):
 
 
 def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O,
-          workspace, stream):
+          workspace):
     dev = _gpu(Q, "Q")
     (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
@@ -726,10 +770,8 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
     if prefix is not None:
         prefix_len = prefix[1]
         front = (_want(prefix[0], "prefix_table", torch.int32, prefix[0].shape, dev) or None, prefix_len)
-    made = ()
     if O is None:
         O = torch.empty_like(Q)
-        made = (O,)
         out = O.data_ptr()
     else:
         out = _want(O, "O", torch.float16, shape, dev)
@@ -743,8 +785,7 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
     elif need:
         workspace = Q.new_empty((need + 1) // 2)
         ws, ws_bytes = workspace.data_ptr(), need
-        made = (*made, workspace)
-    _launch(fn, dev, made, stream,
+    _launch(fn, dev,
             (q, T, Hq, Hkv, 128, bits, kc, ks, vc, vs, n_pages, page, *front, B, starts, lens, table, max_pages,
              0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both, out, ws, ws_bytes))
     return O
@@ -756,16 +797,22 @@ def spin_kv_attn(Q, cache, page_table, q_start, kv_len, scale=None, softcap=0.0,
 
     ``scale`` is 1 / sqrt(128) by default.  ``workspace`` (uint8, spin_kv_attn_workspace bytes) is allocated if
     it is not given."""
+    if stream is not None:
+        return _on_stream(stream, Q, spin_kv_attn, Q, cache, page_table, q_start, kv_len, scale, softcap,
+                          slopes, window, causal, bidir_len, O, workspace)
     return _attn("spin_kv_attn", Q, cache, None, page_table, q_start, kv_len, scale, softcap, slopes, window, causal,
-                 bidir_len, O, workspace, stream)
+                 bidir_len, O, workspace)
 
 
 def spin_kv_attn_shared(Q, cache, prefix_table, prefix_len, page_table, q_start, kv_len, scale=None, softcap=0.0,
                         slopes=None, window=0, causal=True, bidir_len=None, O=None, workspace=None, stream=None):
     """spin_kv_attn where the first ``prefix_len`` tokens of every sequence lie in the pages ``prefix_table``
     names ([ceil(prefix_len / page_size)] int32) and ``page_table`` and ``kv_len`` count what follows."""
+    if stream is not None:
+        return _on_stream(stream, Q, spin_kv_attn_shared, Q, cache, prefix_table, prefix_len, page_table,
+                          q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O, workspace)
     prefix_len = int(prefix_len)
     if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-prefix_len // cache["K_codes"].shape[2]):
         raise ValueError(f"prefix_table has shape {tuple(prefix_table.shape)}, too few pages for {prefix_len} tokens")
     return _attn("spin_kv_attn_shared", Q, cache, (prefix_table, prefix_len), page_table, q_start, kv_len, scale,
-                 softcap, slopes, window, causal, bidir_len, O, workspace, stream)
+                 softcap, slopes, window, causal, bidir_len, O, workspace)
