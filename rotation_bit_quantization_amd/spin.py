@@ -147,6 +147,14 @@ def _on_stream(stream, of, call, *args, **kw):
     return res
 
 
+def _int(x, name):
+    """x as a C int takes it; ctypes would drop the bits above."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} is {x}, beyond 32 bits")
+    return x
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -193,7 +201,7 @@ def spin_fold_rotation(W, R, r_block, W_rot=None, Wq=None, w_scale=None, stream=
     _check(W_rot, "W_rot", (torch.float32,), (K, N))
     _check(Wq, "Wq", (torch.uint8,), (N, K // 2))
     _check(w_scale, "w_scale", (torch.float32,), (N,))
-    st = load().spin_fold_rotation(_ptr(W), K, N, _ptr(R), int(r_block), _ptr(W_rot), _ptr(Wq),
+    st = load().spin_fold_rotation(_ptr(W), K, N, _ptr(R), _int(r_block, "r_block"), _ptr(W_rot), _ptr(Wq),
                                    _ptr(w_scale), _stream())
     _raise("spin_fold_rotation", st)
     return W_rot, Wq, w_scale
@@ -214,7 +222,7 @@ def spin_fwht_quant(X, had_n, Xq=None, x_scale=None, X_rot=None, want_rot=False,
     _check(x_scale, "x_scale", (torch.float32,), (M,))
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (M, K))
-    st = load().spin_fwht_quant(_ptr(X), _dtype_code(X), M, K, int(had_n), _ptr(Xq), _ptr(x_scale),
+    st = load().spin_fwht_quant(_ptr(X), _dtype_code(X), M, K, _int(had_n, "had_n"), _ptr(Xq), _ptr(x_scale),
                                 _ptr(X_rot), _stream())
     _raise("spin_fwht_quant", st)
     return Xq, x_scale, X_rot
@@ -249,7 +257,7 @@ def spin_w4a4_gemm(Xq, x_scale, Wq, w_scale, Y=None, acc_out=None, want_acc=Fals
         _raise("spin_w4a4_gemm", st)
     else:
         st = load().spin_w4a4_gemm_ex(_ptr(Xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, 2 * Kh,
-                                      _ptr(Y), _ptr(acc_out), int(kernel), _stream())
+                                      _ptr(Y), _ptr(acc_out), _int(kernel, "kernel"), _stream())
         _raise("spin_w4a4_gemm_ex", st)
     return Y, acc_out
 
@@ -274,7 +282,7 @@ def spin_fwht_quant_f6(X, Xf6=None, x_sum=None, x_scale=None, stream=None, had_n
     _check(Xf6, "Xf6", (torch.uint8,), (f6_bytes(M, K),))
     _check(x_sum, "x_sum", (torch.int32,), (M,))
     _check(x_scale, "x_scale", (torch.float32,), (M,))
-    st = load().spin_fwht_quant_f6(_ptr(X), _dtype_code(X), M, K, int(had_n), _ptr(Xf6), _ptr(x_sum),
+    st = load().spin_fwht_quant_f6(_ptr(X), _dtype_code(X), M, K, _int(had_n, "had_n"), _ptr(Xf6), _ptr(x_sum),
                                    _ptr(x_scale), _stream())
     _raise("spin_fwht_quant_f6", st)
     return Xf6, x_sum, x_scale
@@ -347,7 +355,7 @@ def spin_w4a4_gemm_f6f6(Xf6, x_sum, x_scale, Wf6, w_sum, w_scale, K, Y=None, acc
     if acc_out is not None:
         _check(acc_out, "acc_out", (torch.int32,), (M, N))
     st = load().spin_w4a4_gemm_f6f6(_ptr(Xf6), _ptr(x_sum), _ptr(x_scale), _ptr(Wf6), _ptr(w_sum), _ptr(w_scale),
-                                    M, N, K, _ptr(Y), _ptr(acc_out), _stream())
+                                    M, N, _int(K, "K"), _ptr(Y), _ptr(acc_out), _stream())
     _raise("spin_w4a4_gemm_f6f6", st)
     return Y, acc_out
 
@@ -439,7 +447,7 @@ def spin_kv_quant(X, rotate, quantize=True, codes=None, scale=None, X_rot=None, 
         X_rot = torch.empty((T, H, D), dtype=torch.float32, device=dev)
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (T, H, D))
-    st = load().spin_kv_quant(_ptr(X), _dtype_code(X), T, H, D, int(rotate), _ptr(codes),
+    st = load().spin_kv_quant(_ptr(X), _dtype_code(X), T, H, D, _int(rotate, "rotate"), _ptr(codes),
                               _ptr(scale), _ptr(X_rot), _stream())
     _raise("spin_kv_quant", st)
     return codes, scale, X_rot
@@ -462,7 +470,7 @@ def spin_fwht_quant8(X, had_n, Xq8=None, x_scale=None, X_rot=None, want_rot=Fals
     _check(x_scale, "x_scale", (torch.float32,), (M,))
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (M, K))
-    st = load().spin_fwht_quant8(_ptr(X), _dtype_code(X), M, K, int(had_n), _ptr(Xq8), _ptr(x_scale),
+    st = load().spin_fwht_quant8(_ptr(X), _dtype_code(X), M, K, _int(had_n, "had_n"), _ptr(Xq8), _ptr(x_scale),
                                  _ptr(X_rot), _stream())
     _raise("spin_fwht_quant8", st)
     return Xq8, x_scale, X_rot
@@ -510,7 +518,7 @@ def spin_kv_quant8(X, rotate, quantize=True, codes=None, scale=None, X_rot=None,
         X_rot = torch.empty((T, H, D), dtype=torch.float32, device=dev)
     if X_rot is not None:
         _check(X_rot, "X_rot", (torch.float32,), (T, H, D))
-    st = load().spin_kv_quant8(_ptr(X), _dtype_code(X), T, H, D, int(rotate), _ptr(codes),
+    st = load().spin_kv_quant8(_ptr(X), _dtype_code(X), T, H, D, _int(rotate, "rotate"), _ptr(codes),
                                _ptr(scale), _ptr(X_rot), _stream())
     _raise("spin_kv_quant8", st)
     return codes, scale, X_rot
@@ -595,14 +603,6 @@ def _want(t, name, dtype, shape, dev):
     raise ValueError(f"{name} lives on {t.device}, the others on GPU {dev}")
 
 
-def _int(x, name):
-    """x as a C int takes it; ctypes would drop the bits above."""
-    x = int(x)
-    if not -2 ** 31 <= x < 2 ** 31:
-        raise ValueError(f"{name} is {x}, beyond 32 bits")
-    return x
-
-
 def _gpu(t, name):
     """The number of the GPU a tensor lives on."""
     if not isinstance(t, torch.Tensor):
@@ -655,11 +655,13 @@ def _batch(page_table, q_start, kv_len, dev):
     B, max_pages = page_table.shape
     i32 = torch.int32
     if not (q_start.dtype is i32 and kv_len.dtype is i32 and page_table.dtype is i32 and q_start.shape == (B + 1,) and
-            kv_len.shape == (B,) and q_start.get_device() == dev and kv_len.get_device() == dev and
+            kv_len.shape == (B,) and B | max_pages < 2 ** 31 and q_start.get_device() == dev and kv_len.get_device() == dev and
             page_table.get_device() == dev and q_start.is_contiguous() and kv_len.is_contiguous() and page_table.is_contiguous()):
         _want(q_start, "q_start", i32, (B + 1,), dev)
         _want(kv_len, "kv_len", i32, (B,), dev)
         _want(page_table, "page_table", i32, (B, max_pages), dev)
+        _int(B, "B")
+        _int(max_pages, "max_pages")
     return (q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr()), B, max_pages
 
 
@@ -689,7 +691,7 @@ def spin_rope_table(inv_freq, n_pos, pos0=0, attn_scale=1.0, table=None, stream=
     dev = _gpu(inv_freq, "inv_freq")
     if inv_freq.dim() != 1:
         raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [n]")
-    n = inv_freq.shape[0]
+    n, n_pos = _int(inv_freq.shape[0], "n"), _int(n_pos, "n_pos")
     freq = _want(inv_freq, "inv_freq", torch.float64, (n,), dev)
     if table is None:
         table = torch.empty((n_pos, 2 * n), dtype=torch.float32, device=inv_freq.device)
@@ -735,7 +737,7 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError(f"rope has shape {tuple(rope.shape)}, expected [positions, rotated values]")
-        rope_len, rot_dim = rope.shape
+        rope_len, rot_dim = _int(rope.shape[0], "positions"), _int(rope.shape[1], "rotated values")
         rows = _want(rope, "rope", torch.float32, rope.shape, dev)
     if T != 0 and B != 0:           # an empty tensor has no address to pass
         _launch("spin_kv_append", dev,
@@ -748,6 +750,8 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
 @functools.lru_cache(4096)
 def spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len=0):
     """Bytes of workspace that spin_kv_attn (spin_kv_attn_shared with a prefix) takes at these sizes."""
+    for name, x in dict(T=T, Hq=Hq, Hkv=Hkv, B=B, max_pages=max_pages, page_size=page_size, prefix_len=prefix_len).items():
+        _int(x, name)
     n = ctypes.c_size_t(0)
     _raise("spin_kv_attn_workspace", load().spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len,
                                                                    ctypes.byref(n)))
@@ -811,7 +815,7 @@ def spin_kv_attn_shared(Q, cache, prefix_table, prefix_len, page_table, q_start,
     if stream is not None:
         return _on_stream(stream, Q, spin_kv_attn_shared, Q, cache, prefix_table, prefix_len, page_table,
                           q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O, workspace)
-    prefix_len = int(prefix_len)
+    prefix_len = _int(prefix_len, "prefix_len")
     if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-prefix_len // cache["K_codes"].shape[2]):
         raise ValueError(f"prefix_table has shape {tuple(prefix_table.shape)}, too few pages for {prefix_len} tokens")
     return _attn("spin_kv_attn_shared", Q, cache, (prefix_table, prefix_len), page_table, q_start, kv_len, scale,
