@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     int pos = 0, both = 0;                 // the row's position, and the tokens that it sees whatever their order
     if (valid) {
         pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
-        if (a.bidir_len) both = a.bidir_len[b];
+        if (a.bidir_len) both = max(a.bidir_len[b], 0);    // no token stands below 0: differences of it fit 32 bits
     }
     // the tokens that any of the rows sees
     int lo = 0, hi = span.tokens;
@@ -763,7 +763,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         valid = b >= 0;
         if (valid) {
             pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
-            if (a.bidir_len) both = a.bidir_len[b];
+            if (a.bidir_len) both = max(a.bidir_len[b], 0);    // no token stands below 0: differences of it fit 32 bits
         }
     } else {
         // The longest sequences come first (12 chunks of 7566 tokens on up to 5000: 383 -> 341 us), and of each its last tiles;
@@ -795,7 +795,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         head = h * G + (valid ? r - i * G : 0);
         if (valid) {
             pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
-            if (a.bidir_len) both = a.bidir_len[b];
+            if (a.bidir_len) both = max(a.bidir_len[b], 0);    // no token stands below 0: differences of it fit 32 bits
         }
     }
     // positions of the wave's rows, then of the workgroup's: which tokens any of them sees

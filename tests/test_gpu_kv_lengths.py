@@ -78,3 +78,10 @@ def test_append_then_attention(bits):
     for more in (dict(), dict(window=2), dict(window=1)):
         ref, bound = oracle.kv_attend(host(Q), mirror, table, q_start, kv, 128 ** -0.5, **more)
         close(host(spin.spin_kv_attn(Q, d, *args, **more)).astype(np.float64), ref, bound)
+
+
+@pytest.mark.parametrize("bidir", [-1, -2 ** 31, -2 ** 31 + 40, 2 ** 31 - 1])
+@pytest.mark.parametrize("work,q_len,kv_len", [(0, [5, 2], [64, 37]), (2 ** 25, [140, 9], [150, 70]), (2 ** 28, [140, 9], [150, 70])])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_prefixes_seen_both_ways_of_any_length(bidir, work, q_len, kv_len, prefix):
+    check(np.random.default_rng(6), q_len, kv_len, 4, 2, 4, 16, work, prefix_len=prefix, bidir_len=np.array([bidir, 3], np.int32))
