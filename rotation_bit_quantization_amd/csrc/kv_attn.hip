@@ -8,12 +8,11 @@
 //   o   = sum_j e^(z_j) vs_j b_j / sum_j e^(z_j),   0 where nothing is visible.
 // Codes go into the fp16 matrix cores as the integers they are: exact.  The
 // value scale goes into the exponent,
-//   t_j = z_j log2(e) + log2(vs_j),  M = max t,  w_j = 2^(t_j - M) <= 1,
-//   o   = sum w_j b_j / sum w_j / vs_j,
-// so that the weights that are rounded to fp16 for the second product are at
-// most 1 whatever the scales are (a rounding of half a step, 2^-11 relative, of
-// each weight; weights below 2^-14 lose relative precision, which is 2^-25 of
-// the largest term).  Scores, maxima and sums are float32.
+//   t_j = z_j log2(e) + log2(vs_j),  w_j = 2^(t_j - M),  o = sum w_j b_j / sum w_j / vs_j,
+// M no more than the largest t_j and at most kSlack below it, so that the largest of the weights, which are rounded to
+// fp16 for the second product, lies between 1 and 2^kSlack = 256 whatever the scales are.  The rounding is half a step,
+// 2^-11 relative, of each weight; a weight below 2^-14 is off by up to 2^-25, at most 2^-25 of the largest.  Scores,
+// maxima and sums are float32.
 //
 // Both products are computed transposed: S^T = A Q^T leaves a lane with one
 // query and four tokens of a tile of 16, which is what the second product O^T =
@@ -47,7 +46,8 @@ constexpr int kShort = 2048, kShortest = 512;
 constexpr int kTilesWanted = 256, kTilesLeast = 256;      // tiles of 128 and 256: one a CU
 constexpr int kMostSplits = 256;
 constexpr int kCounted = 256;             // sequences up to which tiles of 16 rows are found by counting
-constexpr float kSlack = 8.0f;            // a row's maximum may lag by this many powers of two
+constexpr float kSlack = 8.0f;            // M may lag a row's maximum by this many powers of two
+static_assert(kSlack <= 12.0f, "weights of 2^kSlack lie well below the largest fp16, 65504");
 constexpr float kLog2e = 1.4426950408889634f;
 // Caps up to this one go by capped_plus, whose error is that of a number of the cap's size, above by capped_wide, which is
 // ten operations longer (8 tokens on 32768, INT8, cap 50: 108 and 111 us; 1723 in chunks, cap 30 and a bias: 160 and 191).
