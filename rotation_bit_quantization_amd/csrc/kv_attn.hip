@@ -708,9 +708,9 @@ __device__ __forceinline__ void part_barrier() {
 // Two waves share a SIMD; a step of 64 tokens and 256 rows holds 2 x 1024
 // cycles of MFMA, and 2 x (2 x 850) of exponents and weights, which overlap across
 // the waves but for the loads and the staging, 400 - 550 cycles.  Measured: a prompt of 8192 tokens, 32 + 8 heads,
-// INT4, 605 - 735 us (0.55 TFLOP, 0.75 - 0.91 PFLOP/s); uneven chunks of 1723
+// INT4, 615 - 634 us a call, 690 - 735 traced (0.55 TFLOP, 0.75 - 0.89 PFLOP/s); uneven chunks of 1723
 // tokens, 32 + 32 heads, INT8, capped and with a distance bias, on up to 2900,
-// 154 - 173 us (32 exponentials and reciprocals a lane and 32 tokens more).
+// 149 - 160 us a call, 172 traced (32 exponentials and reciprocals a lane and 32 tokens more).
 template <int BITS, int ROWS, int SCORES>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                 int own_tiles, int own_splits, int own_chunk) {
