@@ -545,7 +545,8 @@ spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dty
  * at most, at caps up to 64 by 2^-20 of the cap.  Softmax weights are rounded to fp16
  * (relative to the row's largest weighted term) for the product with the codes,
  * which are exact.  A row that sees a token whose scale is not finite is NaN;
- * one that does not is not touched by it.
+ * one that does not is not touched by it.  A row of Q that is not finite gives
+ * NaN or zeros, and the others what they are without it, up to their rounding.
  * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (bits, causal, a scale that is
  * not finite, a softcap that is negative or not finite), SPIN_ERR_BAD_SHAPE
  * (also a workspace that is too small, Hkv above 65535, more than 2^22 - 1

@@ -6,9 +6,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from rotation_bit_quantization_amd import spin
 
-from .paged_case import DEV, dev, host, pool, starts, tables
+from .paged_case import DEV, attend, close, dev, host, pool, starts, tables
 from .test_gpu_kv_attn_tiles import check, widened
 
 pytestmark = pytest.mark.gpu
@@ -97,6 +98,56 @@ def test_captured_calls_of_two_launches(plan):
             g.replay()
             assert np.array_equal(host(O), want), rep
     assert np.array_equal(seen[0], seen[-1]) and not np.array_equal(seen[0], seen[1])
+
+
+@pytest.mark.parametrize("plan", sorted(PLANS))
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_queries_that_are_not_finite(plan, bad):
+    """Such a row is NaN or zero; of its token's others each is within its bound, and those of other tokens are those of the
+    call without it, up to the bounds of both.  Not to the bit: rows of a wave move their maxima together, and a weight's
+    rounding goes by where its row's maximum stands.  Of values up to v a bound is at most twice (2^-11 + e) v, with e
+    below 2^-12 for the exponents here (132 roundings of 2^-24 of sums of 12): 2^-8 v for two."""
+    q_len, kv_len, Hq, Hkv, prefix, work = PLANS[plan]
+    rng = np.random.default_rng(10)
+    page, first, T = 64, -(-prefix // 64), sum(q_len)
+    n = first + sum(-(-k // page) for k in kv_len)
+    cache, q = pool(rng, n, Hkv, page, 4), rng.standard_normal((T, Hq, 128)).astype(np.float16)
+    table = widened(tables(rng, kv_len, page, n, first=first), T * Hq // Hkv, Hkv, page, work)
+    args = (cache, table, starts(q_len), kv_len, np.arange(max(first, 1), dtype=np.int32), prefix)
+    for more in (dict(), dict(softcap=20.0), dict(softcap=1e4, window=50)):
+        want = attend(q, *args, **more)
+        odd = q.copy()
+        rows = [(0, 0), (T - 1, Hq - 1), (T // 2, 1)]
+        tokens = sorted({t for t, _ in rows})
+        ref, bound = oracle.kv_attend(q, cache, table, starts(q_len), kv_len, 128 ** -0.5, prefix_table=args[4],
+                                      prefix_len=prefix, rows=set(tokens), **more)
+        for i, (t, h) in enumerate(rows):
+            odd[t, h, 5 + 40 * i] = bad
+        got = attend(odd, *args, **more)
+        for t, h in rows:
+            assert (np.isnan(got[t, h]) | (got[t, h] == 0)).all()
+            got[t, h] = want[t, h]
+        close(got[tokens], ref[tokens], bound[tokens])
+        assert np.abs(got - want).max() <= 2.0 ** -8 * 7 * float(cache["V_scale"].max())
+
+
+@pytest.mark.parametrize("plan", sorted(PLANS))
+@pytest.mark.parametrize("missing", ["some", "all"])
+def test_pages_of_a_prefix_that_are_not_there(plan, missing):
+    q_len, kv_len, Hq, Hkv, prefix, work = PLANS[plan]
+    rng = np.random.default_rng(11)
+    page, first, T = 64, -(-prefix // 64), sum(q_len)
+    n = first + sum(-(-k // page) for k in kv_len)
+    cache, q = pool(rng, n, Hkv, page, 8), rng.standard_normal((T, Hq, 128)).astype(np.float16)
+    table = widened(tables(rng, kv_len, page, n, first=first), T * Hq // Hkv, Hkv, page, work)
+    front = rng.permutation(first).astype(np.int32)
+    front[rng.random(first) < (0.4 if missing == "some" else 2)] = -1
+    front[0], front[first // 2] = n, -2 ** 31
+    rows = {0, T // 2, T - 1}
+    for more in (dict(), dict(window=prefix + 3)):
+        ref, bound = oracle.kv_attend(q, cache, table, starts(q_len), kv_len, 0.1, prefix_table=front, prefix_len=prefix, rows=rows, **more)
+        got = attend(q, cache, table, starts(q_len), kv_len, front, prefix, scale=0.1, **more)
+        close(got[sorted(rows)], ref[sorted(rows)], bound[sorted(rows)])
 
 
 def borders(kind, B, T):
