@@ -87,3 +87,7 @@ def test_tables_of_positions(seen, shape):  # noqa: F811
     with pytest.raises(ValueError, match="32 bits"):
         spin.spin_kv_append(**dict(calls()["spin_kv_append"], rope=Shaped(shape, torch.float32)))
     assert seen["launched"] == []
+
+
+def test_the_names_that_the_binding_offers():
+    assert [n for n in spin.__all__ if not hasattr(spin, n)] == [] and len(set(spin.__all__)) == len(spin.__all__)
