@@ -12,7 +12,8 @@
 // M no more than the largest t_j and at most kSlack below it, so that the largest of the weights, which are rounded to
 // fp16 for the second product, lies between 1 and 2^kSlack = 256 whatever the scales are.  The rounding is half a step,
 // 2^-11 relative, of each weight; a weight below 2^-14 is off by up to 2^-25, at most 2^-25 of the largest.  Scores,
-// maxima and sums are float32.
+// maxima and sums are float32; exponentials, logarithms and reciprocals are the hardware's, off by a unit in the last
+// place, 2^-23, which the rounding of the weights passes by far.
 //
 // Both products are computed transposed: S^T = A Q^T leaves a lane with one
 // query and four tokens of a tile of 16, which is what the second product O^T =
