@@ -99,9 +99,9 @@ def calls():
         "spin_w4a4_gemm": dict(gemm, Xq=z(32, 32, dtype=u8), Wq=z(64, 32, dtype=u8), want_acc=True),
         "spin_w4a8_gemm": dict(gemm, Xq8=z(32, 64, dtype=i8), Wq=z(64, 32, dtype=u8), want_acc=True),
         "spin_w4a4_gemm_f6": dict(gemm, Xf6=z(1536, dtype=u8), x_sum=z(32, dtype=i32), Wq=z(64, 32, dtype=u8), want_acc=True),
-        "spin_codes_f6": dict(Wq=z(64, 32, dtype=u8)),
-        "spin_w4a4_gemm_f6f6": dict(gemm, Xf6=z(1536, dtype=u8), x_sum=z(32, dtype=i32), Wf6=z(3072, dtype=u8), w_sum=z(64, dtype=i32),
-                                    K=64, want_acc=True),
+        "spin_codes_f6": dict(Wq=z(96, 32, dtype=u8)),
+        "spin_w4a4_gemm_f6f6": dict(Xf6=z(1536, dtype=u8), x_sum=z(32, dtype=i32), x_scale=z(32), Wf6=z(4608, dtype=u8),
+                                    w_sum=z(96, dtype=i32), w_scale=z(96), K=64, want_acc=True),
         "spin_fwht_quant_gemm": dict(X=z(4, 12288, dtype=f16), Wq=z(64, 6144, dtype=u8), w_scale=z(64), want_acc=True),
         "spin_kv_quant": dict(X=z(2, 1, 128), rotate=1, want_rot=True),
         "spin_kv_quant8": dict(X=z(2, 1, 128), rotate=1, want_rot=True),
