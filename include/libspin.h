@@ -541,10 +541,11 @@ spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dty
  *   workspace  device memory of the bytes spin_kv_attn_workspace names (it may
  *        be NULL if that is 0); its content before and after means nothing,
  *        and calls that overlap need one each
- * Scores, maxima and sums are float32; a capped score is off by 2^-18 of itself
- * at most, at caps up to 64 by 2^-20 of the cap.  Softmax weights are rounded to fp16
- * (relative to the row's largest weighted term) for the product with the codes,
- * which are exact.  A row that sees a token whose scale is not finite is NaN;
+ * Scores (with the logarithm of the value's scale added: a score of size z
+ * carries it to 2^-24 z), maxima and sums are float32; a capped score is off by
+ * 2^-18 of itself at most, at caps up to 64 by 2^-20 of the cap.  Softmax
+ * weights are rounded to fp16 (relative to the row's largest weighted term) for
+ * the product with the codes, which are exact.  A row that sees a token whose scale is not finite is NaN;
  * one that does not is not touched by it.  A row of Q that is not finite gives
  * NaN or zeros, and the others what they are without it, up to their rounding.
  * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (bits, causal, a scale that is

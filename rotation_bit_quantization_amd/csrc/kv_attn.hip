@@ -171,9 +171,9 @@ __device__ __forceinline__ float capped_wide(float z, float top, float rtop) {
 // a bias.
 enum Scores { kPlain, kFancy, kWideCap };
 
-// A factor of scores within the numbers that keep them finite.  Products are multiples of 2^-48, or zero: ones that this
-// brings down stay past any cap, and further apart than any weight bears.  In a scalar register: as a vector one it
-// makes kv_attn_tile spill four more (chunks 159 -> 162 us).
+// A factor of scores within the numbers that keep them finite.  Products are multiples of 2^-48, or zero: scores that this
+// brings down still lie past every cap up to kNearCap, or so far apart that their roundings, 2^-24 of them, are past what
+// weights tell apart.  In a scalar register: as a vector one it makes kv_attn_tile spill four more (chunks 159 -> 162 us).
 __device__ __forceinline__ float held(float factor) {
     factor = __builtin_fminf(__builtin_fmaxf(factor, -0x1p100f), 0x1p100f);
     return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(factor)));
