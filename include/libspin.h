@@ -522,6 +522,24 @@ spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dty
                            uint16_t* Q_out, void* stream);
 
 /*
+ * spin_kv_append_at — spin_kv_append where `positions` [T] int32 says which
+ * position each row is turned by (its row of rope), in place of pos0 + place: for
+ * drafted tokens, which stand behind each other in the cache and beside each
+ * other in the tree (spin_kv_tree), and for a cache that tokens have left
+ * (spin_kv_choose), where places lag behind positions.  Places, pages and
+ * everything else as there; a row whose position has no row in rope is one whose
+ * position has none there.
+ * Errors: as for spin_kv_append, SPIN_ERR_NULL without positions.
+ */
+spin_status spin_kv_append_at(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq, int Hkv,
+                              int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_norm,
+                              const float* k_norm, float eps, const float* rope, int rope_len, int rot_dim,
+                              int interleaved, const int32_t* positions, int bits, uint8_t* K_codes,
+                              uint16_t* K_scale, uint8_t* V_codes, uint16_t* V_scale, int n_pages, int page_size, int B,
+                              const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                              uint16_t* Q_out, void* stream);
+
+/*
  * spin_kv_attn — attention of the new tokens of every sequence over its pages
  * (page "SpinQuant, Reproduced", Q5: queries and keys both carry R3, which
  * leaves their products unchanged; the values' R2 is undone in o_proj).
@@ -580,9 +598,138 @@ spin_status spin_kv_attn_shared(const uint16_t* Q, int T, int Hq, int Hkv, int D
                                 int causal, const int32_t* bidir_len, uint16_t* O, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* Words of a row of the tree at most: 4096 drafted tokens of a sequence. */
+#define SPIN_KV_TREE_MAX_WORDS 128
+
+/*
+ * spin_kv_tree — ancestors and positions of drafted tokens (speculative decoding:
+ * several continuations of a sequence, as a tree, are verified in one step).
+ *
+ *   parent     [T] int32: of a sequence's i-th new token the number, among its new
+ *              tokens, of the one before it in its continuation; -1 if that is the
+ *              context's last.  A parent comes before its children; any value that
+ *              is not in 0 .. i - 1 counts as -1.
+ *   tree       [T][words] uint32   OUTPUT: bit i % 32 of word i / 32 of a row is set
+ *              if new token i of its sequence is the row's token or one of its
+ *              ancestors
+ *   positions  [T] int32   OUTPUT: pos0 + the context's tokens (kv_len less the new
+ *              ones) + the token's depth (0 with parent -1)
+ * New tokens of a sequence from 32 words on have rows of zeros and depth 0; nobody
+ * sees them.  Rows of no sequence are not written.
+ * Requirements: 0 <= T <= 2^26, B >= 0, 0 <= pos0 <= SPIN_KV_MAX_CONTEXT,
+ * 1 <= words <= SPIN_KV_TREE_MAX_WORDS.
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE, SPIN_ERR_MISALIGNED.
+ */
+spin_status spin_kv_tree(const int32_t* parent, int T, int B, const int32_t* q_start, const int32_t* kv_len, int pos0,
+                         int words, uint32_t* tree, int32_t* positions, void* stream);
+
+/*
+ * spin_kv_attn_ex — spin_kv_attn_shared (spin_kv_attn at prefix_len 0) with two
+ * more things.
+ *
+ *   tree, tree_words, positions   tree non-NULL: which of its sequence's new tokens
+ *        a row sees ([T][tree_words] uint32 as spin_kv_tree writes them; any bits
+ *        are taken).  It sees the prefix and the context, all tokens before the
+ *        sequence's first new one, as well; a row whose bits are all zero sees
+ *        nothing else.  `causal` is then of no effect, and bidir_len NULL.  Distances,
+ *        of the window and the bias, go by positions [T] int32 for the rows and
+ *        the new tokens (held to 0 .. 2^30), by places (behind the prefix) for the
+ *        context's tokens; positions may be NULL without a window and slopes.
+ *        Bits of new tokens that have no place are of no effect.
+ *   lse  [T][Hq] float32 or NULL   OUTPUT: the natural logarithm of the sum of e^z
+ *        over the tokens that the row sees, -infinity where there is none; not
+ *        finite for a row that sees a scale that is not finite, or is not finite
+ *        itself.  For spin_kv_weights.
+ * tree NULL and lse NULL: the bits of spin_kv_attn_shared.  The workspace is the same.
+ * Errors: as for spin_kv_attn_shared; SPIN_ERR_NULL for a tree without positions
+ * where a window or slopes need them, SPIN_ERR_UNSUPPORTED for a tree with
+ * bidir_len, SPIN_ERR_BAD_SHAPE for tree_words outside 1 .. SPIN_KV_TREE_MAX_WORDS.
+ */
+spin_status spin_kv_attn_ex(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                            const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale, int n_pages,
+                            int page_size, const int32_t* prefix_table, int prefix_len, int B, const int32_t* q_start,
+                            const int32_t* kv_len, const int32_t* page_table, int max_pages, float scale,
+                            float softcap, const float* slopes, int window, int causal, const int32_t* bidir_len,
+                            const uint32_t* tree, int tree_words, const int32_t* positions, uint16_t* O, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spin_kv_weights — the attention weight that every cached token of a sequence
+ * draws, for eviction from the cache.
+ *
+ *   Q, lse   [T][Hq][D] fp16 and [T][Hq] float32: queries, and the logarithms that
+ *            spin_kv_attn_ex left for them (with the same scale, softcap, slopes,
+ *            window, causal and bidir_len)
+ *   pos0     position of the first token of the tables: 0, or the length of a prefix
+ *            in other pages
+ *   prior    [n_pages][Hkv][page_size] float32 or NULL; W itself is allowed
+ *   W        [n_pages][Hkv][page_size] float32   OUTPUT: at the slot of every token
+ *            j < kv_len[b] of every sequence, per key head
+ *              W_j = decay * prior_j + sum over rows and heads of e^(z_j - lse)
+ *            over the sequence's rows and the query heads of the key head that see
+ *            the token (without prior, the sum alone).  Other slots keep what they
+ *            hold.
+ * A row whose lse is not finite adds nothing, and a token whose scale is not finite
+ * draws nothing.  Sums are float32, in an order that goes by the sizes alone.  A page
+ * may stand in one table of the batch only.  T == 0 is valid: W = decay * prior.
+ * Errors: as for spin_kv_attn (no workspace); SPIN_ERR_UNSUPPORTED for a decay that
+ * is not finite, SPIN_ERR_BAD_SHAPE for more than 2^24 - 1 workgroups of 256
+ * of a head's tokens.
+ */
+spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
+                            const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
+                            const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                            int pos0, float scale, float softcap, const float* slopes, int window, int causal,
+                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* stream);
+
+/*
+ * spin_kv_choose — which tokens of each sequence stay, per key head: those of
+ * greatest weight.
+ *
+ *   W      [n_pages][Hkv][page_size] float32 (from spin_kv_weights)
+ *   keep   how many stay of a longer sequence, 1 or more; its first `first` and its last
+ *          `recent` tokens are always among them (first + recent <= keep)
+ *   kept   [B][Hkv][keep] int32   OUTPUT: their places, ascending, -1 behind the
+ *          places of a sequence that has no more than keep tokens (all stay)
+ *   lens   [B] int32   OUTPUT: how many stay, min(kv_len[b], keep)
+ * Of equal weights the lowest place stays (-0 equals 0).  NaN, and a token
+ * that lies in no page of the pool, are below all weights.
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE (also more than 2^22 - 1 sequences times
+ * heads), SPIN_ERR_MISALIGNED.
+ */
+spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, int B, const int32_t* kv_len,
+                           const int32_t* page_table, int max_pages, int keep, int first, int recent, int32_t* kept,
+                           int32_t* lens, void* stream);
+
+/*
+ * spin_kv_move — tokens of the cache to other slots, codes and scales as they are.
+ *
+ *   kept   [B][kept_heads][n] int32, kept_heads 1 (all heads alike) or Hkv: the token
+ *          at place at[b] + kept[b][h][i] goes to place at[b] + i; entries below 0
+ *          are passed over.  at [B] int32, NULL for 0.
+ *   to_table   [B][to_pages] int32: the pages that it goes to, none of which may be
+ *          one that tokens of this call come from.  NULL: places of page_table itself,
+ *          in which case a list ascends, so that kept[b][h][i] >= i: the tokens that
+ *          spin_kv_choose names, or the accepted path of a tree behind at[b] tokens
+ *          of context.  (With other lists the slots hold wrong tokens.)
+ *   W      [n_pages][Hkv][page_size] float32 or NULL: moves with the tokens
+ * A token that comes from or goes to a place beyond its table, or a page that is
+ * none of the pool, is passed over.  Slots that nothing goes to keep what they hold.
+ * Position rotations are in the keys, so that a token keeps its position wherever it
+ * lies; what attention takes from places (windows, distances, causal order among new
+ * tokens) goes by the new ones.
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (bits), SPIN_ERR_BAD_SHAPE (also more
+ * than 2^24 - 1 groups of 64 tokens of a head), SPIN_ERR_MISALIGNED (16 bytes; 4
+ * for page_table, kept, at and to_table, which are cut out of longer lists).
+ */
+spin_status spin_kv_move(uint8_t* K_codes, uint16_t* K_scale, uint8_t* V_codes, uint16_t* V_scale, float* W, int Hkv,
+                         int D, int bits, int n_pages, int page_size, int B, const int32_t* page_table, int max_pages,
+                         const int32_t* kept, int kept_heads, int n, const int32_t* at, const int32_t* to_table,
+                         int to_pages, void* stream);
+
 /*
  * spin_kv_attn_workspace — bytes of workspace a spin_kv_attn (prefix_len 0) or
- * spin_kv_attn_shared call of these sizes takes.  It goes by the sizes alone,
+ * spin_kv_attn_shared (or spin_kv_attn_ex) call of these sizes takes.  It goes by the sizes alone,
  * not by what the arrays on the device hold.
  */
 spin_status spin_kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, int prefix_len,

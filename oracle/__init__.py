@@ -25,7 +25,7 @@ Modules
   fold      W' = B^T W (B block-diagonal rotation) + per-output-channel INT4
   gemm      int64 GEMM on INT4 codes (C) + float32 dequant epilogue
   kv        head-wise Hadamard + per-(token, head) INT4 for the KV path
-  paged     position rotation, append into and attention over a paged KV cache
+  paged     position rotation, append into and attention over a paged KV cache; drafted trees, eviction
   stats     kurtosis and orthogonality error
   cayley    Cayley update of an orthogonal matrix (rotation learning, offline)
 
@@ -39,7 +39,8 @@ from .quant import (quantize_rows, quantize_kv_groups, pack_int4, unpack_int4,  
 from .fold import fold_rotation, block_rotation  # noqa: F401
 from .gemm import gemm_int_codes, gemm_int_codes_blas, dequant, w4a4_gemm, w4a8_gemm, gemm_rows  # noqa: F401
 from .kv import kv_quant, kv_quant8  # noqa: F401
-from .paged import rope_table, turn_heads, kv_append, kv_attend  # noqa: F401
+from .paged import (rope_table, turn_heads, kv_append, kv_attend, kv_tree, kv_weights, kv_choose,  # noqa: F401
+                    kv_move)  # noqa: F401
 from .stats import kurtosis_per_token, mean_kurtosis, orthogonality_error  # noqa: F401
 from .fwht_quant import fwht_quant, fwht_quant8  # noqa: F401
 from .cayley import skew_descent, cayley_step  # noqa: F401

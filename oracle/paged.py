@@ -18,7 +18,7 @@ import numpy as np
 from .hadamard import rotate_rows
 from .quant import pack_int4, quantize_kv_groups, unpack_int4
 
-__all__ = ["rope_table", "turn_heads", "kv_append", "kv_attend", "cache_tokens"]
+__all__ = ["rope_table", "turn_heads", "kv_append", "kv_attend", "cache_tokens", "kv_tree", "kv_weights", "kv_choose", "kv_move"]
 
 D = 128
 
@@ -57,18 +57,20 @@ def _places(q_start, kv_len, T):
 
 
 def kv_append(q, k, v, cache, table, q_start, kv_len, rope=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
-              pos0=0):
-    """The cache (a dict of numpy arrays, a changed copy) and the queries in float64 (NaN rows: not written)."""
+              pos0=0, positions=None):
+    """The cache (a dict of numpy arrays, a changed copy) and the queries in float64 (NaN rows: not written).
+    ``positions`` [T]: what rows are turned by, in place of pos0 + place."""
     cache = {name: a.copy() for name, a in cache.items()}
     pages, H, page, width = cache["K_codes"].shape
     bits = width // 16
     T = k.shape[0]
     q_out = np.full(q.shape, np.nan)
     for t, b, p in _places(q_start, kv_len, T):
-        if p < 0 or p >= table.shape[1] * page or (rope is not None and p + pos0 >= len(rope)):
+        turn = p + pos0 if positions is None else int(positions[t])
+        if p < 0 or p >= table.shape[1] * page or (rope is not None and not 0 <= turn < len(rope)):
             q_out[t] = 0.0
             continue
-        row = None if rope is None else rope[p + pos0][None]
+        row = None if rope is None else rope[turn][None]
         q_out[t] = turn_heads(q[t:t + 1], row, interleaved, q_norm, eps)[0]
         at = table[b, p // page]
         if at < 0 or at >= pages:
@@ -108,9 +110,13 @@ def cache_tokens(cache, pages, h, n):
 
 
 def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None, window=0, causal=True, bidir_len=None,
-              prefix_table=None, prefix_len=0, rows=None):
+              prefix_table=None, prefix_len=0, rows=None, tree=None, positions=None, sums=False):
     """(O [T, Hq, 128] float64, NaN rows where nothing is written, bound [T, Hq, 128]).  ``rows``: those of T to
     compute, all by default; what is returned for others means nothing.
+
+    ``tree`` [T, words] uint32: rows see the context and, of their sequence's new tokens, those whose bits are set;
+    distances of new tokens go by ``positions`` [T].  With ``sums`` also (log sum e^z [T, Hq], bound): errors of the
+    scores, weighted, a rounding of the sum for every token and 2^-22 of the logarithm.
 
     ``bound`` is how far a result may be that holds scores in float32, rounds softmax weights (times the value's
     scale, relative to the row's largest) to fp16 and the result to fp16:
@@ -126,6 +132,7 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
     n_pages, H, page, _ = cache["K_codes"].shape
     G = Hq // H
     out, bound = np.full(q.shape, np.nan), np.zeros(q.shape)
+    logs, log_bound = np.full((T, Hq), np.nan), np.zeros((T, Hq))
     for h in range(H):
         if prefix_len:
             front = cache_tokens(cache, prefix_table, h, prefix_len)
@@ -142,15 +149,18 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
                 if rows is not None and t not in rows:
                     continue
                 p = prefix_len + _length(kv_len[b]) - int(q_start[b + 1]) + t
-                seen = there.copy()
-                if causal:
+                seen, at = there.copy(), j
+                if tree is not None:
+                    names, at, p = _tree_row(tree, positions, t, q_start, b, prefix_len + _length(kv_len[b]), j)
+                    seen &= names
+                elif causal:
                     seen &= (j <= p) | (j < (bidir_len[b] if bidir_len is not None else 0))
                 if window:
-                    seen &= np.abs(p - j) < window
+                    seen &= np.abs(p - at) < window
                 for g in range(h * G, (h + 1) * G):
                     x = q[t, g].astype(np.float64)
                     if not seen.any():
-                        out[t, g] = 0.0
+                        out[t, g], logs[t, g] = 0.0, -np.inf
                         continue
                     if not (np.isfinite(ks[seen]).all() and np.isfinite(vs[seen]).all()):
                         out[t, g] = np.inf     # stands for "has to be NaN"
@@ -162,11 +172,13 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
                         z = softcap * np.tanh(z / softcap)
                         ez += softcap * 2.0 ** -22 if softcap <= 64 else np.abs(z) * 2.0 ** -18
                     if slopes is not None:
-                        bias = float(slopes[g]) * np.abs(p - j[seen])
+                        bias = float(slopes[g]) * np.abs(p - at[seen])
                         z = z - bias
                         ez += np.abs(bias) * 2.0 ** -22
                     w = np.exp(z - z.max())
                     l = w.sum()
+                    logs[t, g] = z.max() + np.log(l)
+                    log_bound[t, g] = (w * ez).sum() / l + 2.0 ** -24 * len(z) + 2.0 ** -22 * (abs(logs[t, g]) + 24)
                     v = vd * vsc[:, None]
                     o = (w @ v) / l
                     spread = ((w * (2.0 ** -11 + ez)) @ np.abs(v)) / l
@@ -174,4 +186,136 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
                     tiny = 2.0 ** -25 * top * np.abs(vd).sum(axis=0) / l
                     out[t, g] = o
                     bound[t, g] = spread + tiny + np.abs(o) * (2.0 ** -11 + (w * ez).sum() / l) + 2.0 ** -25
-    return out, bound
+    return (out, bound, logs, log_bound) if sums else (out, bound)
+
+
+def _tree_row(tree, positions, t, q_start, b, end, j):
+    """Which of the tokens j of sequence b, which ends at ``end``, row t names, their positions and its own."""
+    news = int(q_start[b + 1]) - int(q_start[b])
+    i = j - (end - news)
+    bits = np.unpackbits(np.ascontiguousarray(tree[t]).view(np.uint8), bitorder="little").astype(bool)
+    names = i < 0
+    inside = (i >= 0) & (i < min(len(bits), news))
+    names[inside] = bits[i[inside]]
+    if positions is None:
+        return names, j, 0
+    at = np.array(j)
+    fresh = (i >= 0) & (i < news)
+    at[fresh] = positions[int(q_start[b]) + i[fresh]]
+    return names, at, int(positions[t])
+
+
+def kv_tree(parent, q_start, kv_len, words, pos0=0):
+    """(tree [T, words] uint32, positions [T]) of drafted tokens, by walking up from each."""
+    tree, positions = np.zeros((len(parent), words), np.uint32), np.zeros(len(parent), np.int32)
+    for b in range(len(kv_len)):
+        lo, hi = int(q_start[b]), int(q_start[b + 1])
+        for t in range(lo, hi):
+            i, depth = t - lo, -1
+            while i >= 0 and t - lo < 32 * words:
+                tree[t, i // 32] |= np.uint32(1 << (i % 32))
+                p = int(parent[lo + i])
+                i, depth = p if p < i else -1, depth + 1
+            positions[t] = pos0 + _length(kv_len[b]) - (hi - lo) + max(depth, 0)
+    return tree, positions
+
+
+def kv_weights(q, lse, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None, window=0, causal=True, bidir_len=None,
+               pos0=0, prior=None, decay=1.0):
+    """(W [n_pages, Hkv, page] float64, NaN where nothing is written, bound): decay * prior + the attention weight that
+    each token draws.
+
+    A weight is off by the score's error (128 products of the query with codes and their sum, its scale, bias and
+    cap: 132 roundings of 2^-24 of the terms; the cap as in ``kv_attend``), that of
+    the difference to lse in units of log2 (2^-22 of both) and the exponential's 2^-22 (numbers below 2^-126 may be 0); the sum by a rounding of itself for
+    every row, and two for the prior."""
+    T, Hq, _ = q.shape
+    n_pages, H, page, _ = cache["K_codes"].shape
+    G = Hq // H
+    W, bound = np.full((n_pages, H, page), np.nan), np.zeros((n_pages, H, page))
+    for b in range(len(kv_len)):
+        kv = min(_length(kv_len[b]), table.shape[1] * page)
+        j = np.arange(kv)
+        lo, hi = int(q_start[b]), min(int(q_start[b + 1]), T)
+        p = pos0 + _length(kv_len[b]) - int(q_start[b + 1]) + np.arange(lo, hi)[:, None]
+        far = p - (pos0 + j)[None]
+        seen = np.ones(far.shape, bool)
+        if causal:
+            seen &= (far >= 0) | (pos0 + j < (bidir_len[b] if bidir_len is not None else 0))[None]
+        if window:
+            seen &= np.abs(far) < window
+        for h in range(H):
+            kd, ks, _, _, there = cache_tokens(cache, table[b], h, kv)
+            fine = there & np.isfinite(ks)
+            ks = np.where(fine, ks, 0.0)
+            w, e = np.zeros(kv), np.zeros(kv)
+            for g in range(h * G, (h + 1) * G):
+                counts = np.isfinite(lse[lo:hi, g])
+                x = np.where(counts[:, None], q[lo:hi, g].astype(np.float64), 0.0)
+                log = np.where(counts, lse[lo:hi, g].astype(np.float64), 0.0)[:, None]
+                z = scale * (x @ kd.T) * ks
+                ez = 132 * 2.0 ** -24 * abs(scale) * (np.abs(x) @ np.abs(kd).T) * ks
+                if softcap:
+                    z = softcap * np.tanh(z / softcap)
+                    ez += softcap * 2.0 ** -22 if softcap <= 64 else np.abs(z) * 2.0 ** -18
+                if slopes is not None:
+                    z = z - float(slopes[g]) * np.abs(far)
+                    ez += float(slopes[g]) * np.abs(far) * 2.0 ** -22
+                ez += 2.0 ** -22 * (np.abs(z) + np.abs(log) + 1)
+                weight = np.where(seen & counts[:, None] & fine[None], np.exp(np.minimum(z - log, 700.0)), 0.0)
+                w += weight.sum(0)
+                e += (weight * ez).sum(0)
+            e += 2.0 ** -24 * ((hi - lo) * G + 8) * w
+            at, slot = np.where(there, table[b][j // page], 0)[there], (j % page)[there]
+            if prior is not None:
+                w[there] += decay * prior[at, h, slot].astype(np.float64)
+                e[there] += 2.0 ** -23 * (np.abs(decay * prior[at, h, slot]) + np.abs(w[there]))
+            W[at, h, slot], bound[at, h, slot] = w[there], e[there] + 2.0 ** -110
+    return W, bound
+
+
+def kv_choose(W, table, kv_len, keep, first=0, recent=0):
+    """(kept [B, Hkv, keep] int32, lens [B]): by sorting."""
+    n_pages, H, page = W.shape
+    kept, lens = np.full((len(kv_len), H, keep), -1, np.int32), np.zeros(len(kv_len), np.int32)
+    for b in range(len(kv_len)):
+        n = min(max(int(kv_len[b]), 0), table.shape[1] * page)
+        j = np.arange(n)
+        ids = table[b][j // page]
+        there = (ids >= 0) & (ids < n_pages)
+        must = (j < first) | (j >= n - recent)
+        lens[b] = m = min(n, keep)
+        for h in range(H):
+            w = W[np.where(there, ids, 0), h, j % page].astype(np.float64)
+            none = ~there | np.isnan(w)
+            order = np.lexsort((j, -np.where(none, 0.0, w), none, ~must))
+            kept[b, h, :m] = np.sort(order[:m])
+    return kept, lens
+
+
+def kv_move(cache, table, kept, at=None, to_table=None, W=None):
+    """(the changed cache, the changed W): every token is read before any is written."""
+    n_pages, H, page, _ = cache["K_codes"].shape
+    old = dict(cache) if W is None else dict(cache, W=W)
+    new = {k: v.copy() for k, v in old.items()}
+    to_table = table if to_table is None else to_table
+
+    def slot(rows, place):
+        if place < 0 or place >= len(rows) * page or not 0 <= rows[place // page] < n_pages:
+            return None
+        return int(rows[place // page]), place % page
+
+    for b in range(len(table)):
+        start = 0 if at is None else int(at[b])
+        for h in range(H):
+            for i, src in enumerate(kept[b, h % kept.shape[1]]):
+                here, there = slot(table[b], start + int(src)), slot(to_table[b], start + i)
+                if src < 0 or here is None or there is None:
+                    continue
+                (p, s), (q, d) = here, there
+                for name in old:
+                    if name == "V_codes":
+                        new[name][q, h, d // 4, :, d % 4] = old[name][p, h, s // 4, :, s % 4]
+                    else:
+                        new[name][q, h, d] = old[name][p, h, s]
+    return {k: v for k, v in new.items() if k != "W"}, new.get("W")

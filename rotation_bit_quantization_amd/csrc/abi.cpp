@@ -130,16 +130,80 @@ bool aligned_all(std::initializer_list<const void*> ps) {   // NULL counts as al
     return true;
 }
 
+spin_status kv_append_impl(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq, int Hkv,
+                           int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_norm,
+                           const float* k_norm, float eps, const float* rope, int rope_len, int rot_dim,
+                           int interleaved, int pos0, const int32_t* positions, int bits, uint8_t* K_codes, uint16_t* K_scale,
+                           uint8_t* V_codes, uint16_t* V_scale, int n_pages, int page_size, int B,
+                           const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                           uint16_t* Q_out, void* stream) {
+    if (!K || !V || !K_codes || !K_scale || !V_codes || !V_scale || !q_start || !kv_len || !page_table)
+        return SPIN_ERR_NULL;
+    if ((Q == nullptr) != (Q_out == nullptr) || (rope == nullptr) != (rot_dim == 0)) return SPIN_ERR_NULL;
+    if (x_dtype != SPIN_F32 && x_dtype != SPIN_F16) return SPIN_ERR_UNSUPPORTED;
+    if (interleaved != 0 && interleaved != 1) return SPIN_ERR_UNSUPPORTED;
+    if ((q_norm || k_norm) && !(eps >= 0.0f && eps < __builtin_inff())) return SPIN_ERR_UNSUPPORTED;
+    const spin_status ok = paged_ok(D, bits, Hkv, n_pages, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (T < 0 || (Q && Hq < 1) || rot_dim < 0 || rot_dim > 128 || rot_dim % 16 != 0 || pos0 < 0 ||
+        pos0 > SPIN_KV_MAX_CONTEXT || (rope && rope_len < 1))
+        return SPIN_ERR_BAD_SHAPE;
+    const int64_t per16 = x_dtype == SPIN_F16 ? 8 : 4;   // values in 16 bytes
+    const int64_t far = int64_t{1} << 40;
+    for (const int64_t s : {Q ? q_stride : k_stride, k_stride, v_stride})
+        if (s < 128 || s > far || s % per16 != 0) return SPIN_ERR_BAD_SHAPE;
+    if (k_stride < int64_t{128} * Hkv || v_stride < int64_t{128} * Hkv || (Q && q_stride < int64_t{128} * Hq))
+        return SPIN_ERR_BAD_SHAPE;
+    if (spin::kv_append_blocks(T, Q ? Hq : 0, Hkv) > (1LL << 24) - 1) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({Q, K, V, q_norm, k_norm, rope, K_codes, K_scale, V_codes, V_scale, q_start, kv_len, page_table, Q_out, positions}))
+        return SPIN_ERR_MISALIGNED;
+    if (T == 0 || B == 0) return SPIN_OK;
+    spin::KvAppendArgs a = {};
+    a.Q = Q;
+    a.K = K;
+    a.V = V;
+    a.T = T;
+    a.Hq = Q ? Hq : 0;
+    a.Hkv = Hkv;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    a.rope = rope;
+    a.rope_len = rope_len;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved == 1;
+    a.pos0 = pos0;
+    a.positions = positions;
+    a.B = B;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.page_log2 = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.K_codes = K_codes;
+    a.K_scale = K_scale;
+    a.V_codes = V_codes;
+    a.V_scale = V_scale;
+    a.Q_out = Q_out;
+    return from_hip(spin::launch_kv_append(a, x_dtype == SPIN_F16, bits, static_cast<hipStream_t>(stream)));
+}
+
 spin_status kv_attn_impl(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
                          const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale, int n_pages,
                          int page_size, int B, const int32_t* q_start, const int32_t* kv_len,
                          const int32_t* page_table, int max_pages, const int32_t* prefix_table, int prefix_len,
                          float scale, float softcap, const float* slopes, int window, int causal,
-                         const int32_t* bidir_len, uint16_t* O, void* workspace, size_t workspace_bytes,
-                         void* stream) {
+                         const int32_t* bidir_len, const uint32_t* tree, int tree_words, const int32_t* positions,
+                         uint16_t* O, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     if (!Q || !K_codes || !K_scale || !V_codes || !V_scale || !q_start || !kv_len || !page_table || !O)
         return SPIN_ERR_NULL;
     if (prefix_len > 0 && !prefix_table) return SPIN_ERR_NULL;
+    if (tree && !positions && (slopes || window > 0)) return SPIN_ERR_NULL;
+    if (tree && bidir_len) return SPIN_ERR_UNSUPPORTED;
     if (causal != 0 && causal != 1) return SPIN_ERR_UNSUPPORTED;
     if (!(scale > -__builtin_inff() && scale < __builtin_inff()) || !(softcap >= 0.0f && softcap < __builtin_inff()))
         return SPIN_ERR_UNSUPPORTED;
@@ -147,9 +211,10 @@ spin_status kv_attn_impl(const uint16_t* Q, int T, int Hq, int Hkv, int D, int b
     if (ok != SPIN_OK) return ok;
     if (T < 0 || Hq < 1 || Hq % Hkv != 0 || window < 0 || prefix_len < 0 || prefix_len > SPIN_KV_MAX_CONTEXT)
         return SPIN_ERR_BAD_SHAPE;
+    if (tree && (tree_words < 1 || tree_words > SPIN_KV_TREE_MAX_WORDS)) return SPIN_ERR_BAD_SHAPE;
     if (T > 0 && B > 0 && !spin::kv_attn_fits(T, Hq, Hkv, B, max_pages * page_size, prefix_len)) return SPIN_ERR_BAD_SHAPE;
     if (!aligned_all({Q, K_codes, K_scale, V_codes, V_scale, q_start, kv_len, page_table, prefix_table, slopes, bidir_len, O,
-                      workspace}))
+                      workspace, tree, positions, lse}))
         return SPIN_ERR_MISALIGNED;
     if (T == 0 || B == 0) return SPIN_OK;
     const size_t need = spin::kv_attn_workspace(T, Hq, Hkv, B, max_pages * page_size, prefix_len);
@@ -177,8 +242,12 @@ spin_status kv_attn_impl(const uint16_t* Q, int T, int Hq, int Hkv, int D, int b
     a.softcap = softcap;
     a.slopes = slopes;
     a.window = window;
-    a.causal = causal == 1;
+    a.causal = causal == 1 && !tree;
     a.bidir_len = bidir_len;
+    a.tree = tree;
+    a.tree_words = tree_words;
+    a.positions = tree ? positions : nullptr;
+    a.lse = lse;
     a.O = O;
     a.partial = static_cast<float*>(workspace);
     return from_hip(spin::launch_kv_attn(a, bits, static_cast<hipStream_t>(stream)));
@@ -397,58 +466,22 @@ spin_status spin_kv_append(const void* Q, const void* K, const void* V, spin_dty
                            uint8_t* V_codes, uint16_t* V_scale, int n_pages, int page_size, int B,
                            const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
                            uint16_t* Q_out, void* stream) {
-    if (!K || !V || !K_codes || !K_scale || !V_codes || !V_scale || !q_start || !kv_len || !page_table)
-        return SPIN_ERR_NULL;
-    if ((Q == nullptr) != (Q_out == nullptr) || (rope == nullptr) != (rot_dim == 0)) return SPIN_ERR_NULL;
-    if (x_dtype != SPIN_F32 && x_dtype != SPIN_F16) return SPIN_ERR_UNSUPPORTED;
-    if (interleaved != 0 && interleaved != 1) return SPIN_ERR_UNSUPPORTED;
-    if ((q_norm || k_norm) && !(eps >= 0.0f && eps < __builtin_inff())) return SPIN_ERR_UNSUPPORTED;
-    const spin_status ok = paged_ok(D, bits, Hkv, n_pages, page_size, B, max_pages);
-    if (ok != SPIN_OK) return ok;
-    if (T < 0 || (Q && Hq < 1) || rot_dim < 0 || rot_dim > 128 || rot_dim % 16 != 0 || pos0 < 0 ||
-        pos0 > SPIN_KV_MAX_CONTEXT || (rope && rope_len < 1))
-        return SPIN_ERR_BAD_SHAPE;
-    const int64_t per16 = x_dtype == SPIN_F16 ? 8 : 4;   // values in 16 bytes
-    const int64_t far = int64_t{1} << 40;
-    for (const int64_t s : {Q ? q_stride : k_stride, k_stride, v_stride})
-        if (s < 128 || s > far || s % per16 != 0) return SPIN_ERR_BAD_SHAPE;
-    if (k_stride < int64_t{128} * Hkv || v_stride < int64_t{128} * Hkv || (Q && q_stride < int64_t{128} * Hq))
-        return SPIN_ERR_BAD_SHAPE;
-    if (spin::kv_append_blocks(T, Q ? Hq : 0, Hkv) > (1LL << 24) - 1) return SPIN_ERR_BAD_SHAPE;
-    if (!aligned_all({Q, K, V, q_norm, k_norm, rope, K_codes, K_scale, V_codes, V_scale, q_start, kv_len, page_table, Q_out}))
-        return SPIN_ERR_MISALIGNED;
-    if (T == 0 || B == 0) return SPIN_OK;
-    spin::KvAppendArgs a = {};
-    a.Q = Q;
-    a.K = K;
-    a.V = V;
-    a.T = T;
-    a.Hq = Q ? Hq : 0;
-    a.Hkv = Hkv;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.q_norm = q_norm;
-    a.k_norm = k_norm;
-    a.eps = eps;
-    a.rope = rope;
-    a.rope_len = rope_len;
-    a.rot_dim = rot_dim;
-    a.interleaved = interleaved == 1;
-    a.pos0 = pos0;
-    a.B = B;
-    a.q_start = q_start;
-    a.kv_len = kv_len;
-    a.page_table = page_table;
-    a.max_pages = max_pages;
-    a.n_pages = n_pages;
-    a.page_log2 = __builtin_ctz(static_cast<unsigned>(page_size));
-    a.K_codes = K_codes;
-    a.K_scale = K_scale;
-    a.V_codes = V_codes;
-    a.V_scale = V_scale;
-    a.Q_out = Q_out;
-    return from_hip(spin::launch_kv_append(a, x_dtype == SPIN_F16, bits, static_cast<hipStream_t>(stream)));
+    return kv_append_impl(Q, K, V, x_dtype, T, Hq, Hkv, D, q_stride, k_stride, v_stride, q_norm, k_norm, eps, rope,
+                          rope_len, rot_dim, interleaved, pos0, nullptr, bits, K_codes, K_scale, V_codes, V_scale, n_pages,
+                          page_size, B, q_start, kv_len, page_table, max_pages, Q_out, stream);
+}
+
+spin_status spin_kv_append_at(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq, int Hkv,
+                              int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_norm,
+                              const float* k_norm, float eps, const float* rope, int rope_len, int rot_dim,
+                              int interleaved, const int32_t* positions, int bits, uint8_t* K_codes, uint16_t* K_scale,
+                              uint8_t* V_codes, uint16_t* V_scale, int n_pages, int page_size, int B,
+                              const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                              uint16_t* Q_out, void* stream) {
+    if (!positions) return SPIN_ERR_NULL;
+    return kv_append_impl(Q, K, V, x_dtype, T, Hq, Hkv, D, q_stride, k_stride, v_stride, q_norm, k_norm, eps, rope,
+                          rope_len, rot_dim, interleaved, 0, positions, bits, K_codes, K_scale, V_codes, V_scale, n_pages,
+                          page_size, B, q_start, kv_len, page_table, max_pages, Q_out, stream);
 }
 
 spin_status spin_kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, int prefix_len,
@@ -472,7 +505,7 @@ spin_status spin_kv_attn(const uint16_t* Q, int T, int Hq, int Hkv, int D, int b
                          size_t workspace_bytes, void* stream) {
     return kv_attn_impl(Q, T, Hq, Hkv, D, bits, K_codes, K_scale, V_codes, V_scale, n_pages, page_size, B, q_start,
                         kv_len, page_table, max_pages, nullptr, 0, scale, softcap, slopes, window, causal, bidir_len,
-                        O, workspace, workspace_bytes, stream);
+                        nullptr, 0, nullptr, O, nullptr, workspace, workspace_bytes, stream);
 }
 
 spin_status spin_kv_attn_shared(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
@@ -484,7 +517,109 @@ spin_status spin_kv_attn_shared(const uint16_t* Q, int T, int Hq, int Hkv, int D
                                 size_t workspace_bytes, void* stream) {
     return kv_attn_impl(Q, T, Hq, Hkv, D, bits, K_codes, K_scale, V_codes, V_scale, n_pages, page_size, B, q_start,
                         kv_len, page_table, max_pages, prefix_table, prefix_len, scale, softcap, slopes, window,
-                        causal, bidir_len, O, workspace, workspace_bytes, stream);
+                        causal, bidir_len, nullptr, 0, nullptr, O, nullptr, workspace, workspace_bytes, stream);
+}
+
+spin_status spin_kv_attn_ex(const uint16_t* Q, int T, int Hq, int Hkv, int D, int bits, const uint8_t* K_codes,
+                            const uint16_t* K_scale, const uint8_t* V_codes, const uint16_t* V_scale, int n_pages,
+                            int page_size, const int32_t* prefix_table, int prefix_len, int B, const int32_t* q_start,
+                            const int32_t* kv_len, const int32_t* page_table, int max_pages, float scale,
+                            float softcap, const float* slopes, int window, int causal, const int32_t* bidir_len,
+                            const uint32_t* tree, int tree_words, const int32_t* positions, uint16_t* O, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    return kv_attn_impl(Q, T, Hq, Hkv, D, bits, K_codes, K_scale, V_codes, V_scale, n_pages, page_size, B, q_start,
+                        kv_len, page_table, max_pages, prefix_table, prefix_len, scale, softcap, slopes, window,
+                        causal, bidir_len, tree, tree_words, positions, O, lse, workspace, workspace_bytes, stream);
+}
+
+spin_status spin_kv_tree(const int32_t* parent, int T, int B, const int32_t* q_start, const int32_t* kv_len, int pos0,
+                         int words, uint32_t* tree, int32_t* positions, void* stream) {
+    if (!parent || !q_start || !kv_len || !tree || !positions) return SPIN_ERR_NULL;
+    if (T < 0 || T > (1 << 26) || B < 0 || pos0 < 0 || pos0 > SPIN_KV_MAX_CONTEXT || words < 1 || words > SPIN_KV_TREE_MAX_WORDS)
+        return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({parent, q_start, kv_len, tree, positions})) return SPIN_ERR_MISALIGNED;
+    if (T == 0 || B == 0) return SPIN_OK;
+    return from_hip(spin::launch_kv_tree({parent, T, B, q_start, kv_len, pos0, words, tree, positions},
+                                         static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
+                            const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
+                            const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                            int pos0, float scale, float softcap, const float* slopes, int window, int causal,
+                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* stream) {
+    if (!Q || !lse || !K_codes || !K_scale || !q_start || !kv_len || !page_table || !W) return SPIN_ERR_NULL;
+    if (causal != 0 && causal != 1) return SPIN_ERR_UNSUPPORTED;
+    const float inf = __builtin_inff();
+    if (!(scale > -inf && scale < inf) || !(softcap >= 0.0f && softcap < inf) || !(decay > -inf && decay < inf))
+        return SPIN_ERR_UNSUPPORTED;
+    const spin_status ok = paged_ok(D, bits, Hkv, n_pages, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (T < 0 || Hq < 1 || Hq % Hkv != 0 || window < 0 || pos0 < 0 || pos0 > SPIN_KV_MAX_CONTEXT) return SPIN_ERR_BAD_SHAPE;
+    if (!spin::kv_weights_fits(T, Hq, Hkv, B, max_pages * page_size)) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({Q, lse, K_codes, K_scale, q_start, kv_len, page_table, slopes, bidir_len, prior, W}))
+        return SPIN_ERR_MISALIGNED;
+    if (B == 0) return SPIN_OK;
+    spin::KvWeightsArgs a = {};
+    a.Q = Q;
+    a.lse = lse;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.K_codes = K_codes;
+    a.K_scale = K_scale;
+    a.n_pages = n_pages;
+    a.page_log2 = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.B = B;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.pos0 = pos0;
+    a.scale = scale;
+    a.softcap = softcap;
+    a.slopes = slopes;
+    a.window = window;
+    a.causal = causal == 1;
+    a.bidir_len = bidir_len;
+    a.prior = prior;
+    a.decay = decay;
+    a.W = W;
+    return from_hip(spin::launch_kv_weights(a, bits, static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, int B, const int32_t* kv_len,
+                           const int32_t* page_table, int max_pages, int keep, int first, int recent, int32_t* kept,
+                           int32_t* lens, void* stream) {
+    if (!W || !kv_len || !page_table || !kept || !lens) return SPIN_ERR_NULL;
+    const spin_status ok = paged_ok(128, 4, Hkv, n_pages, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (keep < 1 || keep > SPIN_KV_MAX_CONTEXT || first < 0 || recent < 0 || first > keep || recent > keep - first)
+        return SPIN_ERR_BAD_SHAPE;
+    if (!spin::kv_choose_fits(Hkv, B)) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({W, kv_len, page_table, kept, lens})) return SPIN_ERR_MISALIGNED;
+    if (B == 0) return SPIN_OK;
+    return from_hip(spin::launch_kv_choose({W, Hkv, n_pages, __builtin_ctz(static_cast<unsigned>(page_size)), B, kv_len, page_table,
+                                            max_pages, keep, first, recent, kept, lens}, static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_move(uint8_t* K_codes, uint16_t* K_scale, uint8_t* V_codes, uint16_t* V_scale, float* W, int Hkv,
+                         int D, int bits, int n_pages, int page_size, int B, const int32_t* page_table, int max_pages,
+                         const int32_t* kept, int kept_heads, int n, const int32_t* at, const int32_t* to_table,
+                         int to_pages, void* stream) {
+    if (!K_codes || !K_scale || !V_codes || !V_scale || !page_table || !kept) return SPIN_ERR_NULL;
+    const spin_status ok = paged_ok(D, bits, Hkv, n_pages, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (n < 0 || (kept_heads != 1 && kept_heads != Hkv) || (to_table && paged_ok(D, bits, Hkv, n_pages, page_size, B, to_pages) != SPIN_OK))
+        return SPIN_ERR_BAD_SHAPE;
+    if (!spin::kv_move_fits(Hkv, B, n)) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({K_codes, K_scale, V_codes, V_scale, W})) return SPIN_ERR_MISALIGNED;
+    for (const int32_t* p : {page_table, kept, at, to_table})
+        if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return SPIN_ERR_MISALIGNED;
+    if (B == 0 || n == 0) return SPIN_OK;
+    return from_hip(spin::launch_kv_move({K_codes, K_scale, V_codes, V_scale, W, Hkv, n_pages,
+                                          __builtin_ctz(static_cast<unsigned>(page_size)), B, page_table, max_pages, kept,
+                                          kept_heads, n, at, to_table, to_pages}, bits, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

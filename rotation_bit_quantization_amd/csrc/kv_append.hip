@@ -218,18 +218,20 @@ __device__ __forceinline__ F turned(const TIn* __restrict__ x, const float* __re
 struct Place {
     bool in_batch;      // the row belongs to a sequence
     long long pos;      // position within the sequence's own pages, -1 if there is none
+    long long turn;     // position that it is turned by, its row of the rotary table
     int page;           // -1 if there is none
     int slot;
 };
 
 __device__ __forceinline__ Place find_place(const KvAppendArgs& a, int t, int l) {
-    Place p = {false, -1, -1, 0};
+    Place p = {false, -1, 0, -1, 0};
     const int b = find_sequence16(a.q_start, a.B, t, l);
     if (b < 0) return p;
     p.in_batch = true;
     const long long pos = static_cast<long long>(placed(a.kv_len[b])) - a.q_start[b + 1] + t;
     if (pos < 0 || pos >= static_cast<long long>(a.max_pages) << a.page_log2) return p;
-    if (a.rope && pos + a.pos0 >= a.rope_len) return p;
+    p.turn = a.positions ? a.positions[t] : pos + a.pos0;
+    if (a.rope && (p.turn < 0 || p.turn >= a.rope_len)) return p;
     p.pos = pos;
     const int page = a.page_table[static_cast<long long>(b) * a.max_pages + (pos >> a.page_log2)];
     p.page = page >= 0 && page < a.n_pages ? page : -1;
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv_append_kernel(KvAppendAr
             *reinterpret_cast<uint4*>(a.Q_out + (static_cast<long long>(t) * a.Hq + h0 + i) * 128 + 8 * l) = uint4{};
         return;
     }
-    const float* rope_row = a.rope + (p.pos + a.pos0) * a.rot_dim;
+    const float* rope_row = a.rope + p.turn * a.rot_dim;
     if (kind == 0) {
         // Everything of 64 bits is loaded and derived anew for every head: kept, it would take 80 registers.
         for (int i = 0; i < heads; ++i, x += 128) {

@@ -21,18 +21,12 @@
 // from accumulators to operands without leaving the lane, and the rescaling of
 // a row is one multiplication per register.
 #include "kv_batch.h"
+#include "kv_scores.h"
 #include "spin_device.h"
 #include "spin_internal.h"
 
 namespace spin {
 namespace {
-
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
@@ -49,10 +43,6 @@ constexpr int kMostSplits = 256;
 constexpr int kCounted = 256;             // sequences up to which tiles of 16 rows are found by counting
 constexpr float kSlack = 8.0f;            // M may lag a row's maximum by this many powers of two
 static_assert(kSlack <= 12.0f, "weights of 2^kSlack lie well below the largest fp16, 65504");
-constexpr float kLog2e = 1.4426950408889634f;
-// Caps up to this one go by capped_plus, whose error is that of a number of the cap's size, above by capped_wide, which is
-// ten operations longer (8 tokens on 32768, INT8, cap 50: 108 and 111 us; 1723 in chunks, cap 30 and a bias: 160 and 191).
-constexpr float kNearCap = 64.0f;
 // Rows on the same tokens, and rows times tokens of all heads, from which tiles of 128 rows are taken, and of 256 (twice
 // that for a sequence's own tokens: masks leave half of them).  Measured in us on tiles of 16, 128, 256 rows with 32 + 8
 // heads: 16 sequences on 4096 tokens with 64 rows a key head each 56, 58, 77; 128 89, 67, 84; 256 153, 94, 106; 512 278,
@@ -62,52 +52,6 @@ constexpr float kNearCap = 64.0f;
 constexpr int kManyRows = 64;
 constexpr double kTileWork = 1 << 25, kWideWork = 1 << 27;
 constexpr int kPartial = 130;             // floats of a row's partial result: 128 sums, M, sum
-
-union Frag {
-    uint32_t w[4];
-    h8 v;
-};
-
-// Two fp16 integers 1024 + u (u in the low bits of each half) minus `off`: exact.
-__device__ __forceinline__ uint32_t minus(uint32_t x, float off) {
-    const h2 o = {static_cast<_Float16>(-off), static_cast<_Float16>(-off)};
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) + o);
-}
-
-// Eight codes of one token as an operand.  The order of the eight within the
-// operand (order8) is the one that needs fewest instructions; queries are
-// loaded in the same order.
-template <int BITS>
-__device__ __forceinline__ int order8(int i) {
-    // 4 bits: 0 4 1 5 2 6 3 7;  8 bits: 0 2 1 3 4 6 5 7
-    if (BITS == 4) return (i >> 1) + 4 * (i & 1);
-    return (i & 4) + ((i & 2) >> 1) + 2 * (i & 1);
-}
-template <int BITS>
-__device__ __forceinline__ h8 key_operand(const uint32_t* w) {
-    Frag f;
-    if (BITS == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.w[i] = minus(((w[0] >> (4 * i)) & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.w[i] = minus(((w[i >> 1] >> (8 * (i & 1))) & 0x00FF00FFu) ^ 0x64806480u, 1152.0f);
-    }
-    return f.v;
-}
-
-// The same without the subtraction: u = code + 8 (128) as the fp16 number u 2^-24, subnormal, which the matrix cores
-// take as it is.  The sum over a query is then 2^-24 (sum q code + 8 sum q): the second term goes into the accumulator
-// that the sum starts from.
-template <int BITS>
-__device__ __forceinline__ h8 key_operand_small(const uint32_t* w) {
-    Frag f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f.w[i] = BITS == 4 ? ((w[0] >> (4 * i)) & 0x000F000Fu) ^ 0x00080008u
-                           : ((w[i >> 1] >> (8 * (i & 1))) & 0x00FF00FFu) ^ 0x00800080u;
-    return f.v;
-}
 
 // Code j of an octet, of eight tokens: w[BITS / 4 * token + ...], as an operand; 16 times the code for odd j at 4 bits,
 // where it is not shifted down.
@@ -128,79 +72,27 @@ __device__ __forceinline__ h8 value_operand(const uint32_t* w, int j) {
     return f.v;
 }
 
-__device__ __forceinline__ float max_over_groups(float v) {   // lanes l, l ^ 16, l ^ 32, l ^ 48
-    u2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __builtin_fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
-    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __builtin_fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
-}
-__device__ __forceinline__ float sum_over_groups(float v) {
-    u2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(s.x) + __uint_as_float(s.y);
-    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(s.x) + __uint_as_float(s.y);
-}
-
 template <int N>
 __device__ __forceinline__ float row_lane(float v) {   // lane N of the 16 lanes of a row, for all of them
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x150 + N, 0xF, 0xF, true));
 }
 
-// A capped score in the exponent: cap log2(e) tanh(z / cap) = top - 2 top / (2^y + 1), y = 2 log2(e) z / cap, right at
-// both infinities.  `lm` is what is added to it, `top` = cap log2(e) already among it.  The two terms are of the size of
-// the cap whatever the score is, so that their roundings are: ten of 2^-24 cap (2^-21.7 cap measured).  At caps up to
-// kNearCap that is below a twelfth of the rounding of the weight to fp16.
-__device__ __forceinline__ float capped_plus(float y, float top, float lm) {
-    return __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y) + 1.0f), -2.0f * top, lm);
+// Of 32 tokens, the `first` of them counted among a sequence's new ones (below 0: the context), those that a row of the
+// tree names, the context among them.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* __restrict__ row, int words, int first) {
+    const int w = first >> 5;
+    const uint32_t lo = w < 0 ? ~0u : w < words ? row[w] : 0u;
+    const uint32_t hi = w + 1 < 0 ? ~0u : w + 1 < words ? row[w + 1] : 0u;
+    return static_cast<uint32_t>(((static_cast<unsigned long long>(hi) << 32) | lo) >> (first & 31));
 }
 
-// The same for any cap, off by at most 2^-18 of the score: z tanh(u) / u by its series (the next term is 2^-26 at 1/4)
-// where |u| = |z| / cap is small, the form above where the score is a quarter of the cap or more.  z in units of
-// 1 / log2(e), `rtop` = 1 / top.
-__device__ __forceinline__ float capped_wide(float z, float top, float rtop) {
-    const float u = z * rtop, u2 = u * u;
-    float p = __builtin_fmaf(u2, 62.0f / 2835.0f, -17.0f / 315.0f);
-    p = __builtin_fmaf(p, u2, 2.0f / 15.0f);
-    p = __builtin_fmaf(p, u2, -1.0f / 3.0f);
-    p = __builtin_fmaf(p, u2, 1.0f);
-    const float far = __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(u * (2.0f * kLog2e)) + 1.0f), -2.0f * top, top);
-    return __builtin_fabsf(u) < 0.25f ? z * p : far;
+// A new token's position, held to what differences of two fit 32 bits with.
+__device__ __forceinline__ int position(const KvAttnArgs& a, int t) { return min(max(a.positions[t], 0), 1 << 30); }
+
+// The logarithm of a row's sum of exponentials.
+__device__ __forceinline__ float log_sum(float M, float l) {
+    return l == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
-
-// What a kernel does to the scores: nothing; a distance bias, a cap up to kNearCap, or both; a cap above, with or without
-// a bias.
-enum Scores { kPlain, kFancy, kWideCap };
-
-// A factor of scores within the numbers that keep them finite.  Products are multiples of 2^-48, or zero: scores that this
-// brings down still lie past every cap up to kNearCap, or so far apart that their roundings, 2^-24 of them, are past what
-// weights tell apart.  In a scalar register: as a vector one it makes kv_attn_tile spill four more (chunks 159 -> 162 us).
-__device__ __forceinline__ float held(float factor) {
-    factor = __builtin_fminf(__builtin_fmaxf(factor, -0x1p100f), 0x1p100f);
-    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(factor)));
-}
-
-// How a score is capped: the factor of a product and its key's scale, the cap in units of 1 / log2(e) (0: none) and its
-// reciprocal.
-struct Cap {
-    float factor, top, rtop;
-};
-template <int SCORES>
-__device__ __forceinline__ Cap cap_of(const KvAttnArgs& a) {
-    if (SCORES == kWideCap) {
-        const float top = __builtin_fminf(a.softcap * kLog2e, 0x1p126f);       // its double has to be finite
-        return {a.scale * kLog2e, top, 1.0f / top};
-    }
-    const bool capped = SCORES == kFancy && a.softcap > 0.0f;
-    return {capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e, capped ? a.softcap * kLog2e : 0.0f, 0.0f};
-}
-
-// Tokens of sequence b that its table has room for.
-__device__ __forceinline__ int context(const KvAttnArgs& a, int b) {
-    return min(max(a.kv_len[b], 0), a.max_pages << a.page_log2);
-}
-
-// A border of the batch, held to its T rows.
-__device__ __forceinline__ int within(int row, int T) { return min(max(row, 0), T); }
 
 // Which tokens a workgroup has.
 struct Span {
@@ -284,7 +176,7 @@ __device__ __forceinline__ void longest_first(const KvAttnArgs& a, int lane, int
 // busy half of it with turning INT4 codes to fp16, and the last sequences run
 // alone), on 8192 each 5.4 TB/s; 1 on 1000 10 us, of which four loads that wait
 // for each other (sequence, length, page, codes) and four steps.
-template <int BITS, int SCORES, int WAVES>
+template <int BITS, int SCORES, int WAVES, bool TREE>
 __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                   int own_tiles, int own_splits, int own_chunk) {
     __shared__ float o_sh[WAVES][kRows][129];
@@ -311,6 +203,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     int t, head;             // this lane's row
     bool valid;
     int b;
+    int fresh = 0x7FFFFFFF, new0 = 0, news = 0;      // TREE: place of the sequence's first new token, its row, how many
     if (shared) {
         const int r = tile * kRows + n;
         t = r / G;
@@ -350,11 +243,18 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         t = q0 + i;
         head = h * G + (valid ? r - i * G : 0);
         span = {a.page_table + static_cast<long long>(b) * a.max_pages, a.max_pages, context(a, b), a.prefix_len};
+        if (TREE) {
+            new0 = __builtin_amdgcn_readfirstlane(q0);
+            news = __builtin_amdgcn_readfirstlane(q1 - q0);
+            fresh = __builtin_amdgcn_readfirstlane(placed(a.kv_len[b])) - news;
+        }
     }
     if (__ballot(valid) == 0) return;      // the same 16 rows in every wave: the workgroup leaves together
 
     int pos = 0, both = 0;                 // the row's position, and the tokens that it sees whatever their order
-    if (valid) {
+    if (TREE) {
+        if (valid && a.positions) pos = position(a, t);
+    } else if (valid) {
         pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
         if (a.bidir_len) both = max(a.bidir_len[b], 0);    // no token stands below 0: differences of it fit 32 bits
     }
@@ -372,7 +272,10 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     if (a.causal) hi = min(hi, pmax - span.base);
     if (a.window > 0) {
         lo = static_cast<int>(max(static_cast<long long>(pmin) - a.window + 1 - span.base, 0LL));
-        hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(wmax) + a.window - span.base));
+        if (TREE)
+            lo = min(lo, max(fresh, 0));       // new tokens stand where `positions` says
+        else
+            hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(wmax) + a.window - span.base));
     }
     int step0 = lo / kStep;
     const int steps_all = hi > lo ? (hi + kStep - 1) / kStep - step0 : 0;
@@ -382,6 +285,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
     // every row sees every token of the steps whole0 .. whole1 - 1
     int whole0 = 0, whole1 = span.tokens;
     if (a.causal) whole1 = min(whole1, max(pmin + 1, bmin) - span.base);
+    if (TREE) whole1 = min(whole1, fresh);
     if (a.window > 0) {
         whole0 = static_cast<int>(max(static_cast<long long>(wmax) - a.window + 1 - span.base, 0LL));
         whole1 = static_cast<int>(min(static_cast<long long>(whole1), static_cast<long long>(pmin) + a.window - span.base));
@@ -515,8 +419,21 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         fetch_keys(next);
         const float from = SCORES == kFancy ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * g);
+        float far[8];                      // TREE: the tokens' distances
+        if (TREE && SCORES != kPlain) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) far[e] = rel - static_cast<float>(16 * (e >> 2) + (e & 3));
+            if (a.slopes && (st + 1) * kStep > fresh) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = st * kStep + 4 * g + 16 * (e >> 2) + (e & 3) - fresh;
+                    if (i >= 0 && i < news) far[e] = static_cast<float>(pos - position(a, new0 + i));
+                }
+            }
+        }
         auto exponent = [&](int e, float k, float lm, bool capped) __attribute__((always_inline)) {
-            if (SCORES != kPlain) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
+            if (SCORES != kPlain)
+                lm = __builtin_fmaf(-slope, __builtin_fabsf(TREE ? far[e] : rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
             x[e] = SCORES == kWideCap ? capped_wide(x[e] * k, cap.top, cap.rtop) + lm
                                       : capped ? capped_plus(x[e] * k, cap.top, lm) : __builtin_fmaf(x[e], k, lm);
         };
@@ -537,10 +454,18 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
             const int end = a.causal ? max(rel, both - j0 - 4 * g - 1) : 32;
             const uint32_t off = a.window > 0 ? static_cast<uint32_t>(rel) + static_cast<uint32_t>(a.window) - 1u : 32u;
             const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
+            const int first = st * kStep - fresh;
+            const uint32_t named = TREE && valid ? tree_bits(a.tree + static_cast<long long>(t) * a.tree_words, a.tree_words, first) >> (4 * g) : 0u;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = 16 * (e >> 2) + (e & 3);
-                const bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
+                bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
+                if (TREE) {
+                    const int i = first + 4 * g + c;
+                    if (a.window > 0 && i >= 0 && i < news)
+                        seen = static_cast<uint32_t>(pos - position(a, new0 + i)) + static_cast<uint32_t>(a.window) - 1u < wide;
+                    seen = seen && (named >> c & 1);
+                }
                 x[e] = seen ? x[e] : -__builtin_inff();
             }
         }
@@ -662,6 +587,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         M_run = M_new;
     }
     const float rl = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+    if (a.lse && c == 0) a.lse[at] = log_sum(M_run, l_all);
     Frag res;
 #pragma unroll
     for (int i = 0; i < 8; ++i) res.v[i] = static_cast<_Float16>(out[i] * rl);
@@ -712,7 +638,7 @@ __device__ __forceinline__ void part_barrier() {
 // INT4, 615 - 634 us a call, 690 - 735 traced (0.55 TFLOP, 0.75 - 0.89 PFLOP/s); uneven chunks of 1723
 // tokens, 32 + 32 heads, INT8, capped and with a distance bias, on up to 2900,
 // 149 - 160 us a call, 172 traced (32 exponentials and reciprocals a lane and 32 tokens more).
-template <int BITS, int ROWS, int SCORES>
+template <int BITS, int ROWS, int SCORES, bool TREE>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                 int own_tiles, int own_splits, int own_chunk) {
     constexpr bool kPair = ROWS == 128;            // two waves a row
@@ -746,6 +672,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     Span span;
     int t, head, pos = 0, both = 0;
     bool valid;
+    int fresh = 0x7FFFFFFF, new0 = 0, news = 0;      // TREE: place of the sequence's first new token, its row, how many
     if (shared) {
         span = {a.prefix_table, (a.prefix_len + (1 << a.page_log2) - 1) >> a.page_log2, a.prefix_len, 0};
         const unsigned r = static_cast<unsigned>(tile) * ROWS + row_wave * 32 + n;
@@ -762,7 +689,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         const int b = t < a.T ? find_sequence(fits ? borders : a.q_start, a.B, t) : -1;
         if (fits) __syncthreads();
         valid = b >= 0;
-        if (valid) {
+        if (TREE) {
+            if (valid && a.positions) pos = position(a, t);
+        } else if (valid) {
             pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
             if (a.bidir_len) both = max(a.bidir_len[b], 0);    // no token stands below 0: differences of it fit 32 bits
         }
@@ -794,7 +723,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         const int i = valid ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(G)) : 0;
         t = q0 + i;
         head = h * G + (valid ? r - i * G : 0);
-        if (valid) {
+        if (TREE) {
+            new0 = __builtin_amdgcn_readfirstlane(q0);
+            news = __builtin_amdgcn_readfirstlane(q1 - q0);
+            fresh = __builtin_amdgcn_readfirstlane(placed(a.kv_len[b])) - news;
+            if (valid && a.positions) pos = position(a, t);
+        } else if (valid) {
             pos = a.prefix_len + placed(a.kv_len[b]) - a.q_start[b + 1] + t;
             if (a.bidir_len) both = max(a.bidir_len[b], 0);    // no token stands below 0: differences of it fit 32 bits
         }
@@ -833,7 +767,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         if (a.causal) hi = min(hi, gend - span.base);
         if (a.window > 0) {
             lo = static_cast<int>(max(static_cast<long long>(gmin) - a.window + 1 - span.base, 0LL));
-            hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(gmax) + a.window - span.base));
+            if (TREE)
+                lo = min(lo, max(fresh, 0));       // new tokens stand where `positions` says
+            else
+                hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(gmax) + a.window - span.base));
         }
     }
     lo = __builtin_amdgcn_readfirstlane(lo);
@@ -952,7 +889,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         bool some = wave_any;
         const int last = j0 + kTileTokens - 1;
         if (a.causal) some = some && j0 < max(pmax + 1, bmax);
-        if (a.window > 0)
+        if (a.window > 0 && (!TREE || last - span.base < fresh))
             some = some && static_cast<long long>(last) > static_cast<long long>(pmin) - a.window &&
                    static_cast<long long>(j0) < static_cast<long long>(pmax) + a.window;
         return some;
@@ -961,6 +898,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         bool whole = true;
         const int last = j0 + kTileTokens - 1;
         if (a.causal) whole = last <= pmin || last < bmin;
+        if (TREE) whole = last - span.base < fresh;
         if (a.window > 0) whole = whole && static_cast<long long>(pmax) - j0 < a.window && static_cast<long long>(last) - pmin < a.window;
         return whole;
     };
@@ -983,9 +921,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     auto exponents = [&](int j0) __attribute__((always_inline)) {
         const float from = SCORES == kFancy ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * hf);
+        const int new_at = j0 - span.base + 4 * hf - fresh;
+        const bool drafted = TREE && a.slopes && j0 - span.base + 32 > fresh;
         auto one = [&](int e, float lm, bool capped) __attribute__((always_inline)) {
             const float k = kf[e >> 2][e & 3];
-            if (SCORES != kPlain) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
+            if (SCORES != kPlain) {
+                float far = rel - static_cast<float>(8 * (e >> 2) + (e & 3));
+                if (TREE && drafted) {
+                    const int i = new_at + 8 * (e >> 2) + (e & 3);
+                    if (i >= 0 && i < news) far = static_cast<float>(pos - position(a, new0 + i));
+                }
+                lm = __builtin_fmaf(-slope, __builtin_fabsf(far), lm);
+            }
             s[e] = SCORES == kWideCap ? capped_wide(s[e] * k, cap.top, cap.rtop) + lm
                                       : capped ? capped_plus(s[e] * k, cap.top, lm) : __builtin_fmaf(s[e], k, lm);
         };
@@ -1008,10 +955,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         const int end = a.causal ? max(rel, both - j0 - 4 * hf - 1) : 32;
         const uint32_t off = a.window > 0 ? static_cast<uint32_t>(rel) + static_cast<uint32_t>(a.window) - 1u : 32u;
         const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
+        const int first = j0 - span.base - fresh;
+        const uint32_t named = TREE && valid ? tree_bits(a.tree + static_cast<long long>(t) * a.tree_words, a.tree_words, first) >> (4 * hf) : 0u;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int c = 8 * (e >> 2) + (e & 3);
-            const bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
+            bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
+            if (TREE) {
+                const int i = first + 4 * hf + c;
+                if (a.window > 0 && i >= 0 && i < news)
+                    seen = static_cast<uint32_t>(pos - position(a, new0 + i)) + static_cast<uint32_t>(a.window) - 1u < wide;
+                seen = seen && (named >> c & 1);
+            }
             s[e] = seen ? s[e] : -__builtin_inff();
         }
     };
@@ -1231,6 +1186,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
             }
         }
     }
+    if (a.lse && total_splits == 1 && hf == 0) a.lse[at] = log_sum(M, l);
     if (total_splits > 1 && hf == 0) *reinterpret_cast<f2*>(partial + 128) = f2{l == 0.0f ? -__builtin_inff() : M, l};
 }
 
@@ -1284,6 +1240,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int s
             }
         }
     }
+    if (a.lse && lane == 0) a.lse[at] = log_sum(M, l);
     const float rl = l == 0.0f ? 0.0f : 1.0f / l;
     const h2 res = {static_cast<_Float16>(o.x * rl), static_cast<_Float16>(o.y * rl)};
     reinterpret_cast<h2*>(a.O)[at * 64 + lane] = res;
@@ -1351,41 +1308,41 @@ Plan plan(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
     return p;
 }
 
-template <int BITS, int ROWS, int SCORES>
+template <int BITS, int ROWS, int SCORES, bool TREE>
 hipError_t launch_part(const KvAttnArgs& a, const Part& prefix, const Part& own, hipStream_t s) {
     const unsigned items = static_cast<unsigned>(prefix.tiles * prefix.splits + own.tiles * own.splits);
     const int pt = static_cast<int>(prefix.tiles), ot = static_cast<int>(own.tiles);
     if constexpr (ROWS == kRows) {
         const dim3 grid((items + 7) / 8 * 8 * a.Hkv);
         if (own.waves == 8)
-            hipLaunchKernelGGL((kv_attn_rows16<BITS, SCORES, 8>), grid, dim3(512), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
+            hipLaunchKernelGGL((kv_attn_rows16<BITS, SCORES, 8, TREE>), grid, dim3(512), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
                                own.chunk);
         else
-            hipLaunchKernelGGL((kv_attn_rows16<BITS, SCORES, 4>), grid, dim3(256), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
+            hipLaunchKernelGGL((kv_attn_rows16<BITS, SCORES, 4, TREE>), grid, dim3(256), 0, s, a, pt, prefix.splits, prefix.chunk, ot, own.splits,
                                own.chunk);
     } else {
-        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, SCORES>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
+        hipLaunchKernelGGL((kv_attn_tile<BITS, ROWS, SCORES, TREE>), dim3(items * a.Hkv), dim3(kTileThreads), 0, s, a, pt,
                            prefix.splits, prefix.chunk, ot, own.splits, own.chunk);
     }
     return hipGetLastError();
 }
 
-template <int BITS, int ROWS>
+template <int BITS, int ROWS, bool TREE>
 hipError_t launch_rows(const KvAttnArgs& a, Part prefix, Part own, hipStream_t s) {
     // a part with another tile has a launch of its own; its share of the workspace stays where it is
     if (prefix.rows != ROWS) prefix.tiles = 0;
     if (own.rows != ROWS) own.tiles = 0;
     if (prefix.tiles == 0 && own.tiles == 0) return hipSuccess;
-    if (a.softcap > kNearCap) return launch_part<BITS, ROWS, kWideCap>(a, prefix, own, s);
-    return a.softcap > 0.0f || a.slopes ? launch_part<BITS, ROWS, kFancy>(a, prefix, own, s)
-                                        : launch_part<BITS, ROWS, kPlain>(a, prefix, own, s);
+    if (a.softcap > kNearCap) return launch_part<BITS, ROWS, kWideCap, TREE>(a, prefix, own, s);
+    return a.softcap > 0.0f || a.slopes ? launch_part<BITS, ROWS, kFancy, TREE>(a, prefix, own, s)
+                                        : launch_part<BITS, ROWS, kPlain, TREE>(a, prefix, own, s);
 }
 
-template <int BITS>
+template <int BITS, bool TREE>
 hipError_t launch_bits(const KvAttnArgs& a, const Plan& p, hipStream_t s) {
-    hipError_t e = launch_rows<BITS, 256>(a, p.prefix, p.own, s);
-    if (e == hipSuccess) e = launch_rows<BITS, 128>(a, p.prefix, p.own, s);
-    if (e == hipSuccess) e = launch_rows<BITS, kRows>(a, p.prefix, p.own, s);
+    hipError_t e = launch_rows<BITS, 256, TREE>(a, p.prefix, p.own, s);
+    if (e == hipSuccess) e = launch_rows<BITS, 128, TREE>(a, p.prefix, p.own, s);
+    if (e == hipSuccess) e = launch_rows<BITS, kRows, TREE>(a, p.prefix, p.own, s);
     return e;
 }
 
@@ -1405,7 +1362,8 @@ bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len) {
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s) {
     const Plan p = plan(a.T, a.Hq, a.Hkv, a.B, a.max_pages << a.page_log2, a.prefix_len);
-    const hipError_t e = bits == 8 ? launch_bits<8>(a, p, s) : launch_bits<4>(a, p, s);
+    const hipError_t e = a.tree ? (bits == 8 ? launch_bits<8, true>(a, p, s) : launch_bits<4, true>(a, p, s))
+                                : (bits == 8 ? launch_bits<8, false>(a, p, s) : launch_bits<4, false>(a, p, s));
     // where a prefix has an earlier launch and the sequences' own tokens one share of 16 rows, that joins what both give
     if (e != hipSuccess || p.splits == 1 || (p.own.rows == kRows && p.own.splits == 1 && p.prefix.rows > kRows)) return e;
     const long long rows = static_cast<long long>(a.T) * a.Hq;

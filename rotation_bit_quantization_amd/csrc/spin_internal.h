@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "libspin.h"
+
 namespace spin {
 
 // Hadamard order n = 2^log2p * (has12 ? 12 : 1).
@@ -52,6 +54,7 @@ struct KvAppendArgs {
     int rope_len, rot_dim;
     bool interleaved;
     int pos0, B;
+    const int32_t* positions;      // [T]: in place of pos0 + place, or NULL
     const int32_t* q_start;
     const int32_t* kv_len;
     const int32_t* page_table;
@@ -88,13 +91,85 @@ struct KvAttnArgs {
     int window;
     bool causal;
     const int32_t* bidir_len;
+    const uint32_t* tree;          // [T][tree_words], NULL: new tokens see each other by `causal`, which is false with a tree
+    int tree_words;
+    const int32_t* positions;      // [T], read with a tree; NULL: no window, no slopes
     uint16_t* O;
+    float* lse;                    // [T][Hq] or NULL
     float* partial;                // the workspace
 };
 // Bytes of workspace the launch needs (0: none), and whether it fits one launch.
 size_t kv_attn_workspace(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len);
 bool kv_attn_fits(int T, int Hq, int Hkv, int B, int max_kv, int prefix_len);
 hipError_t launch_kv_attn(const KvAttnArgs& a, int bits, hipStream_t s);
+
+// Ancestors and positions of drafted tokens.
+struct KvTreeArgs {
+    const int32_t* parent;
+    int T, B;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    int pos0, words;
+    uint32_t* tree;
+    int32_t* positions;
+};
+hipError_t launch_kv_tree(const KvTreeArgs& a, hipStream_t s);
+
+// Attention weight of cached tokens.
+struct KvWeightsArgs {
+    const uint16_t* Q;
+    const float* lse;
+    int T, Hq, Hkv;
+    const uint8_t* K_codes;
+    const uint16_t* K_scale;
+    int n_pages, page_log2, B;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int max_pages, pos0;
+    float scale, softcap;
+    const float* slopes;
+    int window;
+    bool causal;
+    const int32_t* bidir_len;
+    const float* prior;            // NULL: none
+    float decay;
+    float* W;
+};
+bool kv_weights_fits(int T, int Hq, int Hkv, int B, int max_kv);
+hipError_t launch_kv_weights(const KvWeightsArgs& a, int bits, hipStream_t s);
+
+// The tokens of greatest weight.
+struct KvChooseArgs {
+    const float* W;
+    int Hkv, n_pages, page_log2, B;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int max_pages, keep, first, recent;
+    int32_t* kept;
+    int32_t* lens;
+};
+bool kv_choose_fits(int Hkv, int B);
+hipError_t launch_kv_choose(const KvChooseArgs& a, hipStream_t s);
+
+// Tokens to other slots of the cache.
+struct KvMoveArgs {
+    uint8_t* K_codes;
+    uint16_t* K_scale;
+    uint8_t* V_codes;
+    uint16_t* V_scale;
+    float* W;                      // or NULL
+    int Hkv, n_pages, page_log2, B;
+    const int32_t* page_table;
+    int max_pages;
+    const int32_t* kept;
+    int kept_heads, n;             // 1 or Hkv
+    const int32_t* at;             // or NULL: 0
+    const int32_t* to_table;       // NULL: page_table, in place
+    int to_pages;
+};
+bool kv_move_fits(int Hkv, int B, int n);
+hipError_t launch_kv_move(const KvMoveArgs& a, int bits, hipStream_t s);
 
 // The FP6 matrix-core path of launch_w4a4_gemm (exact for K <= kGemmFp6MaxK).
 constexpr int kGemmFp6MaxK = 65536;

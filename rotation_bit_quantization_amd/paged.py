@@ -1,0 +1,154 @@
+"""Binding of the libspin calls around a paged cache's steps: trees of drafted tokens (ancestors, attention, the accepted
+path's move) and eviction (the weight that tokens draw, the choice of those that stay, their move).
+
+They are reached as spin.spin_kv_tree and so on, and are made as the calls in spin.py are: checks of the tensors, outputs
+on the stream of the call, the C entry of the same name (spin_kv_attn_ex for spin_kv_attn_tree).
+
+Declarations and contracts: include/libspin.h.
+"""
+
+import torch
+
+from .spin import _attn, _batch, _cache, _gpu, _int, _launch, _on_stream, _prefix, _want
+
+__all__ = ["spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_choose", "spin_kv_move"]
+
+
+def spin_kv_tree(parent, q_start, kv_len, words, pos0=0, tree=None, positions=None, stream=None):
+    """parent [T] int32 (of each new token of a sequence, the number of the one before it, -1: the context's last)
+    -> (tree [T, words] int32: bits of each token's ancestors and itself, positions [T] int32)."""
+    if stream is not None:
+        return _on_stream(stream, parent, spin_kv_tree, parent, q_start, kv_len, words, pos0, tree, positions)
+    dev = _gpu(parent, "parent")
+    if parent.dim() != 1 or kv_len.dim() != 1:
+        raise ValueError(f"parent and kv_len have shapes {tuple(parent.shape)} and {tuple(kv_len.shape)}, expected [T] and [B]")
+    T, B, words = _int(parent.shape[0], "T"), _int(kv_len.shape[0], "B"), _int(words, "words")
+    p = _want(parent, "parent", torch.int32, (T,), dev)
+    starts = _want(q_start, "q_start", torch.int32, (B + 1,), dev)
+    lens = _want(kv_len, "kv_len", torch.int32, (B,), dev)
+    if words < 1:
+        raise ValueError(f"words is {words}, expected 1 or more")
+    if tree is None:
+        tree = parent.new_empty((T, words))
+    if positions is None:
+        positions = parent.new_empty((T,))
+    out = _want(tree, "tree", torch.int32, (T, words), dev)
+    at = _want(positions, "positions", torch.int32, (T,), dev)
+    if T != 0 and B != 0:           # an empty tensor has no address to pass
+        _launch("spin_kv_tree", dev, (p, T, B, starts, lens, _int(pos0, "pos0"), words, out, at))
+    return tree, positions
+
+
+def spin_kv_attn_tree(Q, cache, page_table, q_start, kv_len, tree, positions=None, scale=None, softcap=0.0, slopes=None,
+                      window=0, prefix_table=None, prefix_len=0, O=None, workspace=None, stream=None, lse=None):
+    """spin_kv_attn (spin_kv_attn_shared behind a prefix) where ``tree`` [T, words] int32 says which of its sequence's
+    new tokens a row sees beside the context, as spin_kv_tree writes it; ``positions`` [T] int32 are needed with a
+    window or slopes."""
+    if stream is not None:
+        return _on_stream(stream, Q, spin_kv_attn_tree, Q, cache, page_table, q_start, kv_len, tree, positions, scale,
+                          softcap, slopes, window, prefix_table, prefix_len, O, workspace, lse=lse)
+    if tree is None:
+        raise TypeError("tree must be a torch.Tensor")
+    if prefix_table is None and prefix_len:
+        raise ValueError("prefix_len without prefix_table")
+    prefix = None if prefix_table is None else _prefix(prefix_table, prefix_len, cache)
+    return _attn("spin_kv_attn_ex", Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slopes, window, False, None,
+                 O, workspace, lse, tree, positions)
+
+
+def _weights(W, name, cache, dev):
+    """Check an fp32 tensor of the cache's slots; returns its address."""
+    return _want(W, name, torch.float32, cache["K_scale"].shape, dev)
+
+
+def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, softcap=0.0, slopes=None, window=0, causal=True,
+                    bidir_len=None, pos0=0, prior=None, decay=1.0, W=None, stream=None):
+    """Q [T, Hq, 128] fp16 and lse [T, Hq] fp32 (from spin_kv_attn, with the same scores and masks) -> W [n_pages, Hkv,
+    page_size] fp32: at each cached token's slot decay * prior + the attention weight it draws from the rows.
+
+    W is made, of zeros, if it is not given; it may be ``prior``."""
+    if stream is not None:
+        return _on_stream(stream, Q, spin_kv_weights, Q, lse, cache, page_table, q_start, kv_len, scale, softcap, slopes,
+                          window, causal, bidir_len, pos0, prior, decay, W)
+    dev = _gpu(Q, "Q")
+    (kc, ks, _, _), n_pages, Hkv, page, bits = _cache(cache, dev)
+    (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
+    shape = Q.shape
+    if len(shape) != 3 or shape[2] != 128:
+        raise ValueError(f"Q has shape {tuple(shape)}, expected [T, Hq, 128]")
+    T, Hq, _ = shape
+    q = _want(Q, "Q", torch.float16, shape, dev)
+    log = _want(lse, "lse", torch.float32, (T, Hq), dev)
+    slope = None if slopes is None else _want(slopes, "slopes", torch.float32, (Hq,), dev)
+    both = None if bidir_len is None else _want(bidir_len, "bidir_len", torch.int32, (B,), dev)
+    old = None if prior is None else _weights(prior, "prior", cache, dev)
+    if W is None:
+        W = torch.zeros(cache["K_scale"].shape, dtype=torch.float32, device=Q.device)
+    out = _weights(W, "W", cache, dev)
+    if B != 0:                      # an empty tensor has no address to pass; no rows are no weights
+        if T == 0:
+            q = log = starts
+        _launch("spin_kv_weights", dev,
+                (q, log, T, Hq, Hkv, 128, bits, kc, ks, n_pages, page, B, starts, lens, table, max_pages, _int(pos0, "pos0"),
+                 0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both,
+                 old, decay, out))
+    return W
+
+
+def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, lens=None, stream=None):
+    """W [n_pages, Hkv, page_size] fp32 -> (kept [B, Hkv, keep] int32: the places of the tokens that stay, ascending, -1
+    behind them, lens [B] int32): per sequence and head its first ``first`` and last ``recent`` tokens and those of
+    greatest weight."""
+    if stream is not None:
+        return _on_stream(stream, W, spin_kv_choose, W, page_table, kv_len, keep, first, recent, kept, lens)
+    dev = _gpu(W, "W")
+    if W.dim() != 3 or page_table.dim() != 2:
+        raise ValueError(f"W and page_table have shapes {tuple(W.shape)} and {tuple(page_table.shape)}, expected [n_pages, Hkv, page_size] "
+                         "and [B, max_pages]")
+    n_pages, Hkv, page = W.shape
+    B, max_pages = page_table.shape
+    w = _want(W, "W", torch.float32, W.shape, dev)
+    table = _want(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    length = _want(kv_len, "kv_len", torch.int32, (B,), dev)
+    keep = _int(keep, "keep")
+    if keep < 1:
+        raise ValueError(f"keep is {keep}, expected 1 or more")
+    if kept is None:
+        kept = page_table.new_empty((B, Hkv, keep))
+    if lens is None:
+        lens = page_table.new_empty((B,))
+    out = _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
+    left = _want(lens, "lens", torch.int32, (B,), dev)
+    if B != 0:                      # an empty tensor has no address to pass
+        _launch("spin_kv_choose", dev, (w, Hkv, n_pages, page, _int(B, "B"), length, table, _int(max_pages, "max_pages"), keep,
+                                        _int(first, "first"), _int(recent, "recent"), out, left))
+    return kept, lens
+
+
+def spin_kv_move(cache, page_table, kept, at=None, to_table=None, W=None, stream=None):
+    """The tokens at places ``at`` + ``kept`` [B, 1 or Hkv, n] int32 of each sequence go to places ``at`` + 0, 1, .. of its
+    pages, or of those that ``to_table`` names, with their weights ``W`` if given; entries below 0 are passed over.
+    Returns ``cache``."""
+    if stream is not None:
+        return _on_stream(stream, kept, spin_kv_move, cache, page_table, kept, at, to_table, W)
+    dev = _gpu(kept, "kept")
+    addresses, n_pages, Hkv, page, bits = _cache(cache, dev)
+    if kept.dim() != 3 or page_table.dim() != 2 or kept.shape[1] not in (1, Hkv):
+        raise ValueError(f"kept and page_table have shapes {tuple(kept.shape)} and {tuple(page_table.shape)}, expected [B, 1 or {Hkv}, n] "
+                         "and [B, max_pages]")
+    B, max_pages = page_table.shape
+    heads, n = kept.shape[1:]
+    table = _want(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    rows = _want(kept, "kept", torch.int32, (B, heads, n), dev)
+    start = None if at is None else _want(at, "at", torch.int32, (B,), dev)
+    to, to_pages = None, 0
+    if to_table is not None:
+        if to_table.dim() != 2:
+            raise ValueError(f"to_table has shape {tuple(to_table.shape)}, expected [B, pages]")
+        to_pages = _int(to_table.shape[1], "to_table's pages")
+        to = _want(to_table, "to_table", torch.int32, (B, to_pages), dev)
+    w = None if W is None else _weights(W, "W", cache, dev)
+    if B != 0 and n != 0 and not (to_table is not None and to_pages == 0):      # an empty tensor has no address to pass
+        _launch("spin_kv_move", dev, (*addresses, w, Hkv, 128, bits, n_pages, page, _int(B, "B"), table, _int(max_pages, "max_pages"), rows,
+                                      heads, _int(n, "n"), start, to, to_pages))
+    return cache

@@ -23,7 +23,8 @@ __all__ = ["SpinError", "load", "library_path", "SPIN_OK", "SPIN_ERR_NULL",
            "spin_w4a4_gemm", "spin_kv_quant", "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8",
            "spin_kv_qkv", "spin_fwht_quant_gemm", "spin_fwht_quant_gemm_noalloc", "spin_fwht_quant_f6", "spin_w4a4_gemm_f6",
            "spin_codes_f6", "spin_w4a4_gemm_f6f6", "f6_bytes", "kv_cache", "spin_rope_table", "spin_kv_append",
-           "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace", "SPIN_GEMM_AUTO", "SPIN_GEMM_INT8", "SPIN_GEMM_FP6", "SPIN_GEMM_FP6_SPLITK",
+           "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace", "spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights",
+           "spin_kv_choose", "spin_kv_move", "SPIN_GEMM_AUTO", "SPIN_GEMM_INT8", "SPIN_GEMM_FP6", "SPIN_GEMM_FP6_SPLITK",
            "EXPORTED_SYMBOLS"]
 
 SPIN_OK, SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE, SPIN_ERR_MISALIGNED, SPIN_ERR_UNSUPPORTED, \
@@ -36,7 +37,8 @@ EXPORTED_SYMBOLS = ("spin_fold_rotation", "spin_fwht_quant", "spin_w4a4_gemm", "
                     "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8", "spin_kv_qkv", "spin_w4a4_gemm_ex",
                     "spin_fwht_quant_gemm", "spin_fwht_quant_gemm_noalloc", "spin_fwht_quant_f6",
                     "spin_w4a4_gemm_f6", "spin_codes_f6", "spin_w4a4_gemm_f6f6", "spin_rope_table", "spin_kv_append",
-                    "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace",
+                    "spin_kv_append_at", "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_ex", "spin_kv_attn_workspace",
+                    "spin_kv_tree", "spin_kv_weights", "spin_kv_choose", "spin_kv_move",
                     "spin_status_string", "spin_version")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -86,12 +88,20 @@ def load():
     lib.spin_rope_table.argtypes = [vp, i, i, i, d, vp, vp]
     lib.spin_kv_append.argtypes = [vp, vp, vp, i, i, i, i, i, q, q, q, vp, vp, f, vp, i, i, i, i, i, vp, vp, vp, vp, i, i,
                                    i, vp, vp, vp, i, vp, vp]
+    at = list(lib.spin_kv_append.argtypes)
+    lib.spin_kv_append_at.argtypes = at[:18] + [vp] + at[19:]
     cache = [vp, i, i, i, i, i, vp, vp, vp, vp, i, i]
     mask = [f, f, vp, i, i, vp, vp, vp, z, vp]
     lib.spin_kv_attn.argtypes = cache + [i, vp, vp, vp, i] + mask
     lib.spin_kv_attn_shared.argtypes = cache + [vp, i, i, vp, vp, vp, i] + mask
+    lib.spin_kv_attn_ex.argtypes = cache + [vp, i, i, vp, vp, vp, i] + mask[:6] + [vp, i, vp, vp, vp] + mask[7:]
+    lib.spin_kv_tree.argtypes = [vp, i, i, vp, vp, i, i, vp, vp, vp]
+    lib.spin_kv_weights.argtypes = [vp, vp, i, i, i, i, i, vp, vp, i, i, i, vp, vp, vp, i, i] + mask[:6] + [vp, f, vp, vp]
+    lib.spin_kv_choose.argtypes = [vp, i, i, i, i, vp, vp, i, i, i, i, vp, vp, vp]
+    lib.spin_kv_move.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, i, vp, i, i, vp, vp, i, vp]
     lib.spin_kv_attn_workspace.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(z)]
-    for name in ("spin_rope_table", "spin_kv_append", "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_workspace"):
+    for name in ("spin_rope_table", "spin_kv_append", "spin_kv_append_at", "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_ex",
+                 "spin_kv_attn_workspace", "spin_kv_tree", "spin_kv_weights", "spin_kv_choose", "spin_kv_move"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("spin_fold_rotation", "spin_fwht_quant", "spin_w4a4_gemm", "spin_kv_quant",
                  "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8", "spin_kv_qkv", "spin_w4a4_gemm_ex", "spin_fwht_quant_gemm",
@@ -702,14 +712,15 @@ def spin_rope_table(inv_freq, n_pos, pos0=0, attn_scale=1.0, table=None, stream=
 
 
 def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, interleaved=False, q_norm=None, k_norm=None,
-                   eps=1e-6, pos0=0, Q_out=None, stream=None):
+                   eps=1e-6, pos0=0, Q_out=None, stream=None, positions=None):
     """Rows of qkv_proj (Q [T, Hq, 128] or None, K and V [T, Hkv, 128], fp16 / fp32, views of one product are
     fine) -> Q_out [T, Hq, 128] fp16 (or None); the codes of K and V go into the pages of ``cache``.
 
-    ``rope`` is a spin_rope_table of the rotated part of a head; ``q_norm`` and ``k_norm`` are [128] fp32 weights."""
+    ``rope`` is a spin_rope_table of the rotated part of a head; ``q_norm`` and ``k_norm`` are [128] fp32 weights.
+    ``positions`` [T] int32 (spin_kv_append_at): the rows of ``rope``, in place of pos0 + place."""
     if stream is not None:
         return _on_stream(stream, K, spin_kv_append, Q, K, V, cache, page_table, q_start, kv_len, rope,
-                          interleaved, q_norm, k_norm, eps, pos0, Q_out)
+                          interleaved, q_norm, k_norm, eps, pos0, Q_out, positions=positions)
     dev = _gpu(K, "K")
     (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
@@ -739,10 +750,15 @@ def spin_kv_append(Q, K, V, cache, page_table, q_start, kv_len, rope=None, inter
             raise ValueError(f"rope has shape {tuple(rope.shape)}, expected [positions, rotated values]")
         rope_len, rot_dim = _int(rope.shape[0], "positions"), _int(rope.shape[1], "rotated values")
         rows = _want(rope, "rope", torch.float32, rope.shape, dev)
+    fn, turn = "spin_kv_append", _int(pos0, "pos0")
+    if positions is not None:
+        if turn != 0:
+            raise ValueError("pos0 goes with places, not with positions")
+        fn, turn = "spin_kv_append_at", _want(positions, "positions", torch.int32, (T,), dev)
     if T != 0 and B != 0:           # an empty tensor has no address to pass
-        _launch("spin_kv_append", dev,
+        _launch(fn, dev,
                 (q, k, v, SPIN_F16 if dtype is torch.float16 else SPIN_F32, T, Hq, Hkv, 128, q_stride, k_stride, v_stride, qn,
-                 kn, eps, rows, rope_len, rot_dim, _int(interleaved, "interleaved"), _int(pos0, "pos0"), bits, kc, ks, vc, vs, n_pages, page, B, starts,
+                 kn, eps, rows, rope_len, rot_dim, _int(interleaved, "interleaved"), turn, bits, kc, ks, vc, vs, n_pages, page, B, starts,
                  lens, table, max_pages, out))
     return Q_out
 
@@ -759,7 +775,7 @@ def spin_kv_attn_workspace(T, Hq, Hkv, B, max_pages, page_size, prefix_len=0):
 
 
 def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O,
-          workspace):
+          workspace, lse=None, tree=None, positions=None):
     dev = _gpu(Q, "Q")
     (kc, ks, vc, vs), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
@@ -774,6 +790,18 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
     if prefix is not None:
         prefix_len = prefix[1]
         front = (_want(prefix[0], "prefix_table", torch.int32, prefix[0].shape, dev) or None, prefix_len)
+    more = ()
+    if lse is not None or tree is not None:
+        fn, words, bits_of, at = "spin_kv_attn_ex", 0, None, None
+        front = front or (None, 0)
+        if tree is not None:
+            if tree.dim() != 2:
+                raise ValueError(f"tree has shape {tuple(tree.shape)}, expected [T, words]")
+            words = tree.shape[1]
+            bits_of = _want(tree, "tree", torch.int32, (T, words), dev)
+            at = None if positions is None else _want(positions, "positions", torch.int32, (T,), dev)
+        more = (bits_of, words, at)
+        log = None if lse is None else _want(lse, "lse", torch.float32, (T, Hq), dev)
     if O is None:
         O = torch.empty_like(Q)
         out = O.data_ptr()
@@ -791,32 +819,53 @@ def _attn(fn, Q, cache, prefix, page_table, q_start, kv_len, scale, softcap, slo
         ws, ws_bytes = workspace.data_ptr(), need
     _launch(fn, dev,
             (q, T, Hq, Hkv, 128, bits, kc, ks, vc, vs, n_pages, page, *front, B, starts, lens, table, max_pages,
-             0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both, out, ws, ws_bytes))
+             0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both, *more,
+             *((out, log) if more else (out,)), ws, ws_bytes))
     return O
 
 
 def spin_kv_attn(Q, cache, page_table, q_start, kv_len, scale=None, softcap=0.0, slopes=None, window=0, causal=True,
-                 bidir_len=None, O=None, workspace=None, stream=None):
+                 bidir_len=None, O=None, workspace=None, stream=None, lse=None):
     """Q [T, Hq, 128] fp16 (from spin_kv_append) over the pages of each sequence -> O [T, Hq, 128] fp16.
 
     ``scale`` is 1 / sqrt(128) by default.  ``workspace`` (uint8, spin_kv_attn_workspace bytes) is allocated if
-    it is not given."""
+    it is not given.  ``lse`` [T, Hq] fp32, if given, takes the logarithms of the rows' sums (spin_kv_weights)."""
     if stream is not None:
         return _on_stream(stream, Q, spin_kv_attn, Q, cache, page_table, q_start, kv_len, scale, softcap,
-                          slopes, window, causal, bidir_len, O, workspace)
+                          slopes, window, causal, bidir_len, O, workspace, lse=lse)
     return _attn("spin_kv_attn", Q, cache, None, page_table, q_start, kv_len, scale, softcap, slopes, window, causal,
-                 bidir_len, O, workspace)
+                 bidir_len, O, workspace, lse)
+
+
+def _prefix(prefix_table, prefix_len, cache):
+    """A prefix's table and length, checked against each other."""
+    prefix_len = _int(prefix_len, "prefix_len")
+    if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-prefix_len // cache["K_codes"].shape[2]):
+        raise ValueError(f"prefix_table has shape {tuple(prefix_table.shape)}, too few pages for {prefix_len} tokens")
+    return prefix_table, prefix_len
 
 
 def spin_kv_attn_shared(Q, cache, prefix_table, prefix_len, page_table, q_start, kv_len, scale=None, softcap=0.0,
-                        slopes=None, window=0, causal=True, bidir_len=None, O=None, workspace=None, stream=None):
+                        slopes=None, window=0, causal=True, bidir_len=None, O=None, workspace=None, stream=None, lse=None):
     """spin_kv_attn where the first ``prefix_len`` tokens of every sequence lie in the pages ``prefix_table``
     names ([ceil(prefix_len / page_size)] int32) and ``page_table`` and ``kv_len`` count what follows."""
     if stream is not None:
         return _on_stream(stream, Q, spin_kv_attn_shared, Q, cache, prefix_table, prefix_len, page_table,
-                          q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O, workspace)
-    prefix_len = _int(prefix_len, "prefix_len")
-    if prefix_table.dim() != 1 or prefix_table.shape[0] < -(-prefix_len // cache["K_codes"].shape[2]):
-        raise ValueError(f"prefix_table has shape {tuple(prefix_table.shape)}, too few pages for {prefix_len} tokens")
-    return _attn("spin_kv_attn_shared", Q, cache, (prefix_table, prefix_len), page_table, q_start, kv_len, scale,
-                 softcap, slopes, window, causal, bidir_len, O, workspace)
+                          q_start, kv_len, scale, softcap, slopes, window, causal, bidir_len, O, workspace, lse=lse)
+    return _attn("spin_kv_attn_shared", Q, cache, _prefix(prefix_table, prefix_len, cache), page_table, q_start, kv_len, scale,
+                 softcap, slopes, window, causal, bidir_len, O, workspace, lse)
+
+
+# Calls of the paged cache beyond a step, which live in paged.py.
+_PAGED = frozenset(("spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_choose", "spin_kv_move"))
+
+
+def __getattr__(name):
+    if name in _PAGED:
+        from . import paged
+        return getattr(paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_PAGED})

@@ -1,0 +1,310 @@
+"""Drafted trees on the paged cache: ancestors and positions, the append by positions, attention over context and tree on
+every kernel, and the logarithm of the rows' sums.  Reference and bounds: the float64 oracle, element by element, within the
+roundings that it counts."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from rotation_bit_quantization_amd import spin
+
+from .paged_case import DEV, close, dev, host, pool, starts, tables
+from .test_gpu_kv_append import frequencies
+from .test_gpu_kv_attn_tiles import widened
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    spin.load()
+
+
+def drafts(rng, q_len, before=0, behind=0):
+    """Parents of random trees; what stands in rows of no sequence means nothing."""
+    rows = [np.minimum((rng.random(n) * (np.arange(n) + 1)).astype(int), np.arange(n)) - 1 for n in q_len]
+    return np.concatenate([np.full(before, 5), *rows, np.full(behind, 3)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("q_len,words", [([1], 1), ([0, 3, 0], 1), ([32, 33, 64], 3), ([70, 1, 200, 0, 13], 7), ([40, 100], 2),
+                                         ([600, 513], 17), ([4096, 4097, 5], 128), ([1] * 300, 1), ([3, 0] * 40, 1)])
+def test_ancestors_and_positions(q_len, words):
+    rng = np.random.default_rng(sum(q_len) + words)
+    parent = drafts(rng, q_len, 2, 3)
+    q_start, kv_len = starts(q_len, 2), np.array([n + (7 * i) % 900 for i, n in enumerate(q_len)], np.int32)
+    T = len(parent)
+    tree, at = torch.full((T, words), 77, dtype=torch.int32, device=DEV), torch.full((T,), 77, dtype=torch.int32, device=DEV)
+    spin.spin_kv_tree(dev(parent), dev(q_start), dev(kv_len), words, pos0=11, tree=tree, positions=at)
+    ref, where = oracle.kv_tree(parent, q_start, kv_len, words, 11)
+    inside = slice(2, T - 3)
+    assert np.array_equal(host(tree).view(np.uint32)[inside], ref[inside]) and np.array_equal(host(at)[inside], where[inside])
+    assert (np.delete(host(tree), np.arange(2, T - 3), 0) == 77).all() and (np.delete(host(at), np.arange(2, T - 3)) == 77).all()
+
+
+def test_parents_that_are_none():
+    """Forward references, the token itself and numbers beyond the batch follow the context; so the walk ends."""
+    parent = np.array([0, 1, -7, 5, 2 ** 31 - 1, -2 ** 31, 1, 6], np.int32)
+    q_start, kv_len = starts([8]), np.array([3], np.int32)          # fewer tokens than rows
+    tree, at = spin.spin_kv_tree(dev(parent), dev(q_start), dev(kv_len), 1)
+    ref, where = oracle.kv_tree(parent, q_start, kv_len, 1)
+    assert np.array_equal(host(tree).view(np.uint32), ref) and np.array_equal(host(at), where)
+    assert ref[7, 0] == 0b11000010 and where.tolist() == [-5, -5, -5, -5, -5, -5, -4, -3]
+
+
+def test_a_chain_of_the_longest():
+    n = 4096
+    tree, at = spin.spin_kv_tree(dev(np.arange(-1, n - 1, dtype=np.int32)), dev(starts([n])), dev(np.array([n + 9], np.int32)), 128)
+    want = np.tril(np.ones((n, n), bool))
+    assert np.array_equal(np.unpackbits(host(tree).view(np.uint8), axis=1, bitorder="little").astype(bool), want)
+    assert np.array_equal(host(at), np.arange(9, n + 9))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("rot,inter", [(128, False), (64, True), (0, False)])
+def test_append_by_positions(bits, dtype, rot, inter):
+    rng = np.random.default_rng(bits + rot)
+    q_len, kv_len, Hq, Hkv, page = [5, 0, 33, 2], [20, 7, 33, 90], 4, 2, 16
+    q_start, T = starts(q_len, 1), 43
+    x = rng.standard_normal((T, Hq + 2 * Hkv, 128)).astype(dtype)
+    cache = pool(rng, 14, Hkv, page, bits)
+    table = tables(rng, kv_len, page, 14)
+    _, at = oracle.kv_tree(drafts(rng, q_len, 1, 2), q_start, kv_len, 2)
+    at[[2, 8, 39]] = -1, 200, 199                                  # none in the table, none, the last
+    rope = oracle.rope_table(frequencies(rot), 200).astype(np.float32) if rot else None
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    ref, q_ref = oracle.kv_append(q, k, v, cache, table, q_start, kv_len, rope=rope, interleaved=inter, positions=at)
+    cd, out = dev(cache), torch.full((T, Hq, 128), 77.0, dtype=torch.float16, device=DEV)
+    d = dev(x)
+    spin.spin_kv_append(d[:, :Hq], d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], cd, dev(table), dev(q_start), dev(np.array(kv_len, np.int32)),
+                        rope=dev(rope), interleaved=inter, positions=dev(at), Q_out=out)
+    for name in ref:
+        assert np.array_equal(host(cd[name]).view(np.uint8), ref[name].view(np.uint8)), name
+    got, silent = host(out).astype(np.float64), np.isnan(q_ref)
+    assert (got[silent] == 77.0).all()
+    # float32 sums of 128 values and a rotation: 16 roundings of 2^-24 of the norm; to fp16 half a step
+    y = np.where(silent, 0, q_ref)
+    norm = np.linalg.norm(np.asarray(x[:, :Hq], np.float64), axis=-1, keepdims=True)
+    assert (np.abs(np.where(silent, 0, got) - y) <= 2.0 ** -11 * np.abs(y) + 2.0 ** -20 * norm + 2.0 ** -25).all()
+
+
+def test_places_as_positions_are_the_plain_append():
+    rng = np.random.default_rng(3)
+    q_len, kv_len = [7, 1, 40], [30, 1, 41]
+    x, cache, table = rng.standard_normal((48, 8, 128)).astype(np.float32), pool(rng, 9, 2, 16, 4), tables(rng, kv_len, 16, 9)
+    at = np.concatenate([np.arange(kv - n, kv) for n, kv in zip(q_len, kv_len)]).astype(np.int32)
+    d, rope = dev(x), spin.spin_rope_table(dev(frequencies(128)), 60)
+    outs = []
+    for more in (dict(), dict(positions=dev(at))):
+        c = dev(cache)
+        Q = spin.spin_kv_append(d[:, :4], d[:, 4:6], d[:, 6:], c, dev(table), dev(starts(q_len)), dev(np.array(kv_len, np.int32)), rope=rope, **more)
+        outs.append([host(Q), *(host(t) for t in c.values())])
+    assert all(np.array_equal(a.view(np.uint8), b.view(np.uint8)) for a, b in zip(*outs))
+
+
+def run(q, cache, table, q_start, kv_len, tree, positions, prefix=None, prefix_len=0, want_lse=True, **more):
+    O = torch.full(q.shape, 77.0, dtype=torch.float16, device=DEV)
+    lse = torch.full(q.shape[:2], 77.0, device=DEV) if want_lse else None
+    more = {k: dev(v) if isinstance(v, np.ndarray) else v for k, v in more.items()}
+    spin.spin_kv_attn_tree(dev(q), dev(cache), dev(table), dev(np.asarray(q_start, np.int32)), dev(np.asarray(kv_len, np.int32)),
+                           dev(tree.view(np.int32)), positions=dev(positions), prefix_table=dev(prefix), prefix_len=prefix_len, O=O,
+                           lse=lse, **more)
+    return host(O).astype(np.float64), host(lse).astype(np.float64) if want_lse else None
+
+
+def close_logs(got, ref, bound):
+    silent = np.isnan(ref)
+    assert (got[silent] == 77.0).all()
+    none = ref == -np.inf
+    assert (got[none] == -np.inf).all()
+    fine = ~silent & ~none
+    assert (np.abs(got - np.where(fine, ref, 0))[fine] <= bound[fine]).all()
+
+
+def check(rng, q_len, kv_len, Hq, Hkv, bits, page, work=0, before=0, behind=0, prefix_len=0, tree=None, positions=True, most=10 ** 9,
+          extra_words=0, cache=None, table=None, **more):
+    q_start = starts(q_len, before)
+    T = before + int(sum(q_len)) + behind
+    q = (1.5 * rng.standard_normal((T, Hq, 128))).astype(np.float16)
+    first = -(-prefix_len // page)
+    n_pages = first + sum(-(-max(n, 0) // page) for n in kv_len) + 2
+    cache = pool(rng, n_pages, Hkv, page, bits) if cache is None else cache
+    table = tables(rng, kv_len, page, n_pages, first=first) if table is None else table
+    table = widened(table, T * Hq // Hkv, Hkv, page, work)
+    words = max(-(-max(q_len) // 32), 1) + extra_words
+    drawn, at = oracle.kv_tree(drafts(rng, q_len, before, behind), q_start, kv_len, words, prefix_len)
+    tree = drawn if tree is None else tree
+    at = at if positions else None
+    if more.pop("alibi", False):
+        more["slopes"] = (2.0 ** (-8 * np.arange(1, Hq + 1) / Hq)).astype(np.float32)
+    prefix = rng.permutation(first).astype(np.int32) if prefix_len else None
+    rows = list(range(before, T - behind))
+    if len(rows) > most:
+        rows = sorted(rng.choice(rows, most, replace=False).tolist())
+    ref, bound, logs, log_bound = oracle.kv_attend(q, cache, table, q_start, kv_len, 128 ** -0.5, rows=set(rows), tree=tree, positions=at,
+                                                   prefix_table=prefix, prefix_len=prefix_len, sums=True, **more)
+    got, lse = run(q, cache, table, q_start, kv_len, tree, at, prefix, prefix_len, **more)
+    rows = [*range(before), *rows, *range(T - behind, T)]
+    close(got[rows], ref[rows], bound[rows])
+    if np.isfinite(got[rows]).all():
+        close_logs(lse[rows], logs[rows], log_bound[rows])
+    again, _ = run(q, cache, table, q_start, kv_len, tree, at, prefix, prefix_len, want_lse=False, **more)
+    assert np.array_equal(again, got, equal_nan=True)
+    return got, lse
+
+
+# rows x tokens x key heads of the tables' room: tiles of 16, of 128, of 256 rows
+WORK = [0, 2 ** 25, 2 ** 28]
+
+
+@pytest.mark.parametrize("work", WORK)
+@pytest.mark.parametrize("q_len,kv_len,Hq,Hkv,bits,page", [
+    ([1], [1], 1, 1, 4, 16),
+    ([64], [64], 2, 1, 8, 16),
+    ([70, 2], [200, 2], 8, 1, 4, 128),
+    ([131, 40, 1, 0], [300, 40, 65, 9], 8, 2, 8, 64),
+    ([37, 1, 18], [37, 80, 130], 36, 3, 4, 16),
+    ([0, 300, 0], [7, 700, 0], 5, 1, 8, 1024),
+    ([60] * 9, [60 + 77 * i for i in range(9)], 8, 2, 4, 32),
+    ([90, 0, 77], [50, 40, 70], 6, 2, 4, 16),                 # more rows than tokens: the first have no place
+])
+def test_shapes(work, q_len, kv_len, Hq, Hkv, bits, page):
+    rng = np.random.default_rng(len(q_len) * 100 + Hq + bits + page)
+    check(rng, q_len, kv_len, Hq, Hkv, bits, page, work, before=2, behind=3, most=200, extra_words=bits // 8)
+
+
+@pytest.mark.parametrize("work", WORK)
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("mask", [
+    dict(softcap=20.0),
+    dict(softcap=1e4),
+    dict(window=1),
+    dict(window=3),
+    dict(window=24),
+    dict(window=100, softcap=5.0, alibi=True),
+    dict(alibi=True),
+    dict(window=2 ** 31 - 1, positions=True),
+    dict(positions=False),
+])
+def test_masks(mask, work, bits):
+    rng = np.random.default_rng(7 + bits)
+    check(rng, [140, 150, 9], [140, 400, 30], 4, 1, bits, 64, work, most=150, **mask)
+    check(rng, [33, 0, 77], [500, 40, 170], 6, 2, bits, 16, work, most=150, **mask)
+
+
+@pytest.mark.parametrize("work", [0, 2 ** 25])
+@pytest.mark.parametrize("q_len,kv_len,Hq,Hkv,prefix,more", [
+    ([2, 1, 9], [3, 17, 60], 8, 2, 300, {}),
+    ([40, 35, 70], [40, 60, 70], 16, 8, 16000, {}),
+    ([40, 35, 70], [40, 60, 70], 16, 8, 15000, dict(window=14990, softcap=20.0)),
+    ([100, 60], [100, 90], 8, 8, 32001, dict(window=300, alibi=True)),
+    ([1] * 128, [1 + i % 37 for i in range(128)], 16, 4, 16500, {}),
+    ([120, 130, 6], [125, 130, 6], 64, 16, 8200, {}),
+])
+def test_shared_prefix(work, q_len, kv_len, Hq, Hkv, prefix, more):
+    rng = np.random.default_rng(prefix)
+    check(rng, q_len, kv_len, Hq, Hkv, 4 if prefix % 2 else 8, 64, work, before=1, behind=2, prefix_len=prefix, most=10, **more)
+
+
+@pytest.mark.parametrize("work", WORK)
+def test_rows_that_see_nothing(work):
+    """No context, and a row of zeros: zeros, and a logarithm of minus infinity; with a context they see that."""
+    rng = np.random.default_rng(5)
+    tree = np.zeros((75, 3), np.uint32)
+    tree[3] = 0xFFFFFFFF                                       # bits of tokens that are not there are of no effect
+    got, lse = check(rng, [70, 5], [70, 45], 8, 2, 4, 16, work, tree=tree)
+    assert (got[0] == 0).all() and (lse[0] == -np.inf).all() and (got[3] != 0).any() and (got[70:] != 0).any()
+
+
+@pytest.mark.parametrize("work", WORK)
+def test_any_bits(work):
+    """Masks that are no tree's, tokens behind the words that are given, and positions of any kind."""
+    rng = np.random.default_rng(6)
+    q_len, kv_len = [70, 100, 31], [90, 100, 300]
+    tree = rng.integers(0, 2 ** 32, (201, 2), dtype=np.uint32)
+    check(rng, q_len, kv_len, 4, 2, 4, 32, work, tree=tree)
+    q_start, cache, table = starts(q_len), pool(rng, 20, 2, 32, 8), tables(rng, kv_len, 32, 20)
+    table = widened(table, 402, 2, 32, work)
+    at = rng.integers(0, 400, 201).astype(np.int32)
+    q = rng.standard_normal((201, 4, 128)).astype(np.float16)
+    slopes = np.array([0.5, 0.1, 0.0, 0.02], np.float32)
+    ref, bound = oracle.kv_attend(q, cache, table, q_start, kv_len, 0.1, tree=tree, positions=at, window=90, slopes=slopes)
+    got, _ = run(q, cache, table, q_start, kv_len, tree, at, scale=0.1, window=90, slopes=slopes)
+    close(got, ref, bound)
+    wild = at.copy()
+    wild[::3] = [-2 ** 31, 2 ** 31 - 1, -1, 2 ** 30] * 16 + [5] * 3
+    held = np.clip(wild, 0, 2 ** 30)
+    for more in (dict(window=40), dict(window=2 ** 31 - 1), dict(window=90, softcap=10.0)):
+        ref, bound = oracle.kv_attend(q, cache, table, q_start, kv_len, 0.1, tree=tree, positions=held.astype(np.int64), **more)
+        got, _ = run(q, cache, table, q_start, kv_len, tree, wild, scale=0.1, **more)
+        close(got, ref, bound)
+
+
+@pytest.mark.parametrize("work", WORK)
+@pytest.mark.parametrize("which,bad", [("K_scale", np.nan), ("V_scale", np.inf), ("K_scale", -np.inf), ("V_scale", np.nan)])
+def test_scales_that_are_not_finite(work, which, bad):
+    """A drafted token's: its descendants are NaN, and their logarithms not finite; others are not touched."""
+    rng = np.random.default_rng(8)
+    q_len, kv_len, page = [70, 6], [100, 6], 16
+    cache, table = pool(rng, 12, 2, page, 4), tables(rng, kv_len, page, 12)
+    cache[which][table[0, 32 // page], 0, 0] = bad              # place 32: the third of the new tokens, one head
+    for b, k in enumerate(kv_len):
+        if k % page:
+            cache[which][table[b, k // page], :, k % page:] = bad
+    got, lse = check(rng, q_len, kv_len, 8, 2, 4, page, work, cache=cache, table=table)
+    assert np.isnan(got[2, :4]).all() and np.isfinite(got[2, 4:]).all() and np.isfinite(got[0]).all()
+    assert np.array_equal(np.isnan(got).any(2), ~np.isfinite(lse)) and np.isnan(got[:70, :4]).any(2).sum() < 4 * 70
+
+
+def test_a_page_that_is_not_there():
+    rng = np.random.default_rng(9)
+    table = tables(rng, [300, 80], 16, 30)
+    table[0, 3], table[1, 4] = -1, 1000
+    check(rng, [40, 20], [300, 80], 4, 2, 4, 16, table=table, cache=pool(rng, 30, 2, 16, 4))
+
+
+@pytest.mark.parametrize("kv", [[2 ** 31 - 1, 70], [-5, 70], [200, 0]])
+def test_lengths_past_the_table(kv):
+    """New tokens stand where their places are; those behind the table's last page have none."""
+    rng = np.random.default_rng(10)
+    table = tables(rng, [160, 80], 16, 30, extra=0)
+    check(rng, [40, 20], kv, 4, 2, 4, 16, table=table, cache=pool(rng, 30, 2, 16, 4), positions=False)
+
+
+# the paths on which a row is finished: one share, shares and a join, tiles, behind a prefix
+@pytest.mark.parametrize("q_len,kv_len,Hq,Hkv,prefix,work", [
+    ([1, 3], [50, 700], 8, 2, 0, 0),
+    ([1, 2], [2500, 6000], 6, 2, 0, 0),
+    ([130, 60], [300, 400], 4, 1, 0, 2 ** 25),
+    ([260, 33], [333, 700], 2, 1, 0, 2 ** 28),
+    ([2, 1, 9], [3, 17, 60], 8, 2, 300, 0),
+    ([1] * 128, [1 + i % 37 for i in range(128)], 16, 2, 16500, 0),
+    ([40, 35, 70], [40, 60, 70], 16, 2, 16000, 2 ** 25),
+])
+@pytest.mark.parametrize("more", [{}, dict(softcap=20.0), dict(window=30, bidir=True), dict(causal=False)])
+def test_logarithms_without_a_tree(q_len, kv_len, Hq, Hkv, prefix, work, more):
+    rng = np.random.default_rng(11)
+    page, first, T = 64, -(-prefix // 64), sum(q_len) + 3
+    n = first + sum(-(-k // page) for k in kv_len) + 1
+    cache, q = pool(rng, n, Hkv, page, 8), rng.standard_normal((T, Hq, 128)).astype(np.float16)
+    table = widened(tables(rng, kv_len, page, n, first=first), T * Hq // Hkv, Hkv, page, work)
+    q_start = starts(q_len, 1)
+    more = dict(more)
+    if more.pop("bidir", False):
+        more["bidir_len"] = np.resize(np.array([20, 0], np.int32), len(q_len))
+    args = [dev(q), dev(cache)] + ([dev(np.arange(first, dtype=np.int32)), prefix] if prefix else []) + [
+        dev(table), dev(q_start), dev(np.array(kv_len, np.int32))]
+    call = spin.spin_kv_attn_shared if prefix else spin.spin_kv_attn
+    on = {k: dev(v) if isinstance(v, np.ndarray) else v for k, v in more.items()}
+    O, lse = torch.full(q.shape, 77.0, dtype=torch.float16, device=DEV), torch.full((T, Hq), 77.0, device=DEV)
+    call(*args, O=O, lse=lse, **on)
+    plain = torch.full(q.shape, 77.0, dtype=torch.float16, device=DEV)
+    call(*args, O=plain, **on)
+    assert np.array_equal(host(O), host(plain))
+    rows = sorted({0, T - 1, T - 2, *rng.choice(T, 12).tolist()})
+    _, _, ref, bound = oracle.kv_attend(q, cache, table, q_start, kv_len, 128 ** -0.5, rows=set(rows), sums=True,
+                                        prefix_table=np.arange(first), prefix_len=prefix, **more)
+    close_logs(host(lse)[rows], ref[rows], bound[rows])
