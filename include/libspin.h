@@ -669,18 +669,27 @@ spin_status spin_kv_attn_ex(const uint16_t* Q, int T, int Hq, int Hkv, int D, in
  *            over the sequence's rows and the query heads of the key head that see
  *            the token (without prior, the sum alone).  Other slots keep what they
  *            hold.
+ *   workspace  device memory of the bytes spin_kv_weights_workspace names (it may
+ *            be NULL if that is 0); its content before and after means nothing, and
+ *            calls that overlap need one each
  * A row whose lse is not finite adds nothing, and a token whose scale is not finite
  * draws nothing.  Sums are float32, in an order that goes by the sizes alone.  A page
  * may stand in one table of the batch only.  T == 0 is valid: W = decay * prior.
- * Errors: as for spin_kv_attn (no workspace); SPIN_ERR_UNSUPPORTED for a decay that
- * is not finite, SPIN_ERR_BAD_SHAPE for more than 2^24 - 1 workgroups of 256
- * of a head's tokens.
+ * Errors: as for spin_kv_attn; SPIN_ERR_UNSUPPORTED for a decay that is not finite,
+ * SPIN_ERR_BAD_SHAPE for more than 2^24 - 1 workgroups of 128 of a head's tokens.
  */
 spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
                             const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
                             const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
                             int pos0, float scale, float softcap, const float* slopes, int window, int causal,
-                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* stream);
+                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * spin_kv_weights_workspace — bytes of workspace a spin_kv_weights call of these
+ * sizes takes (0: none).  It goes by the sizes alone.
+ */
+spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, size_t* bytes);
 
 /*
  * spin_kv_choose — which tokens of each sequence stay, per key head: those of

@@ -547,7 +547,8 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
                             const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
                             const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
                             int pos0, float scale, float softcap, const float* slopes, int window, int causal,
-                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* stream) {
+                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* workspace,
+                            size_t workspace_bytes, void* stream) {
     if (!Q || !lse || !K_codes || !K_scale || !q_start || !kv_len || !page_table || !W) return SPIN_ERR_NULL;
     if (causal != 0 && causal != 1) return SPIN_ERR_UNSUPPORTED;
     const float inf = __builtin_inff();
@@ -557,9 +558,12 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
     if (ok != SPIN_OK) return ok;
     if (T < 0 || Hq < 1 || Hq % Hkv != 0 || window < 0 || pos0 < 0 || pos0 > SPIN_KV_MAX_CONTEXT) return SPIN_ERR_BAD_SHAPE;
     if (!spin::kv_weights_fits(T, Hq, Hkv, B, max_pages * page_size)) return SPIN_ERR_BAD_SHAPE;
-    if (!aligned_all({Q, lse, K_codes, K_scale, q_start, kv_len, page_table, slopes, bidir_len, prior, W}))
+    if (!aligned_all({Q, lse, K_codes, K_scale, q_start, kv_len, page_table, slopes, bidir_len, prior, W, workspace}))
         return SPIN_ERR_MISALIGNED;
     if (B == 0) return SPIN_OK;
+    const size_t need = spin::kv_weights_workspace(T, Hq, Hkv, B, max_pages * page_size);
+    if (need > 0 && !workspace) return SPIN_ERR_NULL;
+    if (workspace_bytes < need) return SPIN_ERR_BAD_SHAPE;
     spin::KvWeightsArgs a = {};
     a.Q = Q;
     a.lse = lse;
@@ -585,7 +589,17 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
     a.prior = prior;
     a.decay = decay;
     a.W = W;
+    a.partial = static_cast<float*>(workspace);
     return from_hip(spin::launch_kv_weights(a, bits, static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, size_t* bytes) {
+    if (!bytes) return SPIN_ERR_NULL;
+    const spin_status ok = paged_ok(128, 4, Hkv, 1, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (T < 0 || Hq < 1 || Hq % Hkv != 0 || !spin::kv_weights_fits(T, Hq, Hkv, B, max_pages * page_size)) return SPIN_ERR_BAD_SHAPE;
+    *bytes = B == 0 ? 0 : spin::kv_weights_workspace(T, Hq, Hkv, B, max_pages * page_size);
+    return SPIN_OK;
 }
 
 spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, int B, const int32_t* kv_len,

@@ -135,7 +135,9 @@ struct KvWeightsArgs {
     const float* prior;            // NULL: none
     float decay;
     float* W;
+    float* partial;                // the workspace
 };
+size_t kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_kv);
 bool kv_weights_fits(int T, int Hq, int Hkv, int B, int max_kv);
 hipError_t launch_kv_weights(const KvWeightsArgs& a, int bits, hipStream_t s);
 

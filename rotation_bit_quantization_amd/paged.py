@@ -7,11 +7,14 @@ on the stream of the call, the C entry of the same name (spin_kv_attn_ex for spi
 Declarations and contracts: include/libspin.h.
 """
 
+import ctypes
+import functools
+
 import torch
 
-from .spin import _attn, _batch, _cache, _gpu, _int, _launch, _on_stream, _prefix, _want
+from .spin import _attn, _batch, _cache, _gpu, _int, _launch, _on_stream, _prefix, _raise, _want, load
 
-__all__ = ["spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_choose", "spin_kv_move"]
+__all__ = ["spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_weights_workspace", "spin_kv_choose", "spin_kv_move"]
 
 
 def spin_kv_tree(parent, q_start, kv_len, words, pos0=0, tree=None, positions=None, stream=None):
@@ -61,15 +64,26 @@ def _weights(W, name, cache, dev):
     return _want(W, name, torch.float32, cache["K_scale"].shape, dev)
 
 
+@functools.lru_cache(4096)
+def spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page_size):
+    """Bytes of workspace that spin_kv_weights takes at these sizes."""
+    for name, x in dict(T=T, Hq=Hq, Hkv=Hkv, B=B, max_pages=max_pages, page_size=page_size).items():
+        _int(x, name)
+    n = ctypes.c_size_t(0)
+    _raise("spin_kv_weights_workspace", load().spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page_size, ctypes.byref(n)))
+    return n.value
+
+
 def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, softcap=0.0, slopes=None, window=0, causal=True,
-                    bidir_len=None, pos0=0, prior=None, decay=1.0, W=None, stream=None):
+                    bidir_len=None, pos0=0, prior=None, decay=1.0, W=None, stream=None, workspace=None):
     """Q [T, Hq, 128] fp16 and lse [T, Hq] fp32 (from spin_kv_attn, with the same scores and masks) -> W [n_pages, Hkv,
     page_size] fp32: at each cached token's slot decay * prior + the attention weight it draws from the rows.
 
-    W is made, of zeros, if it is not given; it may be ``prior``."""
+    W is made, of zeros, if it is not given; it may be ``prior``.  ``workspace`` (uint8, spin_kv_weights_workspace bytes)
+    is allocated if it is not given."""
     if stream is not None:
         return _on_stream(stream, Q, spin_kv_weights, Q, lse, cache, page_table, q_start, kv_len, scale, softcap, slopes,
-                          window, causal, bidir_len, pos0, prior, decay, W)
+                          window, causal, bidir_len, pos0, prior, decay, W, workspace=workspace)
     dev = _gpu(Q, "Q")
     (kc, ks, _, _), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
@@ -88,10 +102,18 @@ def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, soft
     if B != 0:                      # an empty tensor has no address to pass; no rows are no weights
         if T == 0:
             q = log = starts
+        need = spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page)
+        ws, ws_bytes = None, 0
+        if workspace is not None:
+            ws_bytes = workspace.numel()
+            ws = _want(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
+        elif need:
+            workspace = Q.new_empty((need + 1) // 2)
+            ws, ws_bytes = workspace.data_ptr(), need
         _launch("spin_kv_weights", dev,
                 (q, log, T, Hq, Hkv, 128, bits, kc, ks, n_pages, page, B, starts, lens, table, max_pages, _int(pos0, "pos0"),
                  0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both,
-                 old, decay, out))
+                 old, decay, out, ws, ws_bytes))
     return W
 
 

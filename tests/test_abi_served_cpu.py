@@ -1,6 +1,7 @@
 """Argument validation of the calls for drafted trees and eviction, without a GPU: every error is returned before any
 device call (fake, never dereferenced pointers), also under the host sanitizers."""
 
+import ctypes
 import os
 import sys
 
@@ -74,13 +75,28 @@ def test_attention_with_more(lib):
 def test_weights(lib):
     call = caller(lib.spin_kv_weights, dict(Q=A, lse=A, T=5, Hq=32, Hkv=8, D=128, bits=4, kc=A, ks=A, n_pages=10, page=16, B=0, q_start=A,
                                             kv_len=A, table=A, max_pages=5, pos0=0, scale=0.1, cap=0.0, slopes=A, window=0, causal=1,
-                                            bidir=A, prior=A, decay=1.0, W=A, st=None))
+                                            bidir=A, prior=A, decay=1.0, W=A, ws=A, ws_bytes=1 << 30, st=None))
     assert call() == call(slopes=None, bidir=None, prior=None) == call(decay=-2.0) == spin.SPIN_OK
     refusals(call, ("Q", "lse", "kc", "ks", "q_start", "kv_len", "table", "W"),
              (dict(bits=5), dict(causal=2), dict(scale=NAN), dict(scale=INF), dict(cap=-1.0), dict(cap=INF), dict(decay=NAN), dict(decay=-INF)),
              (dict(T=-1), dict(D=64), dict(Hq=31), dict(Hq=0), dict(Hkv=0), dict(window=-1), dict(pos0=-1), dict(pos0=BIG), dict(T=BIG),
               dict(B=1 << 24), dict(B=BIG, max_pages=1 << 25), dict(Hq=1 << 17, Hkv=1 << 17)) + PAGES,
-             ("Q", "lse", "kc", "ks", "q_start", "kv_len", "table", "slopes", "bidir", "prior", "W"))
+             ("Q", "lse", "kc", "ks", "q_start", "kv_len", "table", "slopes", "bidir", "prior", "W", "ws"))
+    # many rows of few heads are dealt out in shares, which need their workspace
+    long = dict(T=4096, B=1, max_pages=256)
+    assert call(**long, ws=None) == spin.SPIN_ERR_NULL
+    assert call(**long, ws_bytes=16) == spin.SPIN_ERR_BAD_SHAPE
+
+
+def test_weights_workspace(lib):
+    n = ctypes.c_size_t(7)
+    call = caller(lib.spin_kv_weights_workspace, dict(T=4096, Hq=32, Hkv=8, B=1, max_pages=256, page=16, out=ctypes.byref(n)))
+    assert call() == spin.SPIN_OK and n.value >= 2 * 8 * 4096 * 4
+    assert call(T=1) == spin.SPIN_OK and n.value == 0
+    assert call(B=0) == spin.SPIN_OK and n.value == 0
+    assert call(out=None) == spin.SPIN_ERR_NULL
+    for bad in (dict(T=-1), dict(Hq=31), dict(Hkv=0), dict(B=-1), dict(max_pages=0), dict(page=7), dict(T=BIG), dict(B=BIG)):
+        assert call(**bad) == spin.SPIN_ERR_BAD_SHAPE, bad
 
 
 def test_choose(lib):

@@ -28,7 +28,7 @@ def weigh(q, lse, cache, table, q_start, kv_len, W, prior=None, **more):
 
 
 def check(rng, q_len, kv_len, Hq, Hkv, bits, page, before=0, behind=0, prior=False, decay=1.0, cache=None, table=None, pos0=0,
-          q=None, exact_logs=True, **more):
+          q=None, exact_logs=True, room=0, **more):
     q_start = starts(q_len, before)
     T = before + int(sum(q_len)) + behind
     q = (1.5 * rng.standard_normal((T, Hq, 128))).astype(np.float16) if q is None else q
@@ -36,6 +36,7 @@ def check(rng, q_len, kv_len, Hq, Hkv, bits, page, before=0, behind=0, prior=Fal
     cache = pool(rng, n_pages, Hkv, page, bits) if cache is None else cache
     n_pages = len(cache["K_scale"])
     table = tables(rng, kv_len, page, n_pages) if table is None else table
+    table = np.pad(table, ((0, 0), (0, max(room // page - table.shape[1], 0))), constant_values=-1)
     if more.pop("alibi", False):
         more["slopes"] = (2.0 ** (-8 * np.arange(1, Hq + 1) / Hq)).astype(np.float32)
     if more.pop("bidir", False):
@@ -99,6 +100,38 @@ def test_masks(more, bits, pos0):
     rng = np.random.default_rng(7 + bits)
     check(rng, [140, 150, 9], [140, 400, 30], 4, 1, bits, 64, pos0=pos0, **more)
     check(rng, [1, 90, 0, 77], [333, 500, 40, 170], 6, 2, bits, 16, pos0=pos0, prior=True, decay=0.0, **more)
+
+
+# Which kernel runs goes by rows, heads and the tables' room: one group of 64 tokens a wave or several in turn, 32 or 64
+# tokens a wave with all rows or a share of them.
+@pytest.mark.parametrize("q_len,kv_len,Hq,Hkv,page,room", [
+    ([1, 3, 0, 2, 1, 1, 1, 1], [900, 70, 33, 2000, 64, 65, 1, 513], 32, 8, 16, 16384),
+    ([1] * 8, [900, 70, 33, 2000, 64, 5000, 1, 513], 16, 8, 64, 131072 + 1024),
+    ([20] * 8, [900, 70, 33, 2000, 64, 65, 20, 513], 8, 8, 64, 16384),
+    ([300], [1100], 4, 1, 16, 66000),
+    ([300, 17], [300, 400], 5, 1, 64, 40000),
+    ([40, 0, 90], [600, 300, 90], 96, 32, 64, 1500),
+])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("more", [{}, dict(softcap=20.0, alibi=True, bidir=True), dict(window=100)])
+def test_kernels(q_len, kv_len, Hq, Hkv, page, room, bits, more):
+    rng = np.random.default_rng(Hq + room)
+    check(rng, q_len, kv_len, Hq, Hkv, bits, page, before=1, behind=1, prior=True, decay=0.5, room=room, **more)
+
+
+def test_shares_in_a_workspace_of_the_callers():
+    rng = np.random.default_rng(9)
+    q, lse = rng.standard_normal((700, 8, 128)).astype(np.float16), rng.uniform(5, 9, (700, 8)).astype(np.float32)
+    cache, table = pool(rng, 60, 2, 16, 4), tables(rng, [900], 16, 60)
+    need = spin.spin_kv_weights_workspace(700, 8, 2, 1, table.shape[1], 16)
+    assert need > 0
+    W = lambda: torch.zeros((60, 2, 16), device=DEV)  # noqa: E731
+    a = weigh(q, lse, cache, table, starts([700]), [900], W())
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)            # NaN wherever it is read unwritten
+    b = weigh(q, lse, cache, table, starts([700]), [900], W(), workspace=ws)
+    assert np.array_equal(a, b) and np.isfinite(a).all()
+    with pytest.raises(spin.SpinError):
+        weigh(q, lse, cache, table, starts([700]), [900], W(), workspace=ws[:need - 16])
 
 
 def test_every_row_gives_a_weight_of_one_a_head():

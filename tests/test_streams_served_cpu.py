@@ -3,9 +3,14 @@
 import torch
 import pytest
 
-from rotation_bit_quantization_amd import spin
+from rotation_bit_quantization_amd import paged, spin
 
 from .test_streams_cpu import Stream, gpu, seen, tensors  # noqa: F401
+
+
+@pytest.fixture(autouse=True)
+def a_workspace(monkeypatch):
+    monkeypatch.setattr(paged, "spin_kv_weights_workspace", lambda *a: 4096)
 
 
 def calls():
@@ -27,7 +32,7 @@ def calls():
 
 
 def test_every_call_is_here():
-    assert spin._PAGED <= set(calls()) and spin._PAGED <= set(spin.__all__) and spin._PAGED <= set(dir(spin))
+    assert spin._PAGED <= {*calls(), "spin_kv_weights_workspace"} and spin._PAGED <= set(spin.__all__) and spin._PAGED <= set(dir(spin))
     with pytest.raises(AttributeError):
         spin.spin_kv_forest
 
