@@ -703,12 +703,23 @@ spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pag
  *   lens   [B] int32   OUTPUT: how many stay, min(kv_len[b], keep)
  * Of equal weights the lowest place stays (-0 equals 0).  NaN, and a token
  * that lies in no page of the pool, are below all weights.
- * Errors: SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE (also more than 2^22 - 1 sequences times
- * heads), SPIN_ERR_MISALIGNED.
+ *   workspace  device memory of the bytes spin_kv_choose_workspace names (it may be
+ *          NULL if that is 0); its content before and after means nothing, and calls
+ *          that overlap need one each
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE (also a workspace that is too small, and
+ * more than 2^22 - 1 sequences times heads, of tables above 32768 tokens a third of
+ * that, or as many times 8192 tokens),
+ * SPIN_ERR_MISALIGNED.
  */
 spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, int B, const int32_t* kv_len,
                            const int32_t* page_table, int max_pages, int keep, int first, int recent, int32_t* kept,
-                           int32_t* lens, void* stream);
+                           int32_t* lens, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spin_kv_choose_workspace — bytes of workspace a spin_kv_choose call of these sizes
+ * takes (0: none, up to 32768 tokens a table).  It goes by the sizes alone.
+ */
+spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_size, size_t* bytes);
 
 /*
  * spin_kv_move — tokens of the cache to other slots, codes and scales as they are.

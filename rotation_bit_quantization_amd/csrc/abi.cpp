@@ -602,19 +602,32 @@ spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pag
     return SPIN_OK;
 }
 
+spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_size, size_t* bytes) {
+    if (!bytes) return SPIN_ERR_NULL;
+    const spin_status ok = paged_ok(128, 4, Hkv, 1, page_size, B, max_pages);
+    if (ok != SPIN_OK) return ok;
+    if (!spin::kv_choose_fits(Hkv, B, max_pages * page_size)) return SPIN_ERR_BAD_SHAPE;
+    *bytes = spin::kv_choose_workspace(Hkv, B, max_pages * page_size);
+    return SPIN_OK;
+}
+
 spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, int B, const int32_t* kv_len,
                            const int32_t* page_table, int max_pages, int keep, int first, int recent, int32_t* kept,
-                           int32_t* lens, void* stream) {
+                           int32_t* lens, void* workspace, size_t workspace_bytes, void* stream) {
     if (!W || !kv_len || !page_table || !kept || !lens) return SPIN_ERR_NULL;
     const spin_status ok = paged_ok(128, 4, Hkv, n_pages, page_size, B, max_pages);
     if (ok != SPIN_OK) return ok;
     if (keep < 1 || keep > SPIN_KV_MAX_CONTEXT || first < 0 || recent < 0 || first > keep || recent > keep - first)
         return SPIN_ERR_BAD_SHAPE;
-    if (!spin::kv_choose_fits(Hkv, B)) return SPIN_ERR_BAD_SHAPE;
-    if (!aligned_all({W, kv_len, page_table, kept, lens})) return SPIN_ERR_MISALIGNED;
+    if (!spin::kv_choose_fits(Hkv, B, max_pages * page_size)) return SPIN_ERR_BAD_SHAPE;
+    if (!aligned_all({W, kv_len, page_table, kept, lens, workspace})) return SPIN_ERR_MISALIGNED;
     if (B == 0) return SPIN_OK;
+    const size_t need = spin::kv_choose_workspace(Hkv, B, max_pages * page_size);
+    if (need > 0 && !workspace) return SPIN_ERR_NULL;
+    if (workspace_bytes < need) return SPIN_ERR_BAD_SHAPE;
     return from_hip(spin::launch_kv_choose({W, Hkv, n_pages, __builtin_ctz(static_cast<unsigned>(page_size)), B, kv_len, page_table,
-                                            max_pages, keep, first, recent, kept, lens}, static_cast<hipStream_t>(stream)));
+                                            max_pages, keep, first, recent, kept, lens, static_cast<int*>(workspace)},
+                                           static_cast<hipStream_t>(stream)));
 }
 
 spin_status spin_kv_move(uint8_t* K_codes, uint16_t* K_scale, uint8_t* V_codes, uint16_t* V_scale, float* W, int Hkv,

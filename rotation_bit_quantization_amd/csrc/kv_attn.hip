@@ -118,17 +118,6 @@ __device__ __forceinline__ int count_tiles(const KvAttnArgs& a, int G, int b0, i
     return rows > 0 ? (rows + ROWS - 1) / ROWS : 0;
 }
 
-// The sum of lanes 0 .. l, in lane l.
-__device__ __forceinline__ int sums_up_to(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // rows of 16: shifts by 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // lane 15 of rows 0, 2 to rows 1, 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // lane 31 to rows 2, 3
-    return v;
-}
-
 // Where `tile` is among the lanes' tiles, b is set and the tile's number in its sequence returned, otherwise its number
 // behind them.
 __device__ __forceinline__ int find_tile(int tiles, int b0, int tile, int& b) {

@@ -150,8 +150,10 @@ struct KvChooseArgs {
     int max_pages, keep, first, recent;
     int32_t* kept;
     int32_t* lens;
+    int* counts;                   // the workspace
 };
-bool kv_choose_fits(int Hkv, int B);
+size_t kv_choose_workspace(int Hkv, int B, int room);
+bool kv_choose_fits(int Hkv, int B, int room);
 hipError_t launch_kv_choose(const KvChooseArgs& a, hipStream_t s);
 
 // Tokens to other slots of the cache.

@@ -12,9 +12,10 @@ import functools
 
 import torch
 
-from .spin import _attn, _batch, _cache, _gpu, _int, _launch, _on_stream, _prefix, _raise, _want, load
+from .spin import _attn, _batch, _cache, _gpu, _int, _launch, _on_stream, _prefix, _ptr, _raise, _want, load
 
-__all__ = ["spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_weights_workspace", "spin_kv_choose", "spin_kv_move"]
+__all__ = ["spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_weights_workspace", "spin_kv_choose",
+           "spin_kv_choose_workspace", "spin_kv_move"]
 
 
 def spin_kv_tree(parent, q_start, kv_len, words, pos0=0, tree=None, positions=None, stream=None):
@@ -74,6 +75,14 @@ def spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page_size):
     return n.value
 
 
+def _workspace(given, need, of, dev):
+    """(the workspace of a call, its bytes): the caller's, or one of ``need`` bytes on ``of``'s GPU."""
+    if given is not None:
+        _want(given, "workspace", torch.uint8, (given.numel(),), dev)
+        return given, given.numel()
+    return (of.new_empty((need,), dtype=torch.uint8), need) if need else (None, 0)
+
+
 def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, softcap=0.0, slopes=None, window=0, causal=True,
                     bidir_len=None, pos0=0, prior=None, decay=1.0, W=None, stream=None, workspace=None):
     """Q [T, Hq, 128] fp16 and lse [T, Hq] fp32 (from spin_kv_attn, with the same scores and masks) -> W [n_pages, Hkv,
@@ -102,27 +111,30 @@ def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, soft
     if B != 0:                      # an empty tensor has no address to pass; no rows are no weights
         if T == 0:
             q = log = starts
-        need = spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page)
-        ws, ws_bytes = None, 0
-        if workspace is not None:
-            ws_bytes = workspace.numel()
-            ws = _want(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
-        elif need:
-            workspace = Q.new_empty((need + 1) // 2)
-            ws, ws_bytes = workspace.data_ptr(), need
+        ws, ws_bytes = _workspace(workspace, spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page), Q, dev)
         _launch("spin_kv_weights", dev,
                 (q, log, T, Hq, Hkv, 128, bits, kc, ks, n_pages, page, B, starts, lens, table, max_pages, _int(pos0, "pos0"),
                  0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both,
-                 old, decay, out, ws, ws_bytes))
+                 old, decay, out, _ptr(ws), ws_bytes))
     return W
 
 
-def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, lens=None, stream=None):
+@functools.lru_cache(4096)
+def spin_kv_choose_workspace(Hkv, B, max_pages, page_size):
+    """Bytes of workspace that spin_kv_choose takes at these sizes."""
+    for name, x in dict(Hkv=Hkv, B=B, max_pages=max_pages, page_size=page_size).items():
+        _int(x, name)
+    n = ctypes.c_size_t(0)
+    _raise("spin_kv_choose_workspace", load().spin_kv_choose_workspace(Hkv, B, max_pages, page_size, ctypes.byref(n)))
+    return n.value
+
+
+def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, lens=None, stream=None, workspace=None):
     """W [n_pages, Hkv, page_size] fp32 -> (kept [B, Hkv, keep] int32: the places of the tokens that stay, ascending, -1
     behind them, lens [B] int32): per sequence and head its first ``first`` and last ``recent`` tokens and those of
-    greatest weight."""
+    greatest weight.  ``workspace`` (uint8, spin_kv_choose_workspace bytes) is allocated if it is not given."""
     if stream is not None:
-        return _on_stream(stream, W, spin_kv_choose, W, page_table, kv_len, keep, first, recent, kept, lens)
+        return _on_stream(stream, W, spin_kv_choose, W, page_table, kv_len, keep, first, recent, kept, lens, workspace=workspace)
     dev = _gpu(W, "W")
     if W.dim() != 3 or page_table.dim() != 2:
         raise ValueError(f"W and page_table have shapes {tuple(W.shape)} and {tuple(page_table.shape)}, expected [n_pages, Hkv, page_size] "
@@ -142,8 +154,9 @@ def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, le
     out = _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
     left = _want(lens, "lens", torch.int32, (B,), dev)
     if B != 0:                      # an empty tensor has no address to pass
+        ws, ws_bytes = _workspace(workspace, spin_kv_choose_workspace(Hkv, _int(B, "B"), _int(max_pages, "max_pages"), page), W, dev)
         _launch("spin_kv_choose", dev, (w, Hkv, n_pages, page, _int(B, "B"), length, table, _int(max_pages, "max_pages"), keep,
-                                        _int(first, "first"), _int(recent, "recent"), out, left))
+                                        _int(first, "first"), _int(recent, "recent"), out, left, _ptr(ws), ws_bytes))
     return kept, lens
 
 

@@ -101,11 +101,24 @@ def test_weights_workspace(lib):
 
 def test_choose(lib):
     call = caller(lib.spin_kv_choose, dict(W=A, Hkv=8, n_pages=10, page=16, B=0, kv_len=A, table=A, max_pages=5, keep=40, first=4, recent=30,
-                                           kept=A, lens=A, st=None))
+                                           kept=A, lens=A, ws=A, ws_bytes=1 << 30, st=None))
     assert call() == call(first=40, recent=0) == call(first=0, recent=40) == spin.SPIN_OK
     refusals(call, ("W", "kv_len", "table", "kept", "lens"), (),
              (dict(keep=0, first=0, recent=0), dict(keep=-1), dict(first=-1), dict(recent=-1), dict(first=11), dict(first=41, recent=0),
-              dict(first=BIG, recent=BIG), dict(keep=BIG), dict(B=1 << 20), dict(Hkv=0)) + PAGES, ("W", "kv_len", "table", "kept", "lens"))
+              dict(first=BIG, recent=BIG), dict(keep=BIG), dict(B=1 << 20), dict(Hkv=0),
+              dict(B=1 << 16, max_pages=1 << 12)) + PAGES, ("W", "kv_len", "table", "kept", "lens", "ws"))
+    assert call(ws=None, ws_bytes=0) == spin.SPIN_OK
+    # long tables are dealt out, which needs a workspace
+    assert call(B=1, max_pages=4096, ws=None) == spin.SPIN_ERR_NULL
+    assert call(B=1, max_pages=4096, ws_bytes=16) == spin.SPIN_ERR_BAD_SHAPE
+    n = ctypes.c_size_t(7)
+    need = caller(lib.spin_kv_choose_workspace, dict(Hkv=8, B=2, max_pages=4096, page=16, out=ctypes.byref(n)))
+    assert need() == spin.SPIN_OK and n.value >= 16 * 4 * 6144
+    assert need(max_pages=2048) == spin.SPIN_OK and n.value == 0
+    assert need(B=0) == spin.SPIN_OK and n.value == 0
+    assert need(out=None) == spin.SPIN_ERR_NULL
+    for bad in (dict(Hkv=0), dict(B=-1), dict(max_pages=0), dict(page=7), dict(B=BIG)):
+        assert need(**bad) == spin.SPIN_ERR_BAD_SHAPE, bad
 
 
 def test_move(lib):

@@ -250,6 +250,13 @@ def choose(W, table, kv_len, keep, first=0, recent=0):
     ([70000], 2, 1024, 69999, 1, 1),
     ([70000, 33000], 1, 64, 512, 0, 0),
     ([140000], 1, 64, 4096, 4, 64),
+    ([9000, 10000, 300], 2, 16, 2048, 7, 9),                                        # 16 tokens a thread in the registers
+    ([33000, 100, 8192, 8193, 40000, 0], 2, 64, 4000, 4, 1000),                     # several workgroups a head
+    ([33000, 100, 8192, 8193, 40000, 0], 2, 64, 50000, 4, 1000),
+    ([60000, 50], 1, 16, 20000, 9000, 11000),
+    ([33000, 500] * 32, 4, 16, 4000, 4, 1000),                                      # more of each for a workgroup
+    ([70000] + [500] * 30, 4, 64, 40000, 4, 1000),
+    ([60000, 17000], 1, 16, 8193, 0, 0),
 ])
 def test_choice(kv_len, Hkv, page, keep, first, recent):
     rng = np.random.default_rng(sum(kv_len))
@@ -288,6 +295,21 @@ def test_choice_of_many_sequences(B):
     table = tables(rng, kv_len, 16, int((-(-kv_len // 16)).sum()) + 1)
     W = rng.random((int((-(-kv_len // 16)).sum()) + 1, 2, 16)).astype(np.float32)
     choose(W, table, kv_len, 50, 2, 10)
+
+
+def test_choice_in_a_workspace_of_the_callers():
+    rng = np.random.default_rng(3)
+    table, W = tables(rng, [50000, 33000], 64, 1400), rng.random((1400, 2, 64)).astype(np.float32)
+    kv = dev(np.array([50000, 33000], np.int32))
+    need = spin.spin_kv_choose_workspace(2, 2, table.shape[1], 64)
+    assert need > 0
+    ref, _ = oracle.kv_choose(W, table, [50000, 33000], 3000, 10, 20)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        kept, _ = spin.spin_kv_choose(dev(W), dev(table), kv, 3000, first=10, recent=20, workspace=ws)
+        assert np.array_equal(host(kept), ref)
+    with pytest.raises(spin.SpinError):
+        spin.spin_kv_choose(dev(W), dev(table), kv, 3000, workspace=ws[:need - 16])
 
 
 # ------------------------------------------------------------------------------------------------ the move

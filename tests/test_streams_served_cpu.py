@@ -11,6 +11,7 @@ from .test_streams_cpu import Stream, gpu, seen, tensors  # noqa: F401
 @pytest.fixture(autouse=True)
 def a_workspace(monkeypatch):
     monkeypatch.setattr(paged, "spin_kv_weights_workspace", lambda *a: 4096)
+    monkeypatch.setattr(paged, "spin_kv_choose_workspace", lambda *a: 4096)
 
 
 def calls():
@@ -32,7 +33,7 @@ def calls():
 
 
 def test_every_call_is_here():
-    assert spin._PAGED <= {*calls(), "spin_kv_weights_workspace"} and spin._PAGED <= set(spin.__all__) and spin._PAGED <= set(dir(spin))
+    assert spin._PAGED <= {*calls(), "spin_kv_weights_workspace", "spin_kv_choose_workspace"} and spin._PAGED <= set(spin.__all__) and spin._PAGED <= set(dir(spin))
     with pytest.raises(AttributeError):
         spin.spin_kv_forest
 
