@@ -199,10 +199,10 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_clear(KvChooseArgs a
 // step 0, 1, 2: count that digit; 3: how many stay; 4: write them
 template <int STEP>
 __global__ __launch_bounds__(kChooseThreads) void kv_choose_part(KvChooseArgs a, int parts) {
+    constexpr int R = kPartRounds;
     __shared__ int count[kBins];
     __shared__ int sums[R * kChooseWaves];
     __shared__ int found[2];
-    constexpr int R = kPartRounds;
     const int head = blockIdx.x / parts, part = blockIdx.x - head * parts, p0 = part * kPart;
     const Head x = head_of(a, head);
     if (STEP == 4 && x.h == 0 && part == 0 && threadIdx.x == 0) a.lens[x.b] = min(x.n, a.keep);
