@@ -89,6 +89,31 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* __restrict__ row, 
 // A new token's position, held to what differences of two fit 32 bits with.
 __device__ __forceinline__ int position(const KvAttnArgs& a, int t) { return min(max(a.positions[t], 0), 1 << 30); }
 
+// Masks a row's exponents of N of 32 tokens, the `first` of which is counted among the new ones, by the tree and the
+// window, and puts the bias of new tokens right, which `rel`, the row's position less the lane's first place, has given them
+// by their places.  Exponent e is that of token lane0 + e % 4 + 128 / N (e / 4) of the 32.  One position at a time: all of
+// them at once take registers that the main path lacks.
+template <int SCORES, int N, typename X>
+__device__ __forceinline__ void tree_mask(const KvAttnArgs& a, X& x, int t, bool valid, int first, int lane0, int news, int new0, int pos, int rel,
+                                          float slope) {
+    const uint32_t named = valid ? tree_bits(a.tree + static_cast<long long>(t) * a.tree_words, a.tree_words, first) >> lane0 : 0u;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int c = 128 / N * (e >> 2) + (e & 3);
+        x[e] = named >> c & 1 ? x[e] : -__builtin_inff();
+    }
+    if (a.window <= 0 && !(biased(SCORES) && a.slopes)) return;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        asm volatile("" ::: "memory");
+        const int c = 128 / N * (e >> 2) + (e & 3), i = first + lane0 + c;
+        const int far = i >= 0 && i < news ? pos - position(a, new0 + i) : rel - c;
+        if (biased(SCORES)) x[e] = __builtin_fmaf(slope, __builtin_fabsf(static_cast<float>(rel - c)) - __builtin_fabsf(static_cast<float>(far)), x[e]);
+        if (a.window > 0)
+            x[e] = static_cast<uint32_t>(far) + static_cast<uint32_t>(a.window) - 1u < 2u * static_cast<uint32_t>(a.window) - 1u ? x[e] : -__builtin_inff();
+    }
+}
+
 // The logarithm of a row's sum of exponentials.
 __device__ __forceinline__ float log_sum(float M, float l) {
     return l == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
@@ -166,7 +191,7 @@ __device__ __forceinline__ void longest_first(const KvAttnArgs& a, int lane, int
 // alone), on 8192 each 5.4 TB/s; 1 on 1000 10 us, of which four loads that wait
 // for each other (sequence, length, page, codes) and four steps.
 template <int BITS, int SCORES, int WAVES, bool TREE>
-__global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
+__global__ __launch_bounds__(64 * WAVES, TREE && BITS == 4 && SCORES == kPlain ? 4 : 3) void kv_attn_rows16(KvAttnArgs a, int prefix_tiles, int prefix_splits, int prefix_chunk,
                                                                   int own_tiles, int own_splits, int own_chunk) {
     __shared__ float o_sh[WAVES][kRows][129];
     __shared__ float m_sh[WAVES][kRows], l_sh[WAVES][kRows];
@@ -308,8 +333,8 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         const float c = sum_over_groups(sum) * (BITS == 4 ? -0x1p-21f : -0x1p-17f);
         start = f4{c, c, c, c};
     }
-    const float slope = SCORES != kPlain && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
-    const bool near_cap = SCORES == kFancy && a.softcap > 0.0f;
+    const float slope = biased(SCORES) && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+    const bool near_cap = SCORES == kCapped || (SCORES == kFancy && a.softcap > 0.0f);
     const Cap cap = cap_of<SCORES>(a);
     const float key_factor = held(cap.factor * 0x1p24f);
 
@@ -406,23 +431,10 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
         const int next = i + 1 < turns ? i + 1 : i;
         if ((next & 31) == 0 && next > 0) load_places(next);
         fetch_keys(next);
-        const float from = SCORES == kFancy ? M - cap.top : M;
+        const float from = SCORES == kFancy || SCORES == kCapped ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * g);
-        float far[8];                      // TREE: the tokens' distances
-        if (TREE && SCORES != kPlain) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) far[e] = rel - static_cast<float>(16 * (e >> 2) + (e & 3));
-            if (a.slopes && (st + 1) * kStep > fresh) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = st * kStep + 4 * g + 16 * (e >> 2) + (e & 3) - fresh;
-                    if (i >= 0 && i < news) far[e] = static_cast<float>(pos - position(a, new0 + i));
-                }
-            }
-        }
         auto exponent = [&](int e, float k, float lm, bool capped) __attribute__((always_inline)) {
-            if (SCORES != kPlain)
-                lm = __builtin_fmaf(-slope, __builtin_fabsf(TREE ? far[e] : rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
+            if (biased(SCORES)) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
             x[e] = SCORES == kWideCap ? capped_wide(x[e] * k, cap.top, cap.rtop) + lm
                                       : capped ? capped_plus(x[e] * k, cap.top, lm) : __builtin_fmaf(x[e], k, lm);
         };
@@ -443,19 +455,15 @@ __global__ __launch_bounds__(64 * WAVES, 3) void kv_attn_rows16(KvAttnArgs a, in
             const int end = a.causal ? max(rel, both - j0 - 4 * g - 1) : 32;
             const uint32_t off = a.window > 0 ? static_cast<uint32_t>(rel) + static_cast<uint32_t>(a.window) - 1u : 32u;
             const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
-            const int first = st * kStep - fresh;
-            const uint32_t named = TREE && valid ? tree_bits(a.tree + static_cast<long long>(t) * a.tree_words, a.tree_words, first) >> (4 * g) : 0u;
+            if (TREE) {
+                tree_mask<SCORES, 8>(a, x, t, valid, st * kStep - fresh, 4 * g, news, new0, pos, rel, slope);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = 16 * (e >> 2) + (e & 3);
-                bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
-                if (TREE) {
-                    const int i = first + 4 * g + c;
-                    if (a.window > 0 && i >= 0 && i < news)
-                        seen = static_cast<uint32_t>(pos - position(a, new0 + i)) + static_cast<uint32_t>(a.window) - 1u < wide;
-                    seen = seen && (named >> c & 1);
+                for (int e = 0; e < 8; ++e) {
+                    const int c = 16 * (e >> 2) + (e & 3);
+                    const bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
+                    x[e] = seen ? x[e] : -__builtin_inff();
                 }
-                x[e] = seen ? x[e] : -__builtin_inff();
             }
         }
         float top = x[0];
@@ -798,8 +806,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         }
     }
     const int at_row = valid ? t * a.Hq + head : -1;       // T * Hq is below 2^26
-    const float slope = SCORES != kPlain && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
-    const bool near_cap = SCORES == kFancy && a.softcap > 0.0f;
+    const float slope = biased(SCORES) && a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+    const bool near_cap = SCORES == kCapped || (SCORES == kFancy && a.softcap > 0.0f);
     const Cap cap = cap_of<SCORES>(a);
     const float key_factor = held(cap.factor);
 
@@ -908,20 +916,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     };
     // products to exponents of the tokens at positions j0 .. j0 + 31, relative to M
     auto exponents = [&](int j0) __attribute__((always_inline)) {
-        const float from = SCORES == kFancy ? M - cap.top : M;
+        const float from = SCORES == kFancy || SCORES == kCapped ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * hf);
-        const int new_at = j0 - span.base + 4 * hf - fresh;
-        const bool drafted = TREE && a.slopes && j0 - span.base + 32 > fresh;
         auto one = [&](int e, float lm, bool capped) __attribute__((always_inline)) {
             const float k = kf[e >> 2][e & 3];
-            if (SCORES != kPlain) {
-                float far = rel - static_cast<float>(8 * (e >> 2) + (e & 3));
-                if (TREE && drafted) {
-                    const int i = new_at + 8 * (e >> 2) + (e & 3);
-                    if (i >= 0 && i < news) far = static_cast<float>(pos - position(a, new0 + i));
-                }
-                lm = __builtin_fmaf(-slope, __builtin_fabsf(far), lm);
-            }
+            if (biased(SCORES)) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
             s[e] = SCORES == kWideCap ? capped_wide(s[e] * k, cap.top, cap.rtop) + lm
                                       : capped ? capped_plus(s[e] * k, cap.top, lm) : __builtin_fmaf(s[e], k, lm);
         };
@@ -944,18 +943,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
         const int end = a.causal ? max(rel, both - j0 - 4 * hf - 1) : 32;
         const uint32_t off = a.window > 0 ? static_cast<uint32_t>(rel) + static_cast<uint32_t>(a.window) - 1u : 32u;
         const uint32_t wide = a.window > 0 ? 2u * static_cast<uint32_t>(a.window) - 1u : 64u;
-        const int first = j0 - span.base - fresh;
-        const uint32_t named = TREE && valid ? tree_bits(a.tree + static_cast<long long>(t) * a.tree_words, a.tree_words, first) >> (4 * hf) : 0u;
+        if (TREE) {
+            const int row = static_cast<int>(static_cast<unsigned>(max(at_row, 0)) / static_cast<unsigned>(a.Hq));
+            tree_mask<SCORES, 16>(a, s, row, at_row >= 0, j0 - span.base - fresh, 4 * hf, news, new0, pos, rel, slope);
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int c = 8 * (e >> 2) + (e & 3);
-            bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
-            if (TREE) {
-                const int i = first + 4 * hf + c;
-                if (a.window > 0 && i >= 0 && i < news)
-                    seen = static_cast<uint32_t>(pos - position(a, new0 + i)) + static_cast<uint32_t>(a.window) - 1u < wide;
-                seen = seen && (named >> c & 1);
-            }
+            const bool seen = (end >= c) & (off - static_cast<uint32_t>(c) < wide);
             s[e] = seen ? s[e] : -__builtin_inff();
         }
     };
@@ -1323,6 +1319,10 @@ hipError_t launch_rows(const KvAttnArgs& a, Part prefix, Part own, hipStream_t s
     if (own.rows != ROWS) own.tiles = 0;
     if (prefix.tiles == 0 && own.tiles == 0) return hipSuccess;
     if (a.softcap > kNearCap) return launch_part<BITS, ROWS, kWideCap, TREE>(a, prefix, own, s);
+    // the tree's masks take registers that a cap with a bias has none of (16 trees of 60 on 4096, INT8, capped: 134 us, with the bias in the kernel 185)
+    if constexpr (TREE) {
+        if (a.softcap > 0.0f && !a.slopes) return launch_part<BITS, ROWS, kCapped, TREE>(a, prefix, own, s);
+    }
     return a.softcap > 0.0f || a.slopes ? launch_part<BITS, ROWS, kFancy, TREE>(a, prefix, own, s)
                                         : launch_part<BITS, ROWS, kPlain, TREE>(a, prefix, own, s);
 }

@@ -102,8 +102,9 @@ __device__ __forceinline__ float capped_wide(float z, float top, float rtop) {
 }
 
 // What a kernel does to the scores: nothing; a distance bias, a cap up to kNearCap, or both; a cap above, with or without
-// a bias.
-enum Scores { kPlain, kFancy, kWideCap };
+// a bias; a cap up to kNearCap and surely no bias.
+enum Scores { kPlain, kFancy, kWideCap, kCapped };
+constexpr bool biased(int scores) { return scores == kFancy || scores == kWideCap; }
 
 // A factor of scores within the numbers that keep them finite.  Products are multiples of 2^-48, or zero: scores that this
 // brings down still lie past every cap up to kNearCap, or so far apart that their roundings, 2^-24 of them, are past what
@@ -124,7 +125,7 @@ __device__ __forceinline__ Cap cap_of(const Args& a) {
         const float top = __builtin_fminf(a.softcap * kLog2e, 0x1p126f);       // its double has to be finite
         return {a.scale * kLog2e, top, 1.0f / top};
     }
-    const bool capped = SCORES == kFancy && a.softcap > 0.0f;
+    const bool capped = SCORES == kCapped || (SCORES == kFancy && a.softcap > 0.0f);
     return {capped ? 2.0f * kLog2e * (a.scale / a.softcap) : a.scale * kLog2e, capped ? a.softcap * kLog2e : 0.0f, 0.0f};
 }
 
