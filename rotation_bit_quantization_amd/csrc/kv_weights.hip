@@ -38,7 +38,10 @@ constexpr int kTilesWanted = 256;
 // Workgroups that shares of the rows bring a call to, tiles of 32 rows that a share has at least, and the most shares: a
 // prompt of 2000 takes 204 us in one share, 37 in up to 16, one of 500 59 and 15.
 constexpr int kSharesWanted = 4096, kLeastTiles = 4, kMostShares = 16;
-constexpr int kMostTurns = 16;             // of a wave: a lane each for the pages of 16 tokens
+constexpr int kCounted = 256;              // sequences up to which their chunks are counted
+// Groups that a wave takes, where there are enough for it (64 sequences on up to 8192 tokens 61 us with one, 47 with four,
+// 53 with twelve), and what enough is.
+constexpr int kMostTurns = 4, kGroupsEnough = 8192;
 
 // What a row adds to tokens, as the kernels hold it: its position, the logarithm in units of log2 (infinite where it adds
 // nothing: every exponential is 0) and its bias.
@@ -106,6 +109,10 @@ __device__ __forceinline__ unsigned long long place_of(const KvWeightsArgs& a, i
 __device__ __forceinline__ float scale_of(uint32_t raw) { return __half2float(__ushort_as_half(static_cast<unsigned short>(raw))); }
 
 // Few rows: 16 at a time, groups of 64 tokens in turn, the next one's keys in flight.
+//
+// Bound: reading the keys, 16 BITS + 2 bytes a token and head, from the second round of workgroups on; before that loads
+// that wait for each other (length, page, keys).  Measured: 64 single tokens of 32 + 8 heads on 2000 to 8192, INT4, 47 us
+// (189 MB, 4.0 TB/s), INT8 83; on 5120 each 4.3 TB/s; 16 on 2000 to 8192 17 us, one on 30000 6.5, one on 1000 4.5.
 template <int BITS, int SCORES>
 __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_rows16(KvWeightsArgs a, int chunks, int turns) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -113,11 +120,30 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_
     const int G = a.Hq / a.Hkv;
     // workgroup L runs on XCD L % 8: the heads of an item follow each other on one, which share lines of scales
     const int h = (blockIdx.x >> 3) % a.Hkv;
-    const int item = (blockIdx.x >> 3) / a.Hkv * 8 + (blockIdx.x & 7);
-    const int b = item / chunks;
-    if (b >= a.B) return;
+    int item = (blockIdx.x >> 3) / a.Hkv * 8 + (blockIdx.x & 7), b = -1;
+    if (a.B <= kCounted) {
+        // numbered without the chunks that sequences are too short for (64 of 2000 to 8192
+        // tokens: 57 to 63 us with gaps, by their number, 47 to 50 without)
+        const int chunk = turns * kWeightWaves * kGroup;
+        for (int b0 = 0; b0 < a.B && b < 0; b0 += 64) {
+            const int own = b0 + lane < a.B ? (context(a, b0 + lane) + chunk - 1) / chunk : 0, upto = sums_up_to(own);
+            const unsigned long long hit = __ballot(upto > item);
+            if (hit == 0) {
+                item -= __builtin_amdgcn_readlane(upto, 63);
+            } else {
+                const int l = __builtin_ctzll(hit);
+                b = b0 + l;
+                item -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l);
+            }
+        }
+        if (b < 0) return;
+    } else {
+        b = item / chunks;
+        item -= b * chunks;
+        if (b >= a.B) return;
+    }
     const int tokens = context(a, b);
-    const int first = ((item - b * chunks) * turns * kWeightWaves + wave) * kGroup;      // then every kWeightWaves-th group
+    const int first = (item * turns * kWeightWaves + wave) * kGroup;      // then every kWeightWaves-th group
     if (first >= tokens) return;
     const int q0 = within(a.q_start[b], a.T), q1 = within(a.q_start[b + 1], a.T);
     const int news = max(q1 - q0, 0);
@@ -223,6 +249,7 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = exponent<SCORES>(a, cap, s[e], kf[i], less[e], slopes[e], where[e], p);
                 if (!whole) {
+                    asm volatile("" ::: "memory");     // keeps this a branch
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = sees(a, where[e], p, both) ? x[e] : -__builtin_inff();
                 }
@@ -249,6 +276,12 @@ constexpr int kTileRows = 32;
 
 // Many rows: the workgroup stages 32 rows at a time in LDS, and each wave holds the keys of 32 M tokens as operands and
 // takes all rows past them.
+//
+// Bound: the vector work of the weights beside the matrix work, 24 cycles (a multiply-add, an exponential, an addition) of
+// 64 scores against 16, with a cap and a bias 72, and what staging 32 rows takes.  A token's sum is carried with what its
+// additions have lost, 32 rows at a time, so that it is as exact for a long prompt as for a row.  Measured with 32 + 8 heads
+// and INT4: a prompt of 8192 tokens 320 us (0.86 PFLOP/s), of 2000 37, 32 tokens each of two on 16384 21; three prompts of
+// 1670, 32 + 32 heads, INT8, capped and biased, 125.
 template <int BITS, int SCORES, int M>
 __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsArgs a, int splits) {
     struct Stage {
@@ -470,7 +503,7 @@ Plan plan(int T, int Hq, int Hkv, int B, int room, bool plain) {
         if (splits > rows / (kTileRows * kLeastTiles)) splits = rows / (kTileRows * kLeastTiles);
         p.splits = static_cast<int>(splits < 1 ? 1 : splits > kMostShares ? kMostShares : splits);
     } else {
-        const long long turns = heads * ((room + kGroup - 1) / kGroup) / (kWeightWaves * 2048);
+        const long long turns = heads * ((room + kGroup - 1) / kGroup) / kGroupsEnough;
         p.turns = static_cast<int>(turns < 1 ? 1 : turns > kMostTurns ? kMostTurns : turns);
     }
     return p;

@@ -12,10 +12,17 @@ import functools
 
 import torch
 
-from .spin import _attn, _batch, _cache, _gpu, _int, _launch, _on_stream, _prefix, _ptr, _raise, _want, load
+from .spin import _attn, _batch, _cache, _check, _gpu, _int, _launch, _on_stream, _prefix, _ptr, _raise, _want, load
 
 __all__ = ["spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spin_kv_weights_workspace", "spin_kv_choose",
            "spin_kv_choose_workspace", "spin_kv_move"]
+
+
+def _all(dev, *given):
+    """Raise unless every (tensor, name, dtype, shape) is contiguous, of that type and shape, on GPU `dev`."""
+    for t, name, dtype, shape in given:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+            _want(t, name, dtype, shape, dev) if isinstance(t, torch.Tensor) else _check(t, name, (dtype,), shape)
 
 
 def spin_kv_tree(parent, q_start, kv_len, words, pos0=0, tree=None, positions=None, stream=None):
@@ -27,19 +34,20 @@ def spin_kv_tree(parent, q_start, kv_len, words, pos0=0, tree=None, positions=No
     if parent.dim() != 1 or kv_len.dim() != 1:
         raise ValueError(f"parent and kv_len have shapes {tuple(parent.shape)} and {tuple(kv_len.shape)}, expected [T] and [B]")
     T, B, words = _int(parent.shape[0], "T"), _int(kv_len.shape[0], "B"), _int(words, "words")
-    p = _want(parent, "parent", torch.int32, (T,), dev)
-    starts = _want(q_start, "q_start", torch.int32, (B + 1,), dev)
-    lens = _want(kv_len, "kv_len", torch.int32, (B,), dev)
     if words < 1:
         raise ValueError(f"words is {words}, expected 1 or more")
+    _all(dev, (parent, "parent", torch.int32, (T,)), (q_start, "q_start", torch.int32, (B + 1,)), (kv_len, "kv_len", torch.int32, (B,)))
     if tree is None:
-        tree = parent.new_empty((T, words))
+        tree = torch.empty((T, words), dtype=torch.int32, device=parent.device)
+    else:
+        _want(tree, "tree", torch.int32, (T, words), dev)
     if positions is None:
-        positions = parent.new_empty((T,))
-    out = _want(tree, "tree", torch.int32, (T, words), dev)
-    at = _want(positions, "positions", torch.int32, (T,), dev)
+        positions = torch.empty_like(parent)
+    else:
+        _want(positions, "positions", torch.int32, (T,), dev)
     if T != 0 and B != 0:           # an empty tensor has no address to pass
-        _launch("spin_kv_tree", dev, (p, T, B, starts, lens, _int(pos0, "pos0"), words, out, at))
+        _launch("spin_kv_tree", dev, (parent.data_ptr(), T, B, q_start.data_ptr(), kv_len.data_ptr(), _int(pos0, "pos0"), words,
+                                      tree.data_ptr(), positions.data_ptr()))
     return tree, positions
 
 
@@ -141,22 +149,22 @@ def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, le
                          "and [B, max_pages]")
     n_pages, Hkv, page = W.shape
     B, max_pages = page_table.shape
-    w = _want(W, "W", torch.float32, W.shape, dev)
-    table = _want(page_table, "page_table", torch.int32, (B, max_pages), dev)
-    length = _want(kv_len, "kv_len", torch.int32, (B,), dev)
     keep = _int(keep, "keep")
     if keep < 1:
         raise ValueError(f"keep is {keep}, expected 1 or more")
+    _all(dev, (W, "W", torch.float32, W.shape), (page_table, "page_table", torch.int32, (B, max_pages)), (kv_len, "kv_len", torch.int32, (B,)))
     if kept is None:
-        kept = page_table.new_empty((B, Hkv, keep))
+        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=W.device)
+    else:
+        _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
     if lens is None:
-        lens = page_table.new_empty((B,))
-    out = _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
-    left = _want(lens, "lens", torch.int32, (B,), dev)
+        lens = torch.empty_like(kv_len)
+    else:
+        _want(lens, "lens", torch.int32, (B,), dev)
     if B != 0:                      # an empty tensor has no address to pass
-        ws, ws_bytes = _workspace(workspace, spin_kv_choose_workspace(Hkv, _int(B, "B"), _int(max_pages, "max_pages"), page), W, dev)
-        _launch("spin_kv_choose", dev, (w, Hkv, n_pages, page, _int(B, "B"), length, table, _int(max_pages, "max_pages"), keep,
-                                        _int(first, "first"), _int(recent, "recent"), out, left, _ptr(ws), ws_bytes))
+        ws, ws_bytes = _workspace(workspace, spin_kv_choose_workspace(Hkv, B, max_pages, page), W, dev)
+        _launch("spin_kv_choose", dev, (W.data_ptr(), Hkv, n_pages, page, B, kv_len.data_ptr(), page_table.data_ptr(), max_pages, keep,
+                                        _int(first, "first"), _int(recent, "recent"), kept.data_ptr(), lens.data_ptr(), _ptr(ws), ws_bytes))
     return kept, lens
 
 
@@ -173,8 +181,7 @@ def spin_kv_move(cache, page_table, kept, at=None, to_table=None, W=None, stream
                          "and [B, max_pages]")
     B, max_pages = page_table.shape
     heads, n = kept.shape[1:]
-    table = _want(page_table, "page_table", torch.int32, (B, max_pages), dev)
-    rows = _want(kept, "kept", torch.int32, (B, heads, n), dev)
+    _all(dev, (page_table, "page_table", torch.int32, (B, max_pages)), (kept, "kept", torch.int32, (B, heads, n)))
     start = None if at is None else _want(at, "at", torch.int32, (B,), dev)
     to, to_pages = None, 0
     if to_table is not None:
@@ -184,6 +191,6 @@ def spin_kv_move(cache, page_table, kept, at=None, to_table=None, W=None, stream
         to = _want(to_table, "to_table", torch.int32, (B, to_pages), dev)
     w = None if W is None else _weights(W, "W", cache, dev)
     if B != 0 and n != 0 and not (to_table is not None and to_pages == 0):      # an empty tensor has no address to pass
-        _launch("spin_kv_move", dev, (*addresses, w, Hkv, 128, bits, n_pages, page, _int(B, "B"), table, _int(max_pages, "max_pages"), rows,
-                                      heads, _int(n, "n"), start, to, to_pages))
+        _launch("spin_kv_move", dev, (*addresses, w, Hkv, 128, bits, n_pages, page, _int(B, "B"), page_table.data_ptr(), _int(max_pages, "max_pages"),
+                                      kept.data_ptr(), heads, _int(n, "n"), start, to, to_pages))
     return cache

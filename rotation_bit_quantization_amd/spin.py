@@ -865,10 +865,17 @@ _PAGED = frozenset(("spin_kv_tree", "spin_kv_attn_tree", "spin_kv_weights", "spi
                     "spin_kv_choose_workspace", "spin_kv_move"))
 
 
+_paged_calls = {}
+
+
 def __getattr__(name):
+    call = _paged_calls.get(name)
+    if call is not None:
+        return call
     if name in _PAGED:
         from . import paged
-        return getattr(paged, name)
+        call = _paged_calls[name] = getattr(paged, name)
+        return call
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

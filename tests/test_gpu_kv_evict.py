@@ -111,6 +111,7 @@ def test_masks(more, bits, pos0):
     ([300], [1100], 4, 1, 16, 66000),
     ([300, 17], [300, 400], 5, 1, 64, 40000),
     ([40, 0, 90], [600, 300, 90], 96, 32, 64, 1500),
+    ([1, 2] * 140, [(37 * i) % 300 + 2 for i in range(280)], 2, 1, 16, 0),
 ])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("more", [{}, dict(softcap=20.0, alibi=True, bidir=True), dict(window=100)])
