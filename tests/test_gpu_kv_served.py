@@ -86,7 +86,7 @@ def test_speculative_steps(bits, page, prefix):
                     got, ref = (t.transpose(0, 2, 4, 1, 3, 5).reshape(-1, Hkv, 16, bits) for t in (got, ref))
                 else:
                     got, ref = (np.moveaxis(t, 1, 2).reshape(-1, Hkv, *t.shape[3:]) for t in (got, ref))
-                assert np.array_equal(got[:ctx[b]].view(np.uint8), ref[:ctx[b]].view(np.uint8)), (step, b, name)
+                assert np.array_equal(got[:ctx[b]], ref[:ctx[b]]), (step, b, name)
 
 
 def test_a_thinned_cache_goes_on():
@@ -193,20 +193,15 @@ def test_captured(case):
     for rep, less in enumerate([0, 7, 1000, 31, 0]):
         s["kv"].fill_(max(kv0 - less, 0))
         s["Q"].copy_(torch.roll(s["Q"], 1, 0))
+        s["W"].zero_()
         want = {k: host(v).copy() for k, v in serve(s).items()}
         seen.append(want["O"])
         for g, out in graphs + graphs[::-1]:
-            s["W"].zero_()
-            serve_w = want["W"]
+            for t in (s["W"], out["O"], out["P"], out["kept"]):
+                t.zero_()
             g.replay()
             for k, v in out.items():
-                if k == "W":                     # slots that this length does not reach are as they were
-                    live = serve_w != 0
-                    assert less >= 1000 or np.array_equal(host(v)[live & (host(v) != 0)], serve_w[live & (host(v) != 0)]), (rep, k)
-                elif k in ("K_codes", "V_codes", "K_scale", "V_scale"):
-                    assert np.array_equal(host(v).view(np.uint8), want[k].view(np.uint8)), (rep, k)
-                else:
-                    assert np.array_equal(host(v), want[k], equal_nan=True), (rep, k)
+                assert np.array_equal(host(v), want[k]), (rep, k)
     assert not np.array_equal(seen[0], seen[1])
 
 
