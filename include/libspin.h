@@ -728,10 +728,11 @@ spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_siz
  *          at place at[b] + kept[b][h][i] goes to place at[b] + i; entries below 0
  *          are passed over.  at [B] int32, NULL for 0.
  *   to_table   [B][to_pages] int32: the pages that it goes to, none of which may be
- *          one that tokens of this call come from.  NULL: places of page_table itself,
- *          in which case a list ascends, so that kept[b][h][i] >= i: the tokens that
- *          spin_kv_choose names, or the accepted path of a tree behind at[b] tokens
- *          of context.  (With other lists the slots hold wrong tokens.)
+ *          one that tokens of this call come from.  NULL, or page_table
+ *          again: places of page_table itself.  The entries of a list (but for those
+ *          below 0) then ascend, and kept[b][h][i] >= i: the tokens that spin_kv_choose
+ *          names, or the accepted path of a tree behind at[b] tokens of context.
+ *          (With other lists the slots hold wrong tokens.)
  *   W      [n_pages][Hkv][page_size] float32 or NULL: moves with the tokens
  * A token that comes from or goes to a place beyond its table, or a page that is
  * none of the pool, is passed over.  Slots that nothing goes to keep what they hold.

@@ -86,13 +86,16 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* __restrict__ row, 
     return static_cast<uint32_t>(((static_cast<unsigned long long>(hi) << 32) | lo) >> (first & 31));
 }
 
+// Is any of 32 tokens new, the `first` of them counted among the new ones.
+__device__ __forceinline__ bool any_new(int first) { return first > -32; }
+
 // A new token's position, held to what differences of two fit 32 bits with.
 __device__ __forceinline__ int position(const KvAttnArgs& a, int t) { return min(max(a.positions[t], 0), 1 << 30); }
 
 // Masks a row's exponents of N of 32 tokens, the `first` of which is counted among the new ones, by the tree and the
-// window, and puts the bias of new tokens right, which `rel`, the row's position less the lane's first place, has given them
-// by their places.  Exponent e is that of token lane0 + e % 4 + 128 / N (e / 4) of the 32.  One position at a time: all of
-// them at once take registers that the main path lacks.
+// window, and adds the bias where some of them are new: their distances go by their positions, the others' by `rel`, the
+// row's position less the lane's first place.  Exponent e is that of token lane0 + e % 4 + 128 / N (e / 4) of the 32.  One
+// position at a time: all of them at once take registers that the main path lacks.
 template <int SCORES, int N, typename X>
 __device__ __forceinline__ void tree_mask(const KvAttnArgs& a, X& x, int t, bool valid, int first, int lane0, int news, int new0, int pos, int rel,
                                           float slope) {
@@ -108,7 +111,7 @@ __device__ __forceinline__ void tree_mask(const KvAttnArgs& a, X& x, int t, bool
         asm volatile("" ::: "memory");
         const int c = 128 / N * (e >> 2) + (e & 3), i = first + lane0 + c;
         const int far = i >= 0 && i < news ? pos - position(a, new0 + i) : rel - c;
-        if (biased(SCORES)) x[e] = __builtin_fmaf(slope, __builtin_fabsf(static_cast<float>(rel - c)) - __builtin_fabsf(static_cast<float>(far)), x[e]);
+        if (biased(SCORES) && any_new(first)) x[e] = __builtin_fmaf(-slope, __builtin_fabsf(static_cast<float>(far)), x[e]);
         if (a.window > 0)
             x[e] = static_cast<uint32_t>(far) + static_cast<uint32_t>(a.window) - 1u < 2u * static_cast<uint32_t>(a.window) - 1u ? x[e] : -__builtin_inff();
     }
@@ -433,8 +436,9 @@ __global__ __launch_bounds__(64 * WAVES, TREE && BITS == 4 && SCORES == kPlain ?
         fetch_keys(next);
         const float from = SCORES == kFancy || SCORES == kCapped ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * g);
+        const float slope_here = TREE && any_new(st * kStep - fresh) ? 0.0f : slope;       // tree_mask adds it then
         auto exponent = [&](int e, float k, float lm, bool capped) __attribute__((always_inline)) {
-            if (biased(SCORES)) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
+            if (biased(SCORES)) lm = __builtin_fmaf(-slope_here, __builtin_fabsf(rel - static_cast<float>(16 * (e >> 2) + (e & 3))), lm);
             x[e] = SCORES == kWideCap ? capped_wide(x[e] * k, cap.top, cap.rtop) + lm
                                       : capped ? capped_plus(x[e] * k, cap.top, lm) : __builtin_fmaf(x[e], k, lm);
         };
@@ -918,9 +922,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attn_tile(KvAttnArgs a, in
     auto exponents = [&](int j0) __attribute__((always_inline)) {
         const float from = SCORES == kFancy || SCORES == kCapped ? M - cap.top : M;
         const float rel = static_cast<float>(pos - j0 - 4 * hf);
+        const float slope_here = TREE && any_new(j0 - span.base - fresh) ? 0.0f : slope;   // tree_mask adds it then
         auto one = [&](int e, float lm, bool capped) __attribute__((always_inline)) {
             const float k = kf[e >> 2][e & 3];
-            if (biased(SCORES)) lm = __builtin_fmaf(-slope, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
+            if (biased(SCORES)) lm = __builtin_fmaf(-slope_here, __builtin_fabsf(rel - static_cast<float>(8 * (e >> 2) + (e & 3))), lm);
             s[e] = SCORES == kWideCap ? capped_wide(s[e] * k, cap.top, cap.rtop) + lm
                                       : capped ? capped_plus(s[e] * k, cap.top, lm) : __builtin_fmaf(s[e], k, lm);
         };

@@ -116,7 +116,7 @@ __device__ __forceinline__ int over_and_ties(const uint4& u, uint32_t top) {
 // Writes those that stay, in order of places; `overs` and `ties` are how many there are before token p0.  4096 R tokens
 // are 32768 at most, so that their counts fit 16 bits.
 template <int R>
-__device__ __forceinline__ void write_kept(const Head& x, const uint4* u, int p0, uint32_t top, int equal, int overs, int ties, int* sums) {
+__device__ __forceinline__ void write_kept(const KvChooseArgs& a, const Head& x, const uint4* u, int p0, uint32_t top, int equal, int overs, int ties, int* sums) {
     static_assert(R <= 8, "two counts a number, and two of the waves' counts a lane");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int before[R];
@@ -148,7 +148,10 @@ __device__ __forceinline__ void write_kept(const Head& x, const uint4* u, int p0
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool tie = v[e] == top;
-            if (v[e] > top || (tie && left > 0)) x.kept[at++] = j + e;
+            if (v[e] > top || (tie && left > 0)) {
+                if (at < a.keep) x.kept[at] = j + e;         // not behind the list, if the weights change meanwhile
+                ++at;
+            }
             left -= tie;
         }
     }
@@ -182,7 +185,7 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_kernel(KvChooseArgs 
         top |= static_cast<uint32_t>(digit) << digit_shift(d);
         above += greater;
     }
-    write_kept<R>(x, u, 0, top, a.keep - above, 0, 0, sums);
+    write_kept<R>(a, x, u, 0, top, a.keep - above, 0, 0, sums);
 }
 
 // Longer tables: a workgroup for 8192 tokens of a head, and a launch for each step: the counts cleared, then each digit's
@@ -248,7 +251,7 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_part(KvChooseArgs a,
     }
     overs = __builtin_amdgcn_readlane(sums_up_to(overs), 63);
     ties = __builtin_amdgcn_readlane(sums_up_to(ties), 63);
-    write_kept<R>(x, u, p0, top, a.keep - above, overs, ties, sums);
+    write_kept<R>(a, x, u, p0, top, a.keep - above, overs, ties, sums);
 }
 
 bool in_parts(int room) { return room > 32 * kChooseThreads; }

@@ -357,6 +357,11 @@ def test_move(bits, weights, kv_len, Hkv, heads, page, n):
     move(cache, table, kept, W=W)                                                   # to the front of their own pages
     to_table = order[used:used + len(kv_len) * to].reshape(len(kv_len), to).astype(np.int32)
     move(cache, table, kept, to_table=to_table, W=W)
+    c = dev(cache)
+    spin.spin_kv_move(c, dev(table), dev(kept), W=dev(W))
+    again, same = dev(cache), dev(table)
+    spin.spin_kv_move(again, same, dev(kept), to_table=same, W=dev(W))              # its own table: in place
+    assert all(np.array_equal(host(c[k]).view(np.uint8), host(again[k]).view(np.uint8)) for k in c)
     shuffled = kept[:, :, rng.permutation(n)]                                       # any order into other pages
     move(cache, table, shuffled, to_table=to_table, W=W)
 

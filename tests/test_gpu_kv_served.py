@@ -252,6 +252,10 @@ def test_refusals_of_the_binding():
            lambda: choose(keep=0), lambda: choose(W=s["W"][0]), lambda: choose(kv_len=i32(3)), lambda: choose(kept=i32(2, 2, 8)),
            lambda: move(kept=i32(2, 3, 4)), lambda: move(kept=i32(1, 2, 4)), lambda: move(at=i32(3)), lambda: move(to_table=i32(3, 2)),
            lambda: move(W=s["W"][:1])]
+    x = torch.zeros((6, 2, 128), device=DEV)
+    append = lambda **kw: spin.spin_kv_append(None, x, x, s["cache"], s["table"], s["q_start"], s["kv"], **kw)  # noqa: E731
+    append(positions=at)
+    bad += [lambda: append(positions=at, pos0=3), lambda: append(positions=i32(5)), lambda: append(positions=at[None])]
     for call in bad:
         with pytest.raises(ValueError):
             call()

@@ -244,6 +244,22 @@ def test_any_bits(work):
 
 
 @pytest.mark.parametrize("work", WORK)
+def test_a_bias_of_positions_far_from_places(work):
+    """As behind a cache that tokens have left: new tokens' biases are those of their distances, whatever their places."""
+    rng = np.random.default_rng(12)
+    q_len, kv_len, page = [70, 40], [70, 40], 16                # no context: distances go by positions alone
+    q_start, cache, table = starts(q_len), pool(rng, 9, 2, page, 4), tables(rng, kv_len, page, 9)
+    table = widened(table, 440, 2, page, work)
+    tree, at = oracle.kv_tree(drafts(rng, q_len), q_start, kv_len, 3, 1 << 24)
+    q = rng.standard_normal((110, 8, 128)).astype(np.float16)
+    slopes = (2.0 ** -np.arange(8)).astype(np.float32)
+    for more in ({}, dict(softcap=20.0), dict(softcap=500.0, window=3)):
+        ref, bound = oracle.kv_attend(q, cache, table, q_start, kv_len, 0.1, tree=tree, positions=at, slopes=slopes, **more)
+        got, _ = run(q, cache, table, q_start, kv_len, tree, at, scale=0.1, slopes=slopes, **more)
+        close(got, ref, bound)
+
+
+@pytest.mark.parametrize("work", WORK)
 @pytest.mark.parametrize("which,bad", [("K_scale", np.nan), ("V_scale", np.inf), ("K_scale", -np.inf), ("V_scale", np.nan)])
 def test_scales_that_are_not_finite(work, which, bad):
     """A drafted token's: its descendants are NaN, and their logarithms not finite; others are not touched."""
