@@ -1,8 +1,9 @@
 /*
  * libspin — the online hot path of SpinQuant (arXiv 2405.16406) on AMD
  * Instinct MI355X (gfx950): Hadamard rotations applied online, symmetric INT4
- * quantization of activations / KV vectors, INT4 x INT4 GEMM, and the offline
- * fold of a rotation into a weight.
+ * quantization of activations / KV vectors, INT4 x INT4 GEMM, the offline
+ * fold of a rotation into a weight, and a paged quantized KV cache with its
+ * attention, drafted trees and eviction.
  *
  * Where each operation comes from (page "SpinQuant, Reproduced"):
  *   - Q1, Q5 "Method 1/2": a pre-norm transformer is invariant to an
@@ -17,7 +18,8 @@
  * Conventions shared by every call
  *   - Tensor pointers are DEVICE pointers to row-major, contiguous memory,
  *     allocated and freed by the caller; the library never allocates, frees
- *     or keeps them.  Every tensor pointer must be 16-byte aligned.
+ *     or keeps them.  Every tensor pointer must be 16-byte aligned (4 bytes
+ *     suffice for the tables and lists of spin_kv_move).
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).
  *     Calls validate their arguments on the host, enqueue kernels on `stream`
  *     and return without synchronising; device faults surface at the caller's

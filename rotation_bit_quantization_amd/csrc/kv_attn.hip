@@ -1,4 +1,4 @@
-// spin_kv_attn / spin_kv_attn_shared kernels: attention over the paged INT4 or
+// spin_kv_attn / spin_kv_attn_shared / spin_kv_attn_ex kernels: attention over the paged INT4 or
 // INT8 KV cache (the abstract's 4-bit KV cache; page "SpinQuant, Reproduced",
 // Q5: queries and keys both carry R3, so their products are unchanged).
 //
@@ -14,6 +14,12 @@
 // 2^-11 relative, of each weight; a weight below 2^-14 is off by up to 2^-25, at most 2^-25 of the largest.  Scores,
 // maxima and sums are float32; exponentials, logarithms and reciprocals are the hardware's, off by a unit in the last
 // place, 2^-23, which the rounding of the weights passes by far.
+//
+// With a tree a row sees the context and, of its sequence's new tokens, those that its bits name.  Only steps that hold new
+// tokens look at them (tree_mask).  Measured with 32 + 8 heads: a tree of 16 tokens on 1000, INT4, 12 us; 16 of 60 on 4096
+// 102 - 112 us (as many rows in order 102 - 107), INT8 and capped 134 (134); 64 of 8 on 2000 54 (55).
+//
+// A row's log sum e^z is M and the sum of w_j / vs_j, which attention divides by, together.
 //
 // Both products are computed transposed: S^T = A Q^T leaves a lane with one
 // query and four tokens of a tile of 16, which is what the second product O^T =

@@ -5,7 +5,8 @@
 // position is the context's end plus its depth, the row's bits less one.
 //
 // Bound: the launch, and a chain of loads as long as the tree is deep, from L1: a
-// sequence's parents are a few cache lines.  16 lanes walk the same chain and
+// sequence's parents are a few cache lines.  Measured: 64 trees of 60 tokens 3.6
+// us, 5 of 1337 together 4.7.  16 lanes walk the same chain and
 // hold the row's words, so that a row is written once.
 #include "kv_batch.h"
 #include "spin_internal.h"
