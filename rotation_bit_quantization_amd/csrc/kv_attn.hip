@@ -515,6 +515,7 @@ __global__ __launch_bounds__(64 * WAVES, TREE && BITS == 4 && SCORES == kPlain ?
     if (low > 0.0f) M = -__builtin_inff();     // no token seen
 
     // join the waves
+    asm volatile("" ::"s"(a.lse));             // read now: behind the sums everything would wait for it
     l_sum = sum_over_groups(l_sum);
     if (g == 0) m_sh[wave][n] = M;
     __syncthreads();
@@ -1199,6 +1200,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv_attn_join(KvAttnArgs a, int s
     const int b = find_last64(a.B, lane, [&](int i) { return a.q_start[i] <= t; });
     if (t < a.q_start[b] || t >= a.q_start[b + 1]) return;
     const float* row = a.partial + at * kPartial;
+    asm volatile("" ::"s"(a.lse));             // read now: behind the sums everything would wait for it
     float M = -__builtin_inff(), l = 0.0f;
     f2 o = {};
     for (int s0 = 0; s0 < splits; s0 += 64) {
