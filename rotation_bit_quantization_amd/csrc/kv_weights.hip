@@ -39,8 +39,8 @@ constexpr int kTilesWanted = 256;
 // prompt of 2000 takes 204 us in one share, 37 in up to 16, one of 500 59 and 15.
 constexpr int kSharesWanted = 4096, kLeastTiles = 4, kMostShares = 16;
 constexpr int kCounted = 256;              // sequences up to which their chunks are counted
-// Groups that a wave takes, where there are enough for it (64 sequences on up to 8192 tokens 61 us with one, 47 with four,
-// 53 with twelve), and what enough is.
+// Groups that a wave takes, where there are enough for it (64 sequences on up to 8192 tokens, 16 rows at a time, 61 us with
+// one, 47 with four, 53 with twelve), and what enough is.
 constexpr int kMostTurns = 4, kGroupsEnough = 8192;
 
 // What a row adds to tokens, as the kernels hold it: its position, the logarithm in units of log2 (infinite where it adds
@@ -63,13 +63,49 @@ __device__ __forceinline__ Row row_of(const KvWeightsArgs& a, int r, bool valid,
     return row;
 }
 
-// A product to the exponent of its weight.
-template <int SCORES>
-__device__ __forceinline__ float exponent(const KvWeightsArgs& a, const Cap& cap, float s, float kf, float lse2, float slope, int pos, int p) {
-    if (SCORES == kPlain) return __builtin_fmaf(s, kf, -lse2);
-    const float lm = __builtin_fmaf(-slope, __builtin_fabsf(static_cast<float>(pos - p)), -lse2);
-    if (SCORES == kWideCap) return capped_wide(s * kf, cap.top, cap.rtop) + lm;
-    return a.softcap > 0.0f ? capped_plus(s * kf, cap.top, lm + cap.top) : __builtin_fmaf(s, kf, lm);
+// What a kernel does to the scores here: nothing, a bias, or (kWideCap) a cap, with or without a bias.
+//
+// A capped score is z tanh(u) / u with u = z / cap.  Up to |u| = sqrt(1/2) the ratio is a polynomial of degree 5 in u^2,
+// fitted to the least relative error, 2^-24.7, six multiply-adds and no transcendental; above the exponential's form, whose
+// error is of the cap's size, ten of 2^-24, and then of the score's too.  Attention's form for caps up to 64 is off by that
+// at any score, which fp32 weights show (cap 30 and 50: errors of weights 1.1e-6 in place of 4e-7).
+constexpr float kNear = 0.70710678f;       // of |u|
+__device__ __forceinline__ float capped_near(float z, float rtop, float lm) {
+    const float u = z * rtop, t = u * u;
+    float p = __builtin_fmaf(t, -0.005034888628870249f, 0.01996474526822567f);
+    p = __builtin_fmaf(p, t, -0.05350292846560478f);
+    p = __builtin_fmaf(p, t, 0.13328056037425995f);
+    p = __builtin_fmaf(p, t, -0.3333311080932617f);
+    p = __builtin_fmaf(p, t, 1.0f);
+    return __builtin_fmaf(z, p, lm);
+}
+__device__ __forceinline__ float capped_any(float z, const Cap& cap, float lm) {
+    const float u = z * cap.rtop;
+    const float far = __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(u * (2.0f * kLog2e)) + 1.0f), -2.0f * cap.top, cap.top + lm);
+    return __builtin_fabsf(u) <= kNear ? capped_near(z, cap.rtop, lm) : far;
+}
+
+// N scores, held in s as products and left there as exponents of weights: `factor` of the products, `lm` added to a score.
+template <int SCORES, int N, typename S, typename Less>
+__device__ __forceinline__ void exponents(const Cap& cap, S& s, float factor, Less lm) {
+    if (SCORES != kWideCap) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = __builtin_fmaf(s[e], factor, lm(e));
+        return;
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        s[e] *= factor;
+        top = __builtin_fmaxf(top, __builtin_fabsf(s[e]));
+    }
+    if (__ballot(!(top * cap.rtop <= kNear)) == 0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = capped_near(s[e], cap.rtop, lm(e));
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = capped_any(s[e], cap, lm(e));
+    }
 }
 
 __device__ __forceinline__ bool sees(const KvWeightsArgs& a, int pos, int p, int both) {
@@ -108,13 +144,15 @@ __device__ __forceinline__ unsigned long long place_of(const KvWeightsArgs& a, i
 
 __device__ __forceinline__ float scale_of(uint32_t raw) { return __half2float(__ushort_as_half(static_cast<unsigned short>(raw))); }
 
-// Few rows: 16 at a time, groups of 64 tokens in turn, the next one's keys in flight.
+// Few rows: 4 N at a time (N is 1, 2 or 4), groups of 64 tokens in turn, the next one's keys in flight.  A lane's results
+// are N rows of a token: rows stand in the matrix cores' operand so that its four places hold rows g, g + 4, ..
 //
 // Bound: reading the keys, 16 BITS + 2 bytes a token and head, from the second round of workgroups on; before that loads
-// that wait for each other (length, page, keys).  Measured: 64 single tokens of 32 + 8 heads on 2000 to 8192, INT4, 47 us
-// (189 MB, 4.0 TB/s), INT8 83; on 5120 each 4.3 TB/s; 16 on 2000 to 8192 17 us, one on 30000 6.5, one on 1000 4.5.
-template <int BITS, int SCORES>
-__global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_rows16(KvWeightsArgs a, int chunks, int turns) {
+// that wait for each other (length, page, keys).  Measured: 64 single tokens of 32 + 8 heads on 2000 to 8192, INT4, 44 us
+// from the last-level cache and 51 from memory (189 MB, 3.7 TB/s), capped 53, INT8 83; 16 on 2000 to 8192 16 us, one on 30000
+// 6, one on 1000 4.5.  With 16 rows at a time whatever there is, capped 65.  Five waves a SIMD spill (62 us).
+template <int BITS, int SCORES, int N>
+__global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4 : 3) void kv_weights_rows16(KvWeightsArgs a, int chunks, int turns) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int G = a.Hq / a.Hkv;
@@ -186,11 +224,12 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_
     };
 
     h8 q[4];
-    float less[4], slopes[4];
-    int where[4], loaded = -1;
+    float less[N], slopes[N];
+    int where[N];
     auto load_rows = [&](int r0, int row_end) __attribute__((always_inline)) {
-        // lane (n, g): values 32 g .. 32 g + 31 of row n, in the order of the keys' codes
-        const Row row = row_of<SCORES>(a, r0 + n, r0 + n < row_end, q0, start, h, G);
+        // lane (n, g): values 32 g .. 32 g + 31 of row n / 4 + 4 (n % 4), in the order of the keys' codes
+        const int r = r0 + (n >> 2) + 4 * (n & 3);
+        const Row row = row_of<SCORES>(a, r, r < row_end && (n & 3) < N, q0, start, h, G);
         const bool counts = row.lse2 < __builtin_inff();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -202,18 +241,17 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_
             q[j] = f.v;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < N; ++e) {
             less[e] = __shfl(row.lse2, 4 * g + e, 64);
             slopes[e] = SCORES != kPlain ? __shfl(row.slope, 4 * g + e, 64) : 0.0f;
             where[e] = __shfl(row.pos, 4 * g + e, 64);
         }
-        loaded = r0;
     };
 
     const int groups = min(turns, (tokens - first + kWeightWaves * kGroup - 1) / (kWeightWaves * kGroup));
     Raw raw = fetch(0);
     const int rows = news * G;
-    if (rows <= 16) load_rows(0, rows);
+    if (rows <= 4 * N) load_rows(0, rows);
     for (int t = 0; t < groups; ++t) {
         const int j0 = first + t * kWeightWaves * kGroup, last = min(j0 + kGroup, tokens) - 1;
         // a row that sees a scale that is not finite has no weights
@@ -229,15 +267,15 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_
         if (t + 1 < groups) next = fetch(t + 1);
         const Range on = rows_on(a, a.pos0 + j0, a.pos0 + last, start, news, both);
         const int row_end = on.hi * G;
-        for (int r0 = rows <= 16 ? 0 : on.lo * G; r0 < row_end; r0 += 16) {
-            if (rows > 16) load_rows(r0, row_end);
-            // unpacked anew for every 16 rows: kept, the operands of 64 tokens take 64 registers
+        for (int r0 = rows <= 4 * N ? 0 : on.lo * G; r0 < row_end; r0 += 4 * N) {
+            if (rows > 4 * N) load_rows(r0, row_end);
+            const bool whole = all_seen(a, start + r0 / G, start + (min(r0 + 4 * N, rows) - 1) / G, a.pos0 + j0, a.pos0 + last, both);
+            // unpacked anew for these rows: kept, the operands of 64 tokens take 64 registers
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int x = 0; x < BITS; ++x) asm("" : "+v"(raw.k[i][x]));
             }
-            const bool whole = all_seen(a, start + r0 / G, start + (min(r0 + 16, rows) - 1) / G, a.pos0 + j0, a.pos0 + last, both);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f4 s = {};
@@ -245,16 +283,16 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 ? 4 : 3) void kv_weights_
                 for (int j = 0; j < 4; ++j)
                     s = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[j], key_operand<BITS>(raw.k[i] + j * (BITS / 4)), s, 0, 0, 0);
                 const int p = a.pos0 + j0 + 16 * i + n;      // the token's position
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = exponent<SCORES>(a, cap, s[e], kf[i], less[e], slopes[e], where[e], p);
+                exponents<SCORES, N>(cap, s, kf[i], [&](int e) __attribute__((always_inline)) {
+                    return SCORES == kPlain ? -less[e] : __builtin_fmaf(-slopes[e], __builtin_fabsf(static_cast<float>(where[e] - p)), -less[e]);
+                });
                 if (!whole) {
-                    asm volatile("" ::: "memory");     // keeps this a branch
+                    asm volatile("" ::: "memory");           // keeps this a branch
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = sees(a, where[e], p, both) ? x[e] : -__builtin_inff();
+                    for (int e = 0; e < N; ++e) s[e] = sees(a, where[e], p, both) ? s[e] : -__builtin_inff();
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i] += __builtin_amdgcn_exp2f(x[e]);
+                for (int e = 0; e < N; ++e) acc[i] += __builtin_amdgcn_exp2f(s[e]);
             }
         }
         // lane l has token l
@@ -278,10 +316,10 @@ constexpr int kTileRows = 32;
 // takes all rows past them.
 //
 // Bound: the vector work of the weights beside the matrix work, 24 cycles (a multiply-add, an exponential, an addition) of
-// 64 scores against 16, with a cap and a bias 72, and what staging 32 rows takes.  A token's sum is carried with what its
+// 64 scores against 16, with a cap and a bias 66, and what staging 32 rows takes.  A token's sum is carried with what its
 // additions have lost, 32 rows at a time, so that it is as exact for a long prompt as for a row.  Measured with 32 + 8 heads
 // and INT4: a prompt of 8192 tokens 320 us (0.86 PFLOP/s), of 2000 37, 32 tokens each of two on 16384 21; three prompts of
-// 1670, 32 + 32 heads, INT8, capped and biased, 125.
+// 1670, 32 + 32 heads, INT8, capped and biased, 119.
 template <int BITS, int SCORES, int M>
 __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsArgs a, int splits) {
     struct Stage {
@@ -387,7 +425,7 @@ __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsAr
             sh[buf].q[s_row * 17 + s_chunk + 8 * x] = u4{out.w[0], out.w[1], out.w[2], out.w[3]};
         }
         if (s_chunk == 0) {
-            reinterpret_cast<float*>(sh[buf].less)[s_row] = (SCORES == kFancy ? cap.top : 0.0f) - raw.lse2;
+            reinterpret_cast<float*>(sh[buf].less)[s_row] = -raw.lse2;
             if (SCORES != kPlain) reinterpret_cast<float*>(sh[buf].slope)[s_row] = raw.slope;
             reinterpret_cast<float*>(sh[buf].pos)[s_row] = static_cast<float>(raw.pos - i0);
         }
@@ -419,24 +457,12 @@ __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsAr
                 const int p = a.pos0 + j0 + 32 * m + n;
                 const float at = static_cast<float>(p - pmin);
                 float w[4] = {};
-                auto exponents = [&](bool capped) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {      // rows 8 i + 4 hf .. + 3
-                        const f4 less = sh[buf].less[2 * i + hf], slope = SCORES != kPlain ? sh[buf].slope[2 * i + hf] : f4{},
-                                 pos = SCORES != kPlain ? sh[buf].pos[2 * i + hf] : f4{};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float z = s[m][4 * i + e];
-                            const float lm = SCORES != kPlain ? __builtin_fmaf(-slope[e], __builtin_fabsf(pos[e] - at), less[e]) : less[e];
-                            s[m][4 * i + e] = SCORES == kWideCap ? capped_wide(z * kf[m], cap.top, cap.rtop) + lm
-                                              : capped ? capped_plus(z * kf[m], cap.top, lm) : __builtin_fmaf(z, kf[m], lm);
-                        }
-                    }
-                };
-                if (SCORES == kFancy && a.softcap > 0.0f)
-                    exponents(true);
-                else
-                    exponents(false);
+                exponents<SCORES, 16>(cap, s[m], kf[m], [&](int e) __attribute__((always_inline)) {
+                    const int i = 2 * (e >> 2) + hf;       // rows 8 (e / 4) + 4 hf .. + 3
+                    const float less = sh[buf].less[i][e & 3];
+                    return SCORES == kPlain ? less
+                                            : __builtin_fmaf(-sh[buf].slope[i][e & 3], __builtin_fabsf(sh[buf].pos[i][e & 3] - at), less);
+                });
                 if (!whole) {
                     asm volatile("" ::: "memory");     // keeps this a branch
 #pragma unroll
@@ -489,6 +515,7 @@ __global__ __launch_bounds__(kWeightThreads) void kv_weights_join(KvWeightsArgs 
 struct Plan {
     bool tile;
     int m, splits;                 // tiles: 32-token operands of a wave, shares of the rows
+    int n;                         // few rows: four times as many at a time
     int turns;                     // few rows: groups that a wave takes, several where there are workgroups enough
 };
 
@@ -504,6 +531,7 @@ Plan plan(int T, int Hq, int Hkv, int B, int room, bool plain) {
         p.splits = static_cast<int>(splits < 1 ? 1 : splits > kMostShares ? kMostShares : splits);
     } else {
         const long long turns = heads * ((room + kGroup - 1) / kGroup) / kGroupsEnough;
+        p.n = rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
         p.turns = static_cast<int>(turns < 1 ? 1 : turns > kMostTurns ? kMostTurns : turns);
     }
     return p;
@@ -514,23 +542,31 @@ hipError_t launch_scores(const KvWeightsArgs& a, const Plan& p, hipStream_t s) {
     const int room = a.max_pages << a.page_log2;
     if (p.tile) {
         const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv * p.splits * ((room + 128 * p.m - 1) / (128 * p.m)));
-        if (p.m == 2)
-            hipLaunchKernelGGL((kv_weights_tile<BITS, SCORES, 2>), grid, dim3(kWeightThreads), 0, s, a, p.splits);
-        else
-            hipLaunchKernelGGL((kv_weights_tile<BITS, SCORES, 1>), grid, dim3(kWeightThreads), 0, s, a, p.splits);
+        if constexpr (SCORES == kPlain) {
+            if (p.m == 2) {
+                hipLaunchKernelGGL((kv_weights_tile<BITS, SCORES, 2>), grid, dim3(kWeightThreads), 0, s, a, p.splits);
+                return hipGetLastError();
+            }
+        }
+        hipLaunchKernelGGL((kv_weights_tile<BITS, SCORES, 1>), grid, dim3(kWeightThreads), 0, s, a, p.splits);
         return hipGetLastError();
     }
     const int chunk = kWeightWaves * kGroup * p.turns, chunks = (room + chunk - 1) / chunk;
     const long long items = static_cast<long long>(a.B) * chunks;
     const dim3 grid(static_cast<unsigned>((items + 7) / 8 * 8 * a.Hkv));
-    hipLaunchKernelGGL((kv_weights_rows16<BITS, SCORES>), grid, dim3(kWeightThreads), 0, s, a, chunks, p.turns);
+    if (p.n == 1)
+        hipLaunchKernelGGL((kv_weights_rows16<BITS, SCORES, 1>), grid, dim3(kWeightThreads), 0, s, a, chunks, p.turns);
+    else if (p.n == 2)
+        hipLaunchKernelGGL((kv_weights_rows16<BITS, SCORES, 2>), grid, dim3(kWeightThreads), 0, s, a, chunks, p.turns);
+    else
+        hipLaunchKernelGGL((kv_weights_rows16<BITS, SCORES, 4>), grid, dim3(kWeightThreads), 0, s, a, chunks, p.turns);
     return hipGetLastError();
 }
 
 template <int BITS>
 hipError_t launch_bits(const KvWeightsArgs& a, const Plan& p, hipStream_t s) {
-    if (a.softcap > kNearCap) return launch_scores<BITS, kWideCap>(a, p, s);
-    return a.softcap > 0.0f || a.slopes ? launch_scores<BITS, kFancy>(a, p, s) : launch_scores<BITS, kPlain>(a, p, s);
+    if (a.softcap > 0.0f) return launch_scores<BITS, kWideCap>(a, p, s);
+    return a.slopes ? launch_scores<BITS, kFancy>(a, p, s) : launch_scores<BITS, kPlain>(a, p, s);
 }
 
 }  // namespace
