@@ -674,6 +674,9 @@ spin_status spin_kv_attn_ex(const uint16_t* Q, int T, int Hq, int Hkv, int D, in
  *   workspace  device memory of the bytes spin_kv_weights_workspace names (it may
  *            be NULL if that is 0); its content before and after means nothing, and
  *            calls that overlap need one each
+ * Rows are a sequence's last tokens, in order, or some of its last ones.  Of a
+ * drafted tree the accepted rows are passed, behind spin_kv_move: the logarithms
+ * that the tree's attention left for them are the plain sequence's.
  * A row whose lse is not finite adds nothing, and a token whose scale is not finite
  * draws nothing.  Sums are float32, in an order that goes by the sizes alone.  A page
  * may stand in one table of the batch only.  T == 0 is valid: W = decay * prior.
@@ -736,6 +739,8 @@ spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_siz
  *          names, or the accepted path of a tree behind at[b] tokens of context.
  *          (With other lists the slots hold wrong tokens.)
  *   W      [n_pages][Hkv][page_size] float32 or NULL: moves with the tokens
+ * A page that tokens go to may stand in one table of the call only; another sequence
+ * that reads it (a shared prefix in the tables) sees what is moved there.
  * A token that comes from or goes to a place beyond its table, or a page that is
  * none of the pool, is passed over.  Slots that nothing goes to keep what they hold.
  * Position rotations are in the keys, so that a token keeps its position wherever it
