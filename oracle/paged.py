@@ -151,7 +151,7 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
                 p = prefix_len + _length(kv_len[b]) - int(q_start[b + 1]) + t
                 seen, at = there.copy(), j
                 if tree is not None:
-                    names, at, p = _tree_row(tree, positions, t, q_start, b, prefix_len + _length(kv_len[b]), j)
+                    names, at, p = _tree_row(tree, positions, t, q_start, b, prefix_len, _length(kv_len[b]), j)
                     seen &= names
                 elif causal:
                     seen &= (j <= p) | (j < (bidir_len[b] if bidir_len is not None else 0))
@@ -189,20 +189,22 @@ def kv_attend(q, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None,
     return (out, bound, logs, log_bound) if sums else (out, bound)
 
 
-def _tree_row(tree, positions, t, q_start, b, end, j):
-    """Which of the tokens j of sequence b, which ends at ``end``, row t names, their positions and its own."""
+def _tree_row(tree, positions, t, q_start, b, prefix_len, kv, j):
+    """Which of the tokens j, a prefix and the kv of sequence b behind it, row t names, their positions and its own.
+    A prefix's tokens are context, also where the sequence has fewer tokens than rows."""
     news = int(q_start[b + 1]) - int(q_start[b])
-    i = j - (end - news)
+    i = np.where(j < prefix_len, -1, j - (prefix_len + kv - news))
     bits = np.unpackbits(np.ascontiguousarray(tree[t]).view(np.uint8), bitorder="little").astype(bool)
     names = i < 0
     inside = (i >= 0) & (i < min(len(bits), news))
     names[inside] = bits[i[inside]]
     if positions is None:
         return names, j, 0
+    held = lambda rows: np.clip(np.asarray(positions)[rows], 0, 1 << 30)  # noqa: E731
     at = np.array(j)
     fresh = (i >= 0) & (i < news)
-    at[fresh] = positions[int(q_start[b]) + i[fresh]]
-    return names, at, int(positions[t])
+    at[fresh] = held(int(q_start[b]) + i[fresh])
+    return names, at, int(held(t))
 
 
 def kv_tree(parent, q_start, kv_len, words, pos0=0):

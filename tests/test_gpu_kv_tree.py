@@ -210,6 +210,16 @@ def test_shared_prefix(work, q_len, kv_len, Hq, Hkv, prefix, more):
 
 
 @pytest.mark.parametrize("work", WORK)
+@pytest.mark.parametrize("more", [{}, dict(window=7), dict(window=30, alibi=True)])
+def test_a_prefix_and_more_rows_than_tokens(work, more):
+    """New tokens without a place are not the prefix's last: that is seen, at its own places."""
+    rng = np.random.default_rng(13)
+    check(rng, [9, 39, 23, 5], [200, 72, 10, 0], 6, 3, 8, 16, work, before=1, behind=1, prefix_len=17, **more)
+    check(rng, [9, 70], [9, 3], 4, 1, 4, 32, work, prefix_len=500, most=20, **more)
+    check(rng, [9, 40], [9, 25], 4, 1, 4, 32, work, **more)     # positions below 0 are held to 0
+
+
+@pytest.mark.parametrize("work", WORK)
 def test_rows_that_see_nothing(work):
     """No context, and a row of zeros: zeros, and a logarithm of minus infinity; with a context they see that."""
     rng = np.random.default_rng(5)

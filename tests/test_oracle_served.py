@@ -46,6 +46,19 @@ def test_a_path_of_a_tree_is_a_sequence():
                     assert np.allclose(logs[t, g], torch.logsumexp(z, 0))
 
 
+def test_a_prefix_is_context_where_rows_outnumber_tokens():
+    """Three of five new tokens have no place: their bits say nothing, and the prefix is seen all the same."""
+    cache, n, kv, prefix = small(), 5, 2, 20
+    q = rng.standard_normal((n, 4, 128))
+    tree, at = oracle.kv_tree([-1, 0, 1, 2, 3], [0, n], [kv], 1, prefix)
+    tree[3] = 0
+    O, _ = oracle.kv_attend(q, cache, np.array([[3]]), [0, n], [kv], 0.05, tree=tree, positions=at, prefix_table=[0, 1], prefix_len=prefix)
+    last, _ = oracle.kv_attend(q[[4]], cache, np.array([[3]]), [0, 1], [kv], 0.05, prefix_table=[0, 1], prefix_len=prefix)
+    assert np.allclose(O[4], last[0])
+    alone, _ = oracle.kv_attend(q[[3]], cache, np.array([[3]]), [0, 1], [0], 0.05, causal=False, prefix_table=[0, 1], prefix_len=prefix)
+    assert np.allclose(O[3], alone[0])
+
+
 def test_weights_are_the_columns_of_softmax():
     cache, table, kv, n = small(), np.array([[2, 0, 4]]), 40, 7
     q = rng.standard_normal((n, 4, 128)).astype(np.float16)
