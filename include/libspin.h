@@ -734,8 +734,9 @@ spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_siz
  *          are passed over.  at [B] int32, NULL for 0.
  *   to_table   [B][to_pages] int32: the pages that it goes to, none of which may be
  *          one that tokens of this call come from.  NULL, or page_table
- *          again: places of page_table itself.  The entries of a list (but for those
- *          below 0) then ascend, and kept[b][h][i] >= i: the tokens that spin_kv_choose
+ *          again: places of page_table itself; with B == 1 to_pages may then differ from
+ *          max_pages (the first pages of the row alone).  The entries of a list (but for
+ *          those below 0) then ascend, and kept[b][h][i] >= i: the tokens that spin_kv_choose
  *          names, or the accepted path of a tree behind at[b] tokens of context.
  *          (With other lists the slots hold wrong tokens.)
  *   W      [n_pages][Hkv][page_size] float32 or NULL: moves with the tokens
@@ -747,7 +748,8 @@ spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_siz
  * lies; what attention takes from places (windows, distances, causal order among new
  * tokens) goes by the new ones.
  * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (bits), SPIN_ERR_BAD_SHAPE (also more
- * than 2^24 - 1 groups of 64 tokens of a head), SPIN_ERR_MISALIGNED (16 bytes; 4
+ * than 2^24 - 1 groups of 64 tokens of a head, and page_table again for several
+ * sequences with another number of pages), SPIN_ERR_MISALIGNED (16 bytes; 4
  * for page_table, kept, at and to_table, which are cut out of longer lists).
  */
 spin_status spin_kv_move(uint8_t* K_codes, uint16_t* K_scale, uint8_t* V_codes, uint16_t* V_scale, float* W, int Hkv,

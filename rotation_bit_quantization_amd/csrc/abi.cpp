@@ -644,7 +644,11 @@ spin_status spin_kv_move(uint8_t* K_codes, uint16_t* K_scale, uint8_t* V_codes, 
     for (const int32_t* p : {page_table, kept, at, to_table})
         if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return SPIN_ERR_MISALIGNED;
     if (B == 0 || n == 0) return SPIN_OK;
-    if (to_table == page_table && to_pages == max_pages) to_table = nullptr;       // in place
+    // In place, where lists have to be followed in order: page_table again, of which one sequence's row may be cut short.  Of
+    // several sequences rows of another length are other tables in the same memory.
+    if (to_table == page_table && to_pages != max_pages && B > 1) return SPIN_ERR_BAD_SHAPE;
+    if (to_table == page_table) to_table = nullptr;
+    else if (!to_table) to_pages = max_pages;
     return from_hip(spin::launch_kv_move({K_codes, K_scale, V_codes, V_scale, W, Hkv, n_pages,
                                           __builtin_ctz(static_cast<unsigned>(page_size)), B, page_table, max_pages, kept,
                                           kept_heads, n, at, to_table, to_pages}, bits, static_cast<hipStream_t>(stream)));

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_move_kernel(KvMoveArgs a, int c
         const long long i = static_cast<long long>(chunk + turn) * kTokens + threadIdx.x;
         const int src = i < a.n ? list[i] : -1;
         long long from = src >= 0 ? token(a.page_table, a.max_pages, at + src) : -1;
-        const long long to = src >= 0 ? token(a.to_table ? a.to_table : a.page_table, a.to_table ? a.to_pages : a.max_pages, at + i) : -1;
+        const long long to = src >= 0 ? token(a.to_table ? a.to_table : a.page_table, a.to_pages, at + i) : -1;
         if (to < 0 || to == from) from = -1;
         from_sh[turn % 3][threadIdx.x] = from;
         to_sh[turn % 3][threadIdx.x] = to;

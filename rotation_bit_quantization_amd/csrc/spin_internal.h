@@ -170,7 +170,7 @@ struct KvMoveArgs {
     int kept_heads, n;             // 1 or Hkv
     const int32_t* at;             // or NULL: 0
     const int32_t* to_table;       // NULL: page_table, in place
-    int to_pages;
+    int to_pages;                  // of to_table; in place, those of page_table that tokens may go to
 };
 bool kv_move_fits(int Hkv, int B, int n);
 hipError_t launch_kv_move(const KvMoveArgs& a, int bits, hipStream_t s);

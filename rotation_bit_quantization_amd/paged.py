@@ -171,7 +171,7 @@ def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, le
 def spin_kv_move(cache, page_table, kept, at=None, to_table=None, W=None, stream=None):
     """The tokens at places ``at`` + ``kept`` [B, 1 or Hkv, n] int32 of each sequence go to places ``at`` + 0, 1, .. of its
     pages, or of those that ``to_table`` names, with their weights ``W`` if given; entries below 0 are passed over.
-    Returns ``cache``."""
+    ``to_table`` may be ``page_table`` itself, of one sequence also its first pages alone.  Returns ``cache``."""
     if stream is not None:
         return _on_stream(stream, kept, spin_kv_move, cache, page_table, kept, at, to_table, W)
     dev = _gpu(kept, "kept")

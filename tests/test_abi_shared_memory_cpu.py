@@ -1,0 +1,37 @@
+"""Tensors of one call in the same memory, without a GPU: what is refused, before any device call (fake, never dereferenced
+pointers), also under the host sanitizers."""
+
+import os
+import sys
+
+import pytest
+
+from rotation_bit_quantization_amd import spin
+
+from .test_abi_paged_cpu import A, ROOT, caller
+from .test_abi_served_cpu import lib  # noqa: F401
+
+
+def test_a_move_within_rows_of_another_length(lib):  # noqa: F811
+    """Of several sequences rows of another length in page_table's memory are other pages, which may be those that tokens
+    come from."""
+    call = caller(lib.spin_kv_move, dict(kc=A, ks=A, vc=A, vs=A, W=A, Hkv=8, D=128, bits=4, n_pages=10, page=16, B=3, table=A, max_pages=5,
+                                         kept=A, heads=8, n=100, at=A, to=A, to_pages=2, st=None))
+    assert call() == call(to_pages=9) == call(heads=1, W=None) == spin.SPIN_ERR_BAD_SHAPE
+    assert call(n=0) == call(B=0) == spin.SPIN_OK
+
+
+def test_under_host_sanitizers():
+    if os.environ.get("SPIN_LIBRARY"):
+        pytest.skip("already the sanitized library")
+    from rotation_bit_quantization_amd import build
+    from .test_host_sanitizers import _run
+    if not os.path.exists(os.path.join(ROOT, "rotation_bit_quantization_amd", "libspin.so")):
+        pytest.skip("libspin.so not built")
+    try:
+        library, runtime = build.build_host_sanitized(), build.sanitizer_runtime()
+    except RuntimeError as e:
+        pytest.skip(f"host sanitizer build unavailable: {e}")
+    out = _run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider", os.path.join("tests", "test_abi_shared_memory_cpu.py")],
+               {"LD_PRELOAD": runtime, "SPIN_LIBRARY": library})
+    assert " passed" in out and " failed" not in out
