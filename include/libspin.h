@@ -20,6 +20,8 @@
  *     allocated and freed by the caller; the library never allocates, frees
  *     or keeps them.  Every tensor pointer must be 16-byte aligned (4 bytes
  *     suffice for the tables and lists of spin_kv_move).
+ *   - What a call writes lies apart from what it reads and from what else it
+ *     writes, unless the call says that the two may be the same.
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).
  *     Calls validate their arguments on the host, enqueue kernels on `stream`
  *     and return without synchronising; device faults surface at the caller's
@@ -705,16 +707,17 @@ spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pag
  *          `recent` tokens are always among them (first + recent <= keep)
  *   kept   [B][Hkv][keep] int32   OUTPUT: their places, ascending, -1 behind the
  *          places of a sequence that has no more than keep tokens (all stay)
- *   lens   [B] int32   OUTPUT: how many stay, min(kv_len[b], keep)
+ *   lens   [B] int32   OUTPUT: how many stay, min(kv_len[b], keep); kv_len itself is
+ *          allowed (the lengths are then replaced, in a launch of their own)
  * Of equal weights the lowest place stays (-0 equals 0).  NaN, and a token
  * that lies in no page of the pool, are below all weights.
  *   workspace  device memory of the bytes spin_kv_choose_workspace names (it may be
  *          NULL if that is 0); its content before and after means nothing, and calls
  *          that overlap need one each
- * Errors: SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE (also a workspace that is too small, and
- * more than 2^22 - 1 sequences times heads, of tables above 32768 tokens a third of
- * that, or as many times 8192 tokens),
- * SPIN_ERR_MISALIGNED.
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (lens that overlaps kv_len in part),
+ * SPIN_ERR_BAD_SHAPE (also a workspace that is too small, and more than 2^22 - 1
+ * sequences times heads, of tables above 32768 tokens a third of that, or as many
+ * times 8192 tokens), SPIN_ERR_MISALIGNED.
  */
 spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, int B, const int32_t* kv_len,
                            const int32_t* page_table, int max_pages, int keep, int first, int recent, int32_t* kept,

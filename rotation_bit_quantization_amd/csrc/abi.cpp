@@ -130,6 +130,12 @@ bool aligned_all(std::initializer_list<const void*> ps) {   // NULL counts as al
     return true;
 }
 
+// Do n bytes at a and m bytes at b share memory?
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < n : x - y < m;
+}
+
 spin_status kv_append_impl(const void* Q, const void* K, const void* V, spin_dtype x_dtype, int T, int Hq, int Hkv,
                            int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_norm,
                            const float* k_norm, float eps, const float* rope, int rope_len, int rot_dim,
@@ -625,6 +631,8 @@ spin_status spin_kv_choose(const float* W, int Hkv, int n_pages, int page_size, 
     const size_t need = spin::kv_choose_workspace(Hkv, B, max_pages * page_size);
     if (need > 0 && !workspace) return SPIN_ERR_NULL;
     if (workspace_bytes < need) return SPIN_ERR_BAD_SHAPE;
+    const size_t lengths = sizeof(int32_t) * static_cast<size_t>(B);
+    if (lens != kv_len && overlap(lens, lengths, kv_len, lengths)) return SPIN_ERR_UNSUPPORTED;
     return from_hip(spin::launch_kv_choose({W, Hkv, n_pages, __builtin_ctz(static_cast<unsigned>(page_size)), B, kv_len, page_table,
                                             max_pages, keep, first, recent, kept, lens, static_cast<int*>(workspace)},
                                            static_cast<hipStream_t>(stream)));

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_kernel(KvChooseArgs 
     __shared__ int sums[R * kChooseWaves];
     __shared__ int found[2];
     const Head x = head_of(a, blockIdx.x);
-    if (x.h == 0 && threadIdx.x == 0) a.lens[x.b] = min(x.n, a.keep);
+    if (a.lens && x.h == 0 && threadIdx.x == 0) a.lens[x.b] = min(x.n, a.keep);
     if (x.n <= a.keep) {
         keep_all(x, 0, a.keep);
         return;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_part(KvChooseArgs a,
     __shared__ int found[2];
     const int head = blockIdx.x / parts, part = blockIdx.x - head * parts, p0 = part * kPart;
     const Head x = head_of(a, head);
-    if (STEP == 4 && x.h == 0 && part == 0 && threadIdx.x == 0) a.lens[x.b] = min(x.n, a.keep);
+    if (STEP == 4 && a.lens && x.h == 0 && part == 0 && threadIdx.x == 0) a.lens[x.b] = min(x.n, a.keep);
     if (x.n <= a.keep) {
         if (STEP == 4) keep_all(x, p0, part == parts - 1 ? a.keep : min(a.keep, p0 + kPart));
         return;
@@ -254,6 +254,12 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_part(KvChooseArgs a,
     write_kept<R>(a, x, u, p0, top, a.keep - above, overs, ties, sums);
 }
 
+// How many stay, where that takes the place of the lengths: behind the kernels, all of whose heads read them.
+__global__ __launch_bounds__(kChooseThreads) void kv_choose_lens(int32_t* lens, int B, int room, int keep) {
+    const int b = blockIdx.x * kChooseThreads + static_cast<int>(threadIdx.x);
+    if (b < B) lens[b] = min(min(max(lens[b], 0), room), keep);
+}
+
 bool in_parts(int room) { return room > 32 * kChooseThreads; }
 
 int parts_of(int room) { return (room + kPart - 1) / kPart; }
@@ -271,7 +277,9 @@ bool kv_choose_fits(int Hkv, int B, int room) {
     return heads <= most && (!in_parts(room) || (heads * 3 <= most && heads * parts_of(room) <= most));
 }
 
-hipError_t launch_kv_choose(const KvChooseArgs& a, hipStream_t s) {
+namespace {
+
+hipError_t launch_choice(const KvChooseArgs& a, hipStream_t s) {
     const unsigned heads = static_cast<unsigned>(a.B) * a.Hkv;
     const int room = a.max_pages << a.page_log2;
     const dim3 threads(kChooseThreads);
@@ -292,6 +300,19 @@ hipError_t launch_kv_choose(const KvChooseArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((kv_choose_part<2>), grid, threads, 0, s, a, parts);
     hipLaunchKernelGGL((kv_choose_part<3>), grid, threads, 0, s, a, parts);
     hipLaunchKernelGGL((kv_choose_part<4>), grid, threads, 0, s, a, parts);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_choose(const KvChooseArgs& a, hipStream_t s) {
+    if (a.lens != a.kv_len) return launch_choice(a, s);
+    KvChooseArgs places = a;
+    places.lens = nullptr;
+    const hipError_t e = launch_choice(places, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kv_choose_lens, dim3((static_cast<unsigned>(a.B) + kChooseThreads - 1) / kChooseThreads), dim3(kChooseThreads), 0, s, a.lens, a.B,
+                       a.max_pages << a.page_log2, a.keep);
     return hipGetLastError();
 }
 

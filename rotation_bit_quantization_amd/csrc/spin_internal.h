@@ -149,7 +149,7 @@ struct KvChooseArgs {
     const int32_t* page_table;
     int max_pages, keep, first, recent;
     int32_t* kept;
-    int32_t* lens;
+    int32_t* lens;                 // or kv_len itself
     int* counts;                   // the workspace
 };
 size_t kv_choose_workspace(int Hkv, int B, int room);

@@ -140,7 +140,8 @@ def spin_kv_choose_workspace(Hkv, B, max_pages, page_size):
 def spin_kv_choose(W, page_table, kv_len, keep, first=0, recent=0, kept=None, lens=None, stream=None, workspace=None):
     """W [n_pages, Hkv, page_size] fp32 -> (kept [B, Hkv, keep] int32: the places of the tokens that stay, ascending, -1
     behind them, lens [B] int32): per sequence and head its first ``first`` and last ``recent`` tokens and those of
-    greatest weight.  ``workspace`` (uint8, spin_kv_choose_workspace bytes) is allocated if it is not given."""
+    greatest weight.  ``lens`` may be ``kv_len``, which it replaces.  ``workspace`` (uint8, spin_kv_choose_workspace bytes) is
+    allocated if it is not given."""
     if stream is not None:
         return _on_stream(stream, W, spin_kv_choose, W, page_table, kv_len, keep, first, recent, kept, lens, workspace=workspace)
     dev = _gpu(W, "W")

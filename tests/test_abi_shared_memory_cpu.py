@@ -21,6 +21,15 @@ def test_a_move_within_rows_of_another_length(lib):  # noqa: F811
     assert call(n=0) == call(B=0) == spin.SPIN_OK
 
 
+def test_lengths_that_overlap_in_part(lib):  # noqa: F811
+    """Of 100 sequences; lens may be kv_len itself or lie beside it."""
+    call = caller(lib.spin_kv_choose, dict(W=A, Hkv=8, n_pages=10, page=16, B=100, kv_len=1 << 20, table=A, max_pages=5, keep=40, first=4,
+                                           recent=30, kept=A, lens=(1 << 20) + 16, ws=A, ws_bytes=1 << 30, st=None))
+    for lens in ((1 << 20) + 16, (1 << 20) + 384, (1 << 20) - 16, (1 << 20) - 384):
+        assert call(lens=lens) == spin.SPIN_ERR_UNSUPPORTED
+        assert call(lens=lens, B=0) == spin.SPIN_OK
+
+
 def test_under_host_sanitizers():
     if os.environ.get("SPIN_LIBRARY"):
         pytest.skip("already the sanitized library")
