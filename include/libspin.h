@@ -622,7 +622,8 @@ spin_status spin_kv_attn_shared(const uint16_t* Q, int T, int Hq, int Hkv, int D
  * sees them.  Rows of no sequence are not written.
  * Requirements: 0 <= T <= 2^26, B >= 0, 0 <= pos0 <= SPIN_KV_MAX_CONTEXT,
  * 1 <= words <= SPIN_KV_TREE_MAX_WORDS.
- * Errors: SPIN_ERR_NULL, SPIN_ERR_BAD_SHAPE, SPIN_ERR_MISALIGNED.
+ * Errors: SPIN_ERR_NULL, SPIN_ERR_UNSUPPORTED (tree or positions that overlap parent),
+ * SPIN_ERR_BAD_SHAPE, SPIN_ERR_MISALIGNED.
  */
 spin_status spin_kv_tree(const int32_t* parent, int T, int B, const int32_t* q_start, const int32_t* kv_len, int pos0,
                          int words, uint32_t* tree, int32_t* positions, void* stream);

@@ -545,6 +545,8 @@ spin_status spin_kv_tree(const int32_t* parent, int T, int B, const int32_t* q_s
         return SPIN_ERR_BAD_SHAPE;
     if (!aligned_all({parent, q_start, kv_len, tree, positions})) return SPIN_ERR_MISALIGNED;
     if (T == 0 || B == 0) return SPIN_OK;
+    const size_t rows = sizeof(int32_t) * static_cast<size_t>(T);      // each reads other rows' parents
+    if (overlap(parent, rows, positions, rows) || overlap(parent, rows, tree, rows * words)) return SPIN_ERR_UNSUPPORTED;
     return from_hip(spin::launch_kv_tree({parent, T, B, q_start, kv_len, pos0, words, tree, positions},
                                          static_cast<hipStream_t>(stream)));
 }

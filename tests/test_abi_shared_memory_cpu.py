@@ -30,6 +30,15 @@ def test_lengths_that_overlap_in_part(lib):  # noqa: F811
         assert call(lens=lens, B=0) == spin.SPIN_OK
 
 
+def test_a_tree_in_its_parents_memory(lib):  # noqa: F811
+    """Rows walk through other rows' parents."""
+    at = 1 << 20
+    call = caller(lib.spin_kv_tree, dict(parent=at, T=100, B=4, q_start=A, kv_len=A, pos0=0, words=2, tree=1 << 22, pos=1 << 23, st=None))
+    for bad in (dict(pos=at), dict(pos=at + 384), dict(pos=at - 384), dict(tree=at), dict(tree=at + 384), dict(tree=at - 784)):
+        assert call(**bad) == spin.SPIN_ERR_UNSUPPORTED, bad
+        assert call(**bad, T=0) == call(**bad, B=0) == spin.SPIN_OK
+
+
 def test_under_host_sanitizers():
     if os.environ.get("SPIN_LIBRARY"):
         pytest.skip("already the sanitized library")
