@@ -683,8 +683,9 @@ spin_status spin_kv_attn_ex(const uint16_t* Q, int T, int Hq, int Hkv, int D, in
  * A row whose lse is not finite adds nothing, and a token whose scale is not finite
  * draws nothing.  Sums are float32, in an order that goes by the sizes alone.  A page
  * may stand in one table of the batch only.  T == 0 is valid: W = decay * prior.
- * Errors: as for spin_kv_attn; SPIN_ERR_UNSUPPORTED for a decay that is not finite,
- * SPIN_ERR_BAD_SHAPE for more than 2^24 - 1 workgroups of 128 of a head's tokens.
+ * Errors: as for spin_kv_attn; SPIN_ERR_UNSUPPORTED for a decay that is not finite
+ * and a prior that overlaps W in part, SPIN_ERR_BAD_SHAPE for more than 2^24 - 1
+ * workgroups of 128 of a head's tokens.
  */
 spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
                             const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,

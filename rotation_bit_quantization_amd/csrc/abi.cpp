@@ -572,6 +572,8 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
     const size_t need = spin::kv_weights_workspace(T, Hq, Hkv, B, max_pages * page_size);
     if (need > 0 && !workspace) return SPIN_ERR_NULL;
     if (workspace_bytes < need) return SPIN_ERR_BAD_SHAPE;
+    const size_t slots = sizeof(float) * static_cast<size_t>(n_pages) * Hkv * page_size;
+    if (prior && prior != W && overlap(prior, slots, W, slots)) return SPIN_ERR_UNSUPPORTED;
     spin::KvWeightsArgs a = {};
     a.Q = Q;
     a.lse = lse;

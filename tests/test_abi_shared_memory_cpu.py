@@ -39,6 +39,17 @@ def test_a_tree_in_its_parents_memory(lib):  # noqa: F811
         assert call(**bad, T=0) == call(**bad, B=0) == spin.SPIN_OK
 
 
+def test_weights_that_overlap_their_prior_in_part(lib):  # noqa: F811
+    """Of 10 x 8 x 16 slots; prior may be W itself."""
+    at = 1 << 20
+    call = caller(lib.spin_kv_weights, dict(Q=A, lse=A, T=5, Hq=32, Hkv=8, D=128, bits=4, kc=A, ks=A, n_pages=10, page=16, B=1, q_start=A,
+                                            kv_len=A, table=A, max_pages=5, pos0=0, scale=0.1, cap=0.0, slopes=A, window=0, causal=1,
+                                            bidir=A, prior=at, decay=1.0, W=at, ws=A, ws_bytes=1 << 30, st=None))
+    for W in (at + 16, at - 16, at + 5104, at - 5104):
+        assert call(W=W) == spin.SPIN_ERR_UNSUPPORTED
+        assert call(W=W, B=0) == spin.SPIN_OK
+
+
 def test_under_host_sanitizers():
     if os.environ.get("SPIN_LIBRARY"):
         pytest.skip("already the sanitized library")
