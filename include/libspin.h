@@ -667,7 +667,8 @@ spin_status spin_kv_attn_ex(const uint16_t* Q, int T, int Hq, int Hkv, int D, in
  *            window, causal and bidir_len)
  *   pos0     position of the first token of the tables: 0, or the length of a prefix
  *            in other pages
- *   prior    [n_pages][Hkv][page_size] float32 or NULL; W itself is allowed
+ *   prior    [n_pages][Hkv][page_size] float32 or NULL; W itself is allowed.  It has to
+ *            hold a weight for every token, new ones among them (spin_kv_weights_ex)
  *   W        [n_pages][Hkv][page_size] float32   OUTPUT: at the slot of every token
  *            j < kv_len[b] of every sequence, per key head
  *              W_j = decay * prior_j + sum over rows and heads of e^(z_j - lse)
@@ -695,8 +696,27 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
                             size_t workspace_bytes, void* stream);
 
 /*
- * spin_kv_weights_workspace — bytes of workspace a spin_kv_weights call of these
- * sizes takes (0: none).  It goes by the sizes alone.
+ * spin_kv_weights_ex — spin_kv_weights where prior_len [B] int32 says how many of
+ * each sequence's tokens, the first ones, have a prior; that of the others is 0, and
+ * what prior holds at their slots is not read.  NULL: all have one.
+ *
+ * A slot outlives its token: what W held of a token that has left (spin_kv_choose,
+ * spin_kv_move) or of another sequence's, whose pages came back, is there still when
+ * new tokens are appended to that slot.  In a loop that adds up weights prior_len is
+ * the length that the last call of the sequence saw, or that spin_kv_choose left of
+ * it since, and 0 for a sequence that has had none.
+ * Errors: as for spin_kv_weights.
+ */
+spin_status spin_kv_weights_ex(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
+                               const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
+                               const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                               int max_pages, int pos0, float scale, float softcap, const float* slopes, int window,
+                               int causal, const int32_t* bidir_len, const float* prior, const int32_t* prior_len,
+                               float decay, float* W, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spin_kv_weights_workspace — bytes of workspace a spin_kv_weights or
+ * spin_kv_weights_ex call of these sizes takes (0: none).  It goes by the sizes alone.
  */
 spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, size_t* bytes);
 
@@ -748,7 +768,9 @@ spin_status spin_kv_choose_workspace(int Hkv, int B, int max_pages, int page_siz
  * A page that tokens go to may stand in one table of the call only; another sequence
  * that reads it (a shared prefix in the tables) sees what is moved there.
  * A token that comes from or goes to a place beyond its table, or a page that is
- * none of the pool, is passed over.  Slots that nothing goes to keep what they hold.
+ * none of the pool, is passed over.  Slots that nothing goes to keep what they hold,
+ * their weights too, which are not those of tokens that come there later
+ * (spin_kv_weights_ex).
  * Position rotations are in the keys, so that a token keeps its position wherever it
  * lies; what attention takes from places (windows, distances, causal order among new
  * tokens) goes by the new ones.

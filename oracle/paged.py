@@ -223,9 +223,9 @@ def kv_tree(parent, q_start, kv_len, words, pos0=0):
 
 
 def kv_weights(q, lse, cache, table, q_start, kv_len, scale, softcap=0.0, slopes=None, window=0, causal=True, bidir_len=None,
-               pos0=0, prior=None, decay=1.0):
+               pos0=0, prior=None, decay=1.0, prior_len=None):
     """(W [n_pages, Hkv, page] float64, NaN where nothing is written, bound): decay * prior + the attention weight that
-    each token draws.
+    each token draws; of a sequence's tokens from prior_len[b] on the prior is 0.
 
     A weight is off by the score's error (128 products of the query with codes and their sum, its scale, bias and
     cap: 132 roundings of 2^-24 of the terms; the cap as in ``kv_attend``), that of
@@ -270,8 +270,11 @@ def kv_weights(q, lse, cache, table, q_start, kv_len, scale, softcap=0.0, slopes
             e += 2.0 ** -24 * ((hi - lo) * G + 8) * w
             at, slot = np.where(there, table[b][j // page], 0)[there], (j % page)[there]
             if prior is not None:
-                w[there] += decay * prior[at, h, slot].astype(np.float64)
-                e[there] += 2.0 ** -23 * (np.abs(decay * prior[at, h, slot]) + np.abs(w[there]))
+                old = decay * prior[at, h, slot].astype(np.float64)
+                if prior_len is not None:
+                    old = np.where(j[there] < prior_len[b], old, 0.0)
+                w[there] += old
+                e[there] += 2.0 ** -23 * (np.abs(old) + np.abs(w[there]))
             W[at, h, slot], bound[at, h, slot] = w[there], e[there] + 2.0 ** -110
     return W, bound
 

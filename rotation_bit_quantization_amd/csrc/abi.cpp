@@ -551,12 +551,12 @@ spin_status spin_kv_tree(const int32_t* parent, int T, int B, const int32_t* q_s
                                          static_cast<hipStream_t>(stream)));
 }
 
-spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
-                            const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
-                            const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
-                            int pos0, float scale, float softcap, const float* slopes, int window, int causal,
-                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+spin_status spin_kv_weights_ex(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
+                               const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
+                               const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                               int max_pages, int pos0, float scale, float softcap, const float* slopes, int window,
+                               int causal, const int32_t* bidir_len, const float* prior, const int32_t* prior_len,
+                               float decay, float* W, void* workspace, size_t workspace_bytes, void* stream) {
     if (!Q || !lse || !K_codes || !K_scale || !q_start || !kv_len || !page_table || !W) return SPIN_ERR_NULL;
     if (causal != 0 && causal != 1) return SPIN_ERR_UNSUPPORTED;
     const float inf = __builtin_inff();
@@ -566,7 +566,7 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
     if (ok != SPIN_OK) return ok;
     if (T < 0 || Hq < 1 || Hq % Hkv != 0 || window < 0 || pos0 < 0 || pos0 > SPIN_KV_MAX_CONTEXT) return SPIN_ERR_BAD_SHAPE;
     if (!spin::kv_weights_fits(T, Hq, Hkv, B, max_pages * page_size)) return SPIN_ERR_BAD_SHAPE;
-    if (!aligned_all({Q, lse, K_codes, K_scale, q_start, kv_len, page_table, slopes, bidir_len, prior, W, workspace}))
+    if (!aligned_all({Q, lse, K_codes, K_scale, q_start, kv_len, page_table, slopes, bidir_len, prior, prior_len, W, workspace}))
         return SPIN_ERR_MISALIGNED;
     if (B == 0) return SPIN_OK;
     const size_t need = spin::kv_weights_workspace(T, Hq, Hkv, B, max_pages * page_size);
@@ -597,10 +597,22 @@ spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, 
     a.causal = causal == 1;
     a.bidir_len = bidir_len;
     a.prior = prior;
+    a.prior_len = prior_len;
     a.decay = decay;
     a.W = W;
     a.partial = static_cast<float*>(workspace);
     return from_hip(spin::launch_kv_weights(a, bits, static_cast<hipStream_t>(stream)));
+}
+
+spin_status spin_kv_weights(const uint16_t* Q, const float* lse, int T, int Hq, int Hkv, int D, int bits,
+                            const uint8_t* K_codes, const uint16_t* K_scale, int n_pages, int page_size, int B,
+                            const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                            int pos0, float scale, float softcap, const float* slopes, int window, int causal,
+                            const int32_t* bidir_len, const float* prior, float decay, float* W, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    return spin_kv_weights_ex(Q, lse, T, Hq, Hkv, D, bits, K_codes, K_scale, n_pages, page_size, B, q_start, kv_len,
+                              page_table, max_pages, pos0, scale, softcap, slopes, window, causal, bidir_len, prior,
+                              nullptr, decay, W, workspace, workspace_bytes, stream);
 }
 
 spin_status spin_kv_weights_workspace(int T, int Hq, int Hkv, int B, int max_pages, int page_size, size_t* bytes) {

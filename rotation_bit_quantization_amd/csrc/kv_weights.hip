@@ -43,6 +43,11 @@ constexpr int kCounted = 256;              // sequences up to which their chunks
 // one, 47 with four, 53 with twelve), and what enough is.
 constexpr int kMostTurns = 4, kGroupsEnough = 8192;
 
+// Tokens of sequence b, the first ones, that have a prior.
+__device__ __forceinline__ int priors(const KvWeightsArgs& a, int b) {
+    return !a.prior ? 0 : a.prior_len ? a.prior_len[b] : 0x7FFFFFFF;
+}
+
 // What a row adds to tokens, as the kernels hold it: its position, the logarithm in units of log2 (infinite where it adds
 // nothing: every exponential is 0) and its bias.
 struct Row {
@@ -190,6 +195,7 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4
     const Cap cap = cap_of<SCORES>(a);
     const float key_factor = held(cap.factor);
 
+    const int weighed = priors(a, b);
     const int unit = first + (lane >> 2) * kWeightWaves * kGroup + (lane & 3) * 16;
     const unsigned long long places = (lane >> 2) < turns ? place_of(a, b, h, unit, tokens) : ~0ull;
     auto place = [&](int t, int i) __attribute__((always_inline)) {
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4
         if (first + t * kWeightWaves * kGroup + lane >= tokens) raw.token = ~0ull;
         const bool there = raw.token != ~0ull;
         raw.scale = there ? a.K_scale[raw.token] : 0u;
-        raw.prior = there && a.prior ? a.prior[raw.token] : 0.0f;
+        raw.prior = there && first + t * kWeightWaves * kGroup + lane < weighed ? a.prior[raw.token] : 0.0f;
         return raw;
     };
 
@@ -491,7 +497,7 @@ __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsAr
         if (splits > 1) {
             if (j < tokens) a.partial[((static_cast<long long>(split) * a.B + b) * a.Hkv + h) * (static_cast<long long>(a.max_pages) << a.page_log2) + j] = w;
         } else if (token[m] != ~0ull) {
-            a.W[token[m]] = a.prior ? __builtin_fmaf(a.decay, a.prior[token[m]], w) : w;
+            a.W[token[m]] = j < priors(a, b) ? __builtin_fmaf(a.decay, a.prior[token[m]], w) : w;
         }
     }
 }
@@ -508,7 +514,7 @@ __global__ __launch_bounds__(kWeightThreads) void kv_weights_join(KvWeightsArgs 
     float w = 0.0f;
     for (int s = 0; s < splits; ++s) w += part[s * (static_cast<long long>(a.B) * a.Hkv * room)];
     const unsigned long long token = p + (j & 15);
-    a.W[token] = a.prior ? __builtin_fmaf(a.decay, a.prior[token], w) : w;
+    a.W[token] = j < priors(a, b) ? __builtin_fmaf(a.decay, a.prior[token], w) : w;
 }
 
 // How a call of these sizes is dealt out.

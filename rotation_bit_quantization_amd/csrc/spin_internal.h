@@ -133,6 +133,7 @@ struct KvWeightsArgs {
     bool causal;
     const int32_t* bidir_len;
     const float* prior;            // NULL: none
+    const int32_t* prior_len;      // [B]: tokens that have one, NULL: all
     float decay;
     float* W;
     float* partial;                // the workspace

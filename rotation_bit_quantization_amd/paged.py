@@ -92,15 +92,17 @@ def _workspace(given, need, of, dev):
 
 
 def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, softcap=0.0, slopes=None, window=0, causal=True,
-                    bidir_len=None, pos0=0, prior=None, decay=1.0, W=None, stream=None, workspace=None):
+                    bidir_len=None, pos0=0, prior=None, decay=1.0, W=None, stream=None, workspace=None, prior_len=None):
     """Q [T, Hq, 128] fp16 and lse [T, Hq] fp32 (from spin_kv_attn, with the same scores and masks) -> W [n_pages, Hkv,
     page_size] fp32: at each cached token's slot decay * prior + the attention weight it draws from the rows.
 
-    W is made, of zeros, if it is not given; it may be ``prior``.  ``workspace`` (uint8, spin_kv_weights_workspace bytes)
+    W is made, of zeros, if it is not given; it may be ``prior``.  ``prior_len`` [B] int32 (spin_kv_weights_ex): how many of
+    each sequence's tokens have a prior; those behind them, whose slots may hold sums of tokens that are gone, start at 0.
+    ``workspace`` (uint8, spin_kv_weights_workspace bytes)
     is allocated if it is not given."""
     if stream is not None:
         return _on_stream(stream, Q, spin_kv_weights, Q, lse, cache, page_table, q_start, kv_len, scale, softcap, slopes,
-                          window, causal, bidir_len, pos0, prior, decay, W, workspace=workspace)
+                          window, causal, bidir_len, pos0, prior, decay, W, workspace=workspace, prior_len=prior_len)
     dev = _gpu(Q, "Q")
     (kc, ks, _, _), n_pages, Hkv, page, bits = _cache(cache, dev)
     (starts, lens, table), B, max_pages = _batch(page_table, q_start, kv_len, dev)
@@ -113,6 +115,11 @@ def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, soft
     slope = None if slopes is None else _want(slopes, "slopes", torch.float32, (Hq,), dev)
     both = None if bidir_len is None else _want(bidir_len, "bidir_len", torch.int32, (B,), dev)
     old = None if prior is None else _weights(prior, "prior", cache, dev)
+    fn, known = "spin_kv_weights", ()
+    if prior_len is not None:
+        if prior is None:
+            raise ValueError("prior_len without prior")
+        fn, known = "spin_kv_weights_ex", (_want(prior_len, "prior_len", torch.int32, (B,), dev),)
     if W is None:
         W = torch.zeros(cache["K_scale"].shape, dtype=torch.float32, device=Q.device)
     out = _weights(W, "W", cache, dev)
@@ -120,10 +127,10 @@ def spin_kv_weights(Q, lse, cache, page_table, q_start, kv_len, scale=None, soft
         if T == 0:
             q = log = starts
         ws, ws_bytes = _workspace(workspace, spin_kv_weights_workspace(T, Hq, Hkv, B, max_pages, page), Q, dev)
-        _launch("spin_kv_weights", dev,
+        _launch(fn, dev,
                 (q, log, T, Hq, Hkv, 128, bits, kc, ks, n_pages, page, B, starts, lens, table, max_pages, _int(pos0, "pos0"),
                  0.08838834764831845 if scale is None else scale, softcap, slope, _int(window, "window"), _int(causal, "causal"), both,
-                 old, decay, out, _ptr(ws), ws_bytes))
+                 old, *known, decay, out, _ptr(ws), ws_bytes))
     return W
 
 

@@ -38,8 +38,8 @@ EXPORTED_SYMBOLS = ("spin_fold_rotation", "spin_fwht_quant", "spin_w4a4_gemm", "
                     "spin_fwht_quant_gemm", "spin_fwht_quant_gemm_noalloc", "spin_fwht_quant_f6",
                     "spin_w4a4_gemm_f6", "spin_codes_f6", "spin_w4a4_gemm_f6f6", "spin_rope_table", "spin_kv_append",
                     "spin_kv_append_at", "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_ex", "spin_kv_attn_workspace",
-                    "spin_kv_tree", "spin_kv_weights", "spin_kv_weights_workspace", "spin_kv_choose", "spin_kv_choose_workspace",
-                    "spin_kv_move",
+                    "spin_kv_tree", "spin_kv_weights", "spin_kv_weights_ex", "spin_kv_weights_workspace", "spin_kv_choose",
+                    "spin_kv_choose_workspace", "spin_kv_move",
                     "spin_status_string", "spin_version")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -98,14 +98,15 @@ def load():
     lib.spin_kv_attn_ex.argtypes = cache + [vp, i, i, vp, vp, vp, i] + mask[:6] + [vp, i, vp, vp, vp] + mask[7:]
     lib.spin_kv_tree.argtypes = [vp, i, i, vp, vp, i, i, vp, vp, vp]
     lib.spin_kv_weights.argtypes = [vp, vp, i, i, i, i, i, vp, vp, i, i, i, vp, vp, vp, i, i] + mask[:6] + [vp, f, vp, vp, z, vp]
+    lib.spin_kv_weights_ex.argtypes = lib.spin_kv_weights.argtypes[:24] + [vp] + lib.spin_kv_weights.argtypes[24:]
     lib.spin_kv_weights_workspace.argtypes = [i, i, i, i, i, i, ctypes.POINTER(z)]
     lib.spin_kv_choose.argtypes = [vp, i, i, i, i, vp, vp, i, i, i, i, vp, vp, vp, z, vp]
     lib.spin_kv_choose_workspace.argtypes = [i, i, i, i, ctypes.POINTER(z)]
     lib.spin_kv_move.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, i, vp, i, i, vp, vp, i, vp]
     lib.spin_kv_attn_workspace.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(z)]
     for name in ("spin_rope_table", "spin_kv_append", "spin_kv_append_at", "spin_kv_attn", "spin_kv_attn_shared", "spin_kv_attn_ex",
-                 "spin_kv_attn_workspace", "spin_kv_tree", "spin_kv_weights", "spin_kv_weights_workspace", "spin_kv_choose",
-                 "spin_kv_choose_workspace", "spin_kv_move"):
+                 "spin_kv_attn_workspace", "spin_kv_tree", "spin_kv_weights", "spin_kv_weights_ex", "spin_kv_weights_workspace",
+                 "spin_kv_choose", "spin_kv_choose_workspace", "spin_kv_move"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("spin_fold_rotation", "spin_fwht_quant", "spin_w4a4_gemm", "spin_kv_quant",
                  "spin_fwht_quant8", "spin_w4a8_gemm", "spin_kv_quant8", "spin_kv_qkv", "spin_w4a4_gemm_ex", "spin_fwht_quant_gemm",
