@@ -156,8 +156,15 @@ __device__ __forceinline__ float scale_of(uint32_t raw) { return __half2float(__
 // that wait for each other (length, page, keys).  Measured: 64 single tokens of 32 + 8 heads on 2000 to 8192, INT4, 44 us
 // from the last-level cache and 51 from memory (189 MB, 3.7 TB/s), capped 53, INT8 83; 16 on 2000 to 8192 16 us, one on 30000
 // 6, one on 1000 4.5.  With 16 rows at a time whatever there is, capped 65.  Five waves a SIMD spill (62 us).
+//
+// A sequence of more rows than the batch's mean (the host knows no other number) takes them all past each of its groups,
+// 4 N at a time: a prompt of 4000 among 255 single tokens, 8 + 8 heads, 1618 us (the single tokens alone 25), one of 200
+// among 63, 32 + 8 heads, 244 (39).  Its sums are then carried with what their additions have lost, as a tile's are, in
+// LDS, since registers are spent (added plainly 1532 and 230 us, and off by 6e-6 of themselves).
 template <int BITS, int SCORES, int N>
 __global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4 : 3) void kv_weights_rows16(KvWeightsArgs a, int chunks, int turns) {
+    // a lane's sums over more than 4 N rows, and what their additions have lost; no other lane's
+    __shared__ f4 sums[kWeightThreads], lost[kWeightThreads];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int G = a.Hq / a.Hkv;
@@ -257,14 +264,15 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4
     const int groups = min(turns, (tokens - first + kWeightWaves * kGroup - 1) / (kWeightWaves * kGroup));
     Raw raw = fetch(0);
     const int rows = news * G;
-    if (rows <= 4 * N) load_rows(0, rows);
+    const bool many = rows > 4 * N;
+    if (!many) load_rows(0, rows);
     for (int t = 0; t < groups; ++t) {
         const int j0 = first + t * kWeightWaves * kGroup, last = min(j0 + kGroup, tokens) - 1;
         // a row that sees a scale that is not finite has no weights
         const float ks = scale_of(raw.scale);
         const bool fine = __builtin_fabsf(ks) <= 65504.0f;
         const float kf_own = fine ? ks * key_factor : 0.0f;
-        float kf[4], acc[4] = {};
+        float kf[4], acc[4] = {};          // of 4 N rows
 #pragma unroll
         for (int i = 0; i < 4; ++i) kf[i] = __shfl(kf_own, 16 * i + n, 64);
         const unsigned long long token = raw.token;
@@ -273,8 +281,9 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4
         if (t + 1 < groups) next = fetch(t + 1);
         const Range on = rows_on(a, a.pos0 + j0, a.pos0 + last, start, news, both);
         const int row_end = on.hi * G;
-        for (int r0 = rows <= 4 * N ? 0 : on.lo * G; r0 < row_end; r0 += 4 * N) {
-            if (rows > 4 * N) load_rows(r0, row_end);
+        if (many) sums[threadIdx.x] = f4{}, lost[threadIdx.x] = f4{};
+        for (int r0 = many ? on.lo * G : 0; r0 < row_end; r0 += 4 * N) {
+            if (many) load_rows(r0, row_end);
             const bool whole = all_seen(a, start + r0 / G, start + (min(r0 + 4 * N, rows) - 1) / G, a.pos0 + j0, a.pos0 + last, both);
             // unpacked anew for these rows: kept, the operands of 64 tokens take 64 registers
 #pragma unroll
@@ -297,9 +306,20 @@ __global__ __launch_bounds__(kWeightThreads, BITS == 4 && SCORES != kWideCap ? 4
 #pragma unroll
                     for (int e = 0; e < N; ++e) s[e] = sees(a, where[e], p, both) ? s[e] : -__builtin_inff();
                 }
+                acc[i] = __builtin_amdgcn_exp2f(s[0]);
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[i] += __builtin_amdgcn_exp2f(s[e]);
+                for (int e = 1; e < N; ++e) acc[i] += __builtin_amdgcn_exp2f(s[e]);
             }
+            if (many) {
+                const f4 old = sums[threadIdx.x], y = f4{acc[0], acc[1], acc[2], acc[3]} - lost[threadIdx.x], sum = old + y;
+                lost[threadIdx.x] = (sum - old) - y;
+                sums[threadIdx.x] = sum;
+            }
+        }
+        if (many) {
+            const f4 sum = sums[threadIdx.x];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = sum[i];
         }
         // lane l has token l
         float w = 0.0f;
