@@ -228,7 +228,7 @@ def kv_weights(q, lse, cache, table, q_start, kv_len, scale, softcap=0.0, slopes
     each token draws; of a sequence's tokens from prior_len[b] on the prior is 0.
 
     A weight is off by the score's error (128 products of the query with codes and their sum, its scale, bias and
-    cap: 132 roundings of 2^-24 of the terms; the cap as in ``kv_attend``), that of
+    cap: 132 roundings of 2^-24 of the terms; the cap as in ``kv_attend``, below 0.7 of it 2^-22 of the score), that of
     the difference to lse in units of log2 (2^-22 of both) and the exponential's 2^-22 (numbers below 2^-126 may be 0); the sum by a rounding of itself for
     every row, and two for the prior."""
     T, Hq, _ = q.shape
@@ -258,11 +258,12 @@ def kv_weights(q, lse, cache, table, q_start, kv_len, scale, softcap=0.0, slopes
                 z = scale * (x @ kd.T) * ks
                 ez = 132 * 2.0 ** -24 * abs(scale) * (np.abs(x) @ np.abs(kd).T) * ks
                 if softcap:
+                    near = np.abs(z) < 0.7 * softcap
                     z = softcap * np.tanh(z / softcap)
-                    ez += softcap * 2.0 ** -22 if softcap <= 64 else np.abs(z) * 2.0 ** -18
+                    ez += np.where(near, np.abs(z) * 2.0 ** -22, softcap * 2.0 ** -22 if softcap <= 64 else np.abs(z) * 2.0 ** -18)
                 if slopes is not None:
                     z = z - float(slopes[g]) * np.abs(far)
-                    ez += float(slopes[g]) * np.abs(far) * 2.0 ** -22
+                    ez += np.abs(float(slopes[g]) * far) * 2.0 ** -22
                 ez += 2.0 ** -22 * (np.abs(z) + np.abs(log) + 1)
                 weight = np.where(seen & counts[:, None] & fine[None], np.exp(np.minimum(z - log, 700.0)), 0.0)
                 w += weight.sum(0)
