@@ -15,11 +15,19 @@
 // maxima and sums are float32; exponentials, logarithms and reciprocals are the hardware's, off by a unit in the last
 // place, 2^-23, which the rounding of the weights passes by far.
 //
+// Weights are rounded because the matrix instructions take 16 bits, and to fp16 because it holds three bits more than bf16; the
+// rounding goes to either side, and the sum that divides is of the weights as they were, as the logarithm below needs it.
+// Outputs are off by 2.4 to 2.6e-4 (rms, relative), of which the output's own fp16 leaves 2.1e-4: three of ten values are a
+// step beside the nearest.
+//
 // With a tree a row sees the context and, of its sequence's new tokens, those that its bits name.  Only steps that hold new
 // tokens look at them (tree_mask).  Measured with 32 + 8 heads: a tree of 16 tokens on 1000, INT4, 12 us; 16 of 60 on 4096
-// 102 - 112 us (as many rows in order 102 - 107), INT8 and capped 134 (134); 64 of 8 on 2000 54 (55).
+// 102 - 112 us (as many rows in order 97 - 107), INT8 and capped 119 - 134 (127 - 134), with a distance bias 153 (120), INT8
+// with both 183 (144): there the masks spill 20 to 26 registers; 64 of 8 on 2000 54 (55); 16 of 60 on 500 behind a prefix
+// of 4096 131 (127), 64 of 8 78 (77).
 //
-// A row's log sum e^z is M and the sum of w_j / vs_j, which attention divides by, together.
+// A row's log sum e^z is M and the sum of w_j / vs_j, which attention divides by, together.  It keeps what the products are
+// off by (key_operand_small), averaged over the tokens: 9e-6 rms at 4 bits, 1e-6 at 8.
 //
 // Both products are computed transposed: S^T = A Q^T leaves a lane with one
 // query and four tokens of a tile of 16, which is what the second product O^T =

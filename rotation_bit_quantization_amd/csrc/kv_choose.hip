@@ -159,7 +159,9 @@ __device__ __forceinline__ void write_kept(const KvChooseArgs& a, const Head& x,
 
 // One workgroup for all tokens of a head, which it holds in registers.  Bound by what depends on what: length, page, weight,
 // then for each digit the counts, their sum over the workgroup, and the next.  Measured: 8 heads of 64 sequences of 2000 to
-// 8192 tokens, of which 2048 stay, 11 us (14 MB); of one sequence of 2500, 16000 and 32000 6.5, 11 and 17 us.
+// 8192 tokens, of which 2048 stay, 12.6 us on two batches in turn (14 MB), 11 on one again and again; there 18 us in a
+// table for 16384 and 26 for 32768, whose kernels hold as many ranks.  Of one sequence of 2500, 16000 and 32000 6.9, 11.9
+// and 18.7 us.
 template <int R>
 __global__ __launch_bounds__(kChooseThreads) void kv_choose_kernel(KvChooseArgs a) {
     __shared__ int count[kBins];
@@ -191,8 +193,9 @@ __global__ __launch_bounds__(kChooseThreads) void kv_choose_kernel(KvChooseArgs 
 // Longer tables: a workgroup for 8192 tokens of a head, and a launch for each step: the counts cleared, then each digit's
 // counts added up over the workgroups (whole numbers, in any order), then how many of each workgroup's stay, then their
 // places.  Each step finds the digits that are known from their counts again.  Measured: one document of 131072 tokens, 8
-// heads, 28 us (one workgroup a head, which read the weights four times over: 137); 16 of 130000 124 us (with 32768 tokens
-// a workgroup 147).
+// heads, 28 us (one workgroup a head, which read the weights four times over: 137); 16 of 130000 128 us (with 32768 tokens
+// a workgroup 147).  The table's room decides, the host knows no lengths: 64 sequences of 2000 to 8192 tokens in tables for
+// 33000 take 70 us, for 131072 398.
 constexpr int kPartRounds = 2, kPart = 4 * kPartRounds * kChooseThreads;
 
 __global__ __launch_bounds__(kChooseThreads) void kv_choose_clear(KvChooseArgs a) {

@@ -12,9 +12,10 @@
 //
 // Bound: into other pages memory, and in place the loads that wait for each other
 // (the list, the tables, the codes).  Measured: 2048 tokens of each of 16
-// sequences and 8 heads, INT4, with weights, into other pages 19 us (72 MB, 3.8
-// TB/s: sources are spread, four bytes of a value's octet at a time), in place 23 us;
-// the accepted paths of 64 trees 4 us.
+// sequences and 8 heads, INT4, with weights, into other pages 20 us (72 MB, 3.6
+// TB/s: sources are spread, four bytes of a value's octet at a time), in place 24 us
+// (of 64 sequences 77; 4096 of one of 131072 tokens, 16 turns of 16 workgroups, 33,
+// into other pages 5.6); the accepted paths of 64 trees 4.6 us.
 #include "kv_batch.h"
 #include "spin_internal.h"
 

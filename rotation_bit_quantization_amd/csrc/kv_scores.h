@@ -56,7 +56,9 @@ __device__ __forceinline__ h8 key_operand(const uint32_t* w) {
 
 // The same without the subtraction: u = code + 8 (128) as the fp16 number u 2^-24, subnormal, which the matrix cores
 // take as it is.  The sum over a query is then 2^-24 (sum q code + 8 sum q): the second term goes into the accumulator
-// that the sum starts from.
+// that the sum starts from.  The matrix cores align subnormal operands as if their leading bit were there: at queries of 2 a
+// sum of 128 products is off by 3e-4 (rms, 4-bit codes) in place of 1e-6, a score by about 1e-5, far below what weights
+// rounded to fp16 tell apart.
 template <int BITS>
 __device__ __forceinline__ h8 key_operand_small(const uint32_t* w) {
     Frag f;

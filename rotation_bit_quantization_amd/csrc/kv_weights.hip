@@ -156,9 +156,10 @@ __device__ __forceinline__ float scale_of(uint32_t raw) { return __half2float(__
 // are N rows of a token: rows stand in the matrix cores' operand so that its four places hold rows g, g + 4, ..
 //
 // Bound: reading the keys, 16 BITS + 2 bytes a token and head, from the second round of workgroups on; before that loads
-// that wait for each other (length, page, keys).  Measured: 64 single tokens of 32 + 8 heads on 2000 to 8192, INT4, 44 us
-// from the last-level cache and 51 from memory (189 MB, 3.7 TB/s), capped 53, INT8 83; 16 on 2000 to 8192 16 us, one on 30000
-// 6, one on 1000 4.5.  With 16 rows at a time whatever there is, capped 65.  Five waves a SIMD spill (62 us).
+// that wait for each other (length, page, keys).  Measured: 64 single tokens of 32 + 8 heads on 2000 to 8192, INT4, 43 us
+// from the last-level cache and 51 from memory (189 MB, 3.7 TB/s), capped 47 and 53, INT8 83; in a table for 32768 47, for
+// 131072 75; 16 on 2000 to 8192 17 us, one on 30000 6, one on 1000 4.5.  With 16 rows at a time whatever there is, capped
+// 65.  Five waves a SIMD spill (62 us).
 //
 // A sequence of more rows than the batch's mean (the host knows no other number) takes them all past each of its groups,
 // 4 N at a time: a prompt of 4000 among 255 single tokens, 8 + 8 heads, 1618 us (the single tokens alone 25), one of 200
@@ -347,8 +348,9 @@ constexpr int kTileRows = 32;
 // Bound: the vector work of the weights beside the matrix work, 24 cycles (a multiply-add, an exponential, an addition) of
 // 64 scores against 16, with a cap and a bias 66, and what staging 32 rows takes.  A token's sum is carried with what its
 // additions have lost, 32 rows at a time, so that it is as exact for a long prompt as for a row.  Measured with 32 + 8 heads
-// and INT4: a prompt of 8192 tokens 320 us (0.86 PFLOP/s), of 2000 37, 32 tokens each of two on 16384 21; three prompts of
-// 1670, 32 + 32 heads, INT8, capped and biased, 119.
+// and INT4: a prompt of 8192 tokens 320 - 334 us (0.82 - 0.86 PFLOP/s), of 2000 37 (in a table for 8192 40, for 131072, where
+// its rows are one share, 290), 32 tokens each of two on 16384 22; three uneven prompts of 5011 together, 32 + 32 heads, INT8,
+// capped and biased, 111 - 123.
 template <int BITS, int SCORES, int M>
 __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsArgs a, int splits) {
     struct Stage {
