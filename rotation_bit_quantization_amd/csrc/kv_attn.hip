@@ -22,7 +22,7 @@
 //
 // With a tree a row sees the context and, of its sequence's new tokens, those that its bits name.  Only steps that hold new
 // tokens look at them (tree_mask).  Measured with 32 + 8 heads: a tree of 16 tokens on 1000, INT4, 12 us; 16 of 60 on 4096
-// 102 - 112 us (as many rows in order 97 - 107), INT8 and capped 119 - 134 (127 - 134), with a distance bias 153 (120), INT8
+// 98 - 112 us (as many rows in order 97 - 107), INT8 and capped 119 - 134 (127 - 134), with a distance bias 153 (120), INT8
 // with both 183 (144): there the masks spill 20 to 26 registers; 64 of 8 on 2000 54 (55); 16 of 60 on 500 behind a prefix
 // of 4096 131 (127), 64 of 8 78 (77).
 //

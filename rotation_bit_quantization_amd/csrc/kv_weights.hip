@@ -350,7 +350,7 @@ constexpr int kTileRows = 32;
 // additions have lost, 32 rows at a time, so that it is as exact for a long prompt as for a row.  Measured with 32 + 8 heads
 // and INT4: a prompt of 8192 tokens 320 - 334 us (0.82 - 0.86 PFLOP/s), of 2000 37 (in a table for 8192 40, for 131072, where
 // its rows are one share, 290), 32 tokens each of two on 16384 22; three uneven prompts of 5011 together, 32 + 32 heads, INT8,
-// capped and biased, 111 - 123.
+// capped and biased, 106 - 123.
 template <int BITS, int SCORES, int M>
 __global__ __launch_bounds__(kWeightThreads, 2) void kv_weights_tile(KvWeightsArgs a, int splits) {
     struct Stage {
